@@ -26,6 +26,8 @@
  *   w           [d]               norm weight, shared by all value heads
  *   y_fp16      [T][n_vh][d]      IEEE binary16 bits
  * Value head h reads key head h % n_kh.
+ * The selective state space operators (gdn_ssm_*) and gdn_block_norm state their
+ * own layouts: activations of a gdn_dtype with a stride between rows.
  *
  * Ownership: every pointer is a DEVICE pointer owned by the caller, on the
  * current CUDA device.  The library allocates only (a) a 4-byte status word per
@@ -68,6 +70,10 @@ typedef enum gdn_mode {
 /* Token count from which GDN_AUTO takes the chunked form: the measured crossover
  * of the two modes' GPU time per call on GB300 (48 value heads, d = 128). */
 #define GDN_AUTO_CHUNKED_MIN_T 64
+
+/* Activation types of the gdn_ssm_* operators and gdn_block_norm (their parameters
+ * and states are FP32 in every case). */
+typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
 
 typedef enum gdn_status {
     GDN_OK = 0,
@@ -254,6 +260,112 @@ int gdn_recurrence_chunked_noalloc(const float* q, const float* k, const float* 
                                    float* state_inout, float* out,
                                    int64_t T, int n_kh, int n_vh, int d,
                                    void* cuda_stream);
+
+/*
+ * The selective state space layer: gdn_ssm_conv and gdn_ssm_scan for packed
+ * prompts, gdn_ssm_step for one token of each request.  The pages have no
+ * counterpart; the conventions are this library's: head h reads group h % n_groups
+ * of B and C, the state is S[state_dim][head_dim] per head (B's dim the row), the
+ * gates come from a, A_log and dt_bias as in gdn_prestage.
+ *
+ * Packed sequences: the rows of n_seq sequences follow one another; sequence s has
+ * rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of the T rows (cu_seqlens [n_seq + 1],
+ * on the device, not decreasing; NULL: one sequence of all T rows).  Rows before
+ * cu_seqlens[0] and from cu_seqlens[n_seq] on belong to no sequence: their outputs
+ * are left as they were.  Bounds outside [0, T] or out of order make their sequence
+ * empty.
+ *
+ * Slots: sequence s keeps its state (and its convolution history) in slot slots[s]
+ * of a pool of n_slots (slots NULL: slot s).  It starts from the slot's content
+ * where has_state[s] is not 0 (has_state NULL: always), else from zeros, and the
+ * slot receives the content after its last token.  A slot below 0 or not below
+ * n_slots is no slot: the sequence starts from zeros and nothing is kept (in
+ * gdn_ssm_step, the request is a padding row: nothing of it is read or written).
+ * A sequence without tokens leaves its slot as it is.  Within a call a slot belongs
+ * to one sequence; two sequences with the same slot race.
+ *
+ * Strides are in elements, between rows; a row's elements are contiguous.  Inputs
+ * may be columns of one wider row (x, B and C of the convolution's output, say) and
+ * may have stride 0; no output may overlap an input or another output, as address
+ * ranges.  Elements need their own alignment, states 16 bytes; rows that start on
+ * 16-byte boundaries are faster.  Calls keep nothing between them, use no memory of
+ * the library's and may run at the same time on different streams (on different
+ * slots and workspaces), and may be captured into a graph.
+ */
+
+/*
+ * gdn_ssm_conv - causal depthwise convolution over packed sequences:
+ *     y[t][c] = act(bias[c] + sum_{j<width} w[c][j] X[t - (width - 1) + j][c])
+ * with X a sequence's rows, preceded by its history (oldest first).
+ *   x, y [T][channels] of `dtype`; w [channels][width], bias [channels] or NULL: FP32.
+ *   hist [n_slots][width - 1][channels] of `dtype`, or NULL (every sequence starts
+ *   from zeros, nothing is kept).  activation: 1 (SiLU) or 0.
+ * Computed in FP32, rounded once.  width 2, 3 or 4.  A sequence split over calls
+ * with its history carried gives the same bits as one call.
+ */
+int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* bias, void* hist,
+                 const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* has_state, int n_seq, int n_slots,
+                 void* y, int64_t y_stride, int64_t T, int channels, int width, int activation, int dtype,
+                 void* cuda_stream);
+
+/*
+ * gdn_ssm_scan - the selective state space scan over packed sequences.  Per head h,
+ * group g = h % n_groups and token t of a sequence:
+ *     dt = log(1 + exp(a[t][h] + dt_bias[h]))
+ *     S <- exp(-exp(A_log[h]) dt) S + dt B[t][g] x[t][h]^T
+ *     y[t][h] = (S^T C[t][g] + D[h] x[t][h]) silu(z[t][h])
+ *   x, y [T][n_heads][head_dim], z the same or NULL (no gate), a [T][n_heads], B, C
+ *   [T][n_groups][state_dim]: of `dtype`.  A_log, dt_bias, D (or NULL: 0) [n_heads],
+ *   states [n_slots][n_heads][state_dim][head_dim] (or NULL: every sequence starts
+ *   from zeros, nothing is kept): FP32.
+ * The state and every sum are FP32; y is rounded once.  head_dim: a multiple of 32
+ * up to 256; state_dim: 16, 32, 64 or 128.
+ * workspace: gdn_ssm_scan_workspace_bytes() bytes, 16-byte aligned, the call's own
+ * until it has finished (NULL where that is 0).
+ */
+int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const void* B, int64_t b_stride,
+                 const void* C, int64_t c_stride, const void* z, int64_t z_stride, const float* A_log,
+                 const float* dt_bias, const float* D, float* states, const int32_t* cu_seqlens, const int32_t* slots,
+                 const uint8_t* has_state, int n_seq, int n_slots, void* y, int64_t y_stride, int64_t T, int n_heads,
+                 int n_groups, int head_dim, int state_dim, int dtype, void* workspace, size_t workspace_bytes,
+                 void* cuda_stream);
+
+/* Bytes of workspace a gdn_ssm_scan call of these sizes needs (0: none). */
+size_t gdn_ssm_scan_workspace_bytes(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int dtype);
+
+/*
+ * gdn_ssm_step - one token of gdn_ssm_conv and gdn_ssm_scan for each of `batch`
+ * requests, in one launch.  The packed row is [x: n_heads head_dim | B: n_groups
+ * state_dim | C: n_groups state_dim], cw channels in all.
+ *   xbc [batch][cw], a [batch][n_heads], z and y [batch][n_heads][head_dim] (z or
+ *   NULL), hist [n_slots][width - 1][cw]: of `dtype`.  conv_w [cw][width], conv_bias
+ *   [cw] or NULL, A_log, dt_bias, D (or NULL), states as in gdn_ssm_scan: FP32.
+ * Request i has slot slots[i] (NULL: i), which always holds its history and state.
+ * The convolved row is kept in FP32 (the two calls would round it to `dtype`).
+ * batch <= 65535.
+ */
+int gdn_ssm_step(const void* xbc, int64_t xbc_stride, const void* a, int64_t a_stride, const void* z, int64_t z_stride,
+                 const float* conv_w, const float* conv_bias, const float* A_log, const float* dt_bias, const float* D,
+                 void* hist, float* states, const int32_t* slots, int n_slots, void* y, int64_t y_stride, int batch,
+                 int n_heads, int n_groups, int head_dim, int state_dim, int width, int activation, int dtype,
+                 void* cuda_stream);
+
+/*
+ * gdn_block_norm - the norms around a block, with its gate and residual scale, in
+ * one pass.  Per token:
+ *     u = b / sqrt(mean(b^2) + eps) * w_post          (w_post NULL: u = b)
+ *     residual_out = residual + scale * act(gate) * u (gate NULL: 1; act: the sigmoid
+ *                                                      where gate_sigmoid is 1)
+ *     y = residual_out / sqrt(mean(residual_out^2) + eps) * w_pre
+ *   b, gate, y [T][dim] of `dtype` (gate_stride 0: one row for every token); residual,
+ *   residual_out [T][dim] of `residual_dtype`, GDN_F32 or `dtype`; w_post, w_pre [dim]
+ *   FP32.  residual_out may be residual itself.
+ * Computed in FP32; y comes from residual_out before its rounding.  dim <= 16384.
+ */
+int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_t residual_stride, const void* gate,
+                   int64_t gate_stride, int gate_sigmoid, const float* w_post, const float* w_pre, float scale,
+                   float eps, void* residual_out, int64_t residual_out_stride, void* y, int64_t y_stride, int64_t T,
+                   int dim, int dtype, int residual_dtype, void* cuda_stream);
 
 /*
  * Process-wide options.  The library reads no environment variable: the A/B

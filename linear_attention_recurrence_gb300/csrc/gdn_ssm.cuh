@@ -1,0 +1,98 @@
+// Shared by the selective state space kernels and the block norm: the activation
+// types, 16-byte (and narrower) vectors of them, the gate functions, and the reading
+// of packed sequences and state slots.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "gdn_device.cuh"
+
+namespace gdn {
+
+template <class T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+
+// Round to nearest even, once, from FP32.
+template <class T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// N elements of T that one access moves (N * sizeof(T) <= 32 bytes, a power of two;
+// 32 bytes are two 16-byte accesses).
+template <class T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Vec {
+    T v[N];
+};
+template <class T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[N]) {
+    const Vec<T, N> x = *reinterpret_cast<const Vec<T, N>*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f<T>(x.v[i]);
+}
+template <class T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[N]) {
+    Vec<T, N> x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) x.v[i] = from_f<T>(f[i]);
+    *reinterpret_cast<Vec<T, N>*>(p) = x;
+}
+
+// silu(z) = z / (1 + e^-z), with the fast exponential and division (relative error a
+// few FP32 ulp; an infinite divisor gives 0).
+__device__ __forceinline__ float ssm_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// softplus(v) = log(1 + e^v), accurate for small e^v too (log1p); v itself once e^-v
+// is below half an FP32 ulp of v.
+__device__ __forceinline__ float ssm_softplus(float v) { return v > 20.0f ? v : log1pf(expf(v)); }
+
+// -exp(A_log), finite (so that no step, dt = 0, stays no decay).
+__device__ __forceinline__ float ssm_rate(float A_log) { return fmaxf(-expf(A_log), -3.402823466e38f); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+// A token's decay is e^g = 2^(g log2 e).  The exponent is held at -256 or above: such a
+// factor is 0 in FP32 either way, and running sums of the exponents stay finite.
+constexpr float kMinLog2Decay = -256.0f;
+
+// The packed sequences of a call: sequence s has rows [begin, end) of the packed rows.
+// Bounds outside [0, T] or out of order give an empty sequence, so no row outside the
+// arrays is touched whatever cu_seqlens holds.
+struct SsmSeqs {
+    const int32_t* cu;         // [n_seq + 1], or nullptr: one sequence of T rows
+    const int32_t* slots;      // [n_seq], or nullptr: sequence s has slot s
+    const uint8_t* has_state;  // [n_seq], or nullptr: every sequence continues from its slot
+    int n_seq;
+    int n_slots;
+    int64_t T;
+};
+__device__ __forceinline__ void seq_rows(const SsmSeqs& q, int s, int64_t& begin, int64_t& end) {
+    begin = 0;
+    end = q.T;
+    if (q.cu) {
+        begin = __ldg(q.cu + s);
+        end = __ldg(q.cu + s + 1);
+        if (begin < 0 || end > q.T || end < begin) end = begin = 0;
+    }
+}
+// The slot of sequence s, or -1 if it has none (negative or out of range).
+__device__ __forceinline__ int seq_slot(const SsmSeqs& q, int s) {
+    const int slot = q.slots ? __ldg(q.slots + s) : s;
+    return slot >= 0 && slot < q.n_slots ? slot : -1;
+}
+__device__ __forceinline__ bool seq_has_state(const SsmSeqs& q, int s) {
+    return !q.has_state || __ldg(q.has_state + s) != 0;
+}
+
+}  // namespace gdn

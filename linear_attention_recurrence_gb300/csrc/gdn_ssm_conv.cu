@@ -1,0 +1,178 @@
+// Causal depthwise convolution over packed sequences, with bias and SiLU:
+//     y[t][c] = act(bias[c] + sum_j w[c][j] X[t - (K - 1) + j][c]),   K = 2, 3 or 4,
+// the K - 1 rows before a sequence's first token taken from its slot of the history
+// (zeros for a new sequence); the slot then receives the sequence's last K - 1 rows.
+//
+// Bound by HBM: every row is read once and written once.  A thread holds 16 bytes of
+// channels (its taps and bias in registers) and walks a tile of rows with the last
+// K - 1 rows in registers, so a row is fetched once per tile; the K - 1 rows before a
+// tile are fetched again (3 in 16 or 32, from L2).
+//
+// History without a race: the tile that holds a sequence's first row also owns the
+// rows at positions 1 .. K - 2 (a tile boundary that would fall there moves behind
+// them).  So the old history is read by exactly one thread per channel, which then
+// writes the new one, in place.
+#include "gdn_ssm.cuh"
+#include "gdn_ssm.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAhead = 4;  // rows whose loads are in flight together
+
+// Sequences whose begin is at or before rows r0 and r1 (all lanes get both counts; one
+// pass of independent loads instead of two binary searches of dependent ones).
+__device__ __forceinline__ void count_begins(const SsmSeqs& q, int64_t r0, int64_t r1, int& c0, int& c1) {
+    c0 = c1 = 1;
+    if (!q.cu) return;
+    c0 = c1 = 0;
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; i < q.n_seq; i += 32) {
+        const int v = i + lane < q.n_seq ? __ldg(q.cu + i + lane) : INT32_MAX;
+        c0 += __popc(__ballot_sync(0xffffffffu, v <= r0));
+        c1 += __popc(__ballot_sync(0xffffffffu, v <= r1));
+    }
+}
+
+// Tile boundary r, moved behind the first K - 1 rows of the sequence that holds it.
+template <int K>
+__device__ __forceinline__ int64_t tile_edge(const SsmSeqs& q, int64_t r, int count) {
+    if (count > 0) {
+        int64_t b, e;
+        seq_rows(q, count - 1, b, e);
+        if (b < r && r < e && r - b < K - 1) r = b + (K - 1) < e ? b + (K - 1) : e;
+    }
+    return r;
+}
+
+template <class T, int K, int VEC>
+__global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams p, const SsmSeqs q, int tile_rows) {
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * tile_rows;
+    const int64_t r1 = r0 + tile_rows < q.T ? r0 + tile_rows : q.T;
+    int c0, c1;
+    count_begins(q, r0, r1, c0, c1);
+    const int64_t lo = tile_edge<K>(q, r0, c0), hi = r1 < q.T ? tile_edge<K>(q, r1, c1) : q.T;
+    const int c = (blockIdx.y * kThreads + threadIdx.x) * VEC;
+    if (c >= p.channels) return;
+
+    float w[VEC][K], bias[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[v][j] = __ldg(p.w + static_cast<int64_t>(c + v) * K + j);
+        bias[v] = p.bias ? __ldg(p.bias + c + v) : 0.f;
+    }
+    const T* x = static_cast<const T*>(p.x) + c;
+    T* y = static_cast<T*>(p.y) + c;
+    T* hist = static_cast<T*>(p.hist);
+
+    int64_t r = lo, b, e;
+    int s = c0 > 0 ? c0 - 1 : 0;
+    seq_rows(q, s, b, e);
+    while (r < hi) {
+        while (e <= r) {
+            if (++s >= q.n_seq) return;
+            seq_rows(q, s, b, e);
+        }
+        if (r < b) {  // rows of no sequence
+            r = b < hi ? b : hi;
+            continue;
+        }
+        float win[K - 1][VEC];
+        if (r == b) {
+            const int slot = hist ? seq_slot(q, s) : -1;
+            T* h = hist + (static_cast<int64_t>(slot) * (K - 1)) * p.channels + c;
+            const bool old = slot >= 0 && seq_has_state(q, s);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) win[j][v] = 0.f;
+                if (old) load_vec<T, VEC>(h + static_cast<int64_t>(j) * p.channels, win[j]);
+            }
+            if (slot >= 0) {
+                const int64_t len = e - b;
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) {
+                    const int64_t at = len - (K - 1) + j;  // the row that becomes history row j
+                    float f[VEC];
+                    if (at >= 0) {
+                        load_vec<T, VEC>(x + (b + at) * p.x_stride, f);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < K - 1; ++i)
+                            if (i == at + (K - 1)) {
+#pragma unroll
+                                for (int v = 0; v < VEC; ++v) f[v] = win[i][v];
+                            }
+                    }
+                    store_vec<T, VEC>(h + static_cast<int64_t>(j) * p.channels, f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) load_vec<T, VEC>(x + (r - (K - 1) + j) * p.x_stride, win[j]);
+        }
+        const int64_t stop = e < hi ? e : hi;
+        for (; r < stop; r += kAhead) {
+            float cur[kAhead][VEC];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (r + u < stop) load_vec<T, VEC>(x + (r + u) * p.x_stride, cur[u]);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (r + u >= stop) break;
+                float f[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float acc = bias[v];
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) acc = fmaf(w[v][j], win[j][v], acc);
+                    acc = fmaf(w[v][K - 1], cur[u][v], acc);
+                    f[v] = p.activation ? ssm_silu(acc) : acc;
+#pragma unroll
+                    for (int j = 0; j + 1 < K - 1; ++j) win[j][v] = win[j + 1][v];
+                    win[K - 2][v] = cur[u][v];
+                }
+                store_vec<T, VEC>(y + (r + u) * p.y_stride, f);
+            }
+        }
+        r = stop;
+    }
+}
+
+template <class T, int K>
+void launch_k(const SsmConvParams& p, const SsmSeqs& q, int sm_count, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const int vec = p.vector ? V : 1;
+    const int blocks_y = (p.channels + kThreads * vec - 1) / (kThreads * vec);
+    // 32-row tiles re-read a tenth of the rows, 16-row tiles a fifth but give twice the
+    // CTAs: short calls take the latter (fewer than 8 CTAs per SM otherwise).
+    const int tile = (q.T / 32) * blocks_y >= static_cast<int64_t>(8) * sm_count ? 32 : 16;
+    const dim3 grid(static_cast<unsigned>((q.T + tile - 1) / tile), blocks_y);
+    if (vec == V)
+        ssm_conv_kernel<T, K, V><<<grid, kThreads, 0, s>>>(p, q, tile);
+    else
+        ssm_conv_kernel<T, K, 1><<<grid, kThreads, 0, s>>>(p, q, tile);
+}
+
+template <class T>
+void launch_t(const SsmConvParams& p, const SsmSeqs& q, int sm_count, cudaStream_t s) {
+    if (p.width == 2) launch_k<T, 2>(p, q, sm_count, s);
+    else if (p.width == 3) launch_k<T, 3>(p, q, sm_count, s);
+    else launch_k<T, 4>(p, q, sm_count, s);
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_conv(const SsmConvParams& p, int sm_count, cudaStream_t s) {
+    const SsmSeqs q{p.cu, p.slots, p.has_state, p.n_seq, p.n_slots, p.T};
+    switch (p.dtype) {
+        case GDN_F32: launch_t<float>(p, q, sm_count, s); break;
+        case GDN_BF16: launch_t<__nv_bfloat16>(p, q, sm_count, s); break;
+        default: launch_t<__half>(p, q, sm_count, s); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

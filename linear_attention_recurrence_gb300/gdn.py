@@ -37,6 +37,11 @@ GDN_OPT_SEQ_ROWS_PER_THREAD = 4
 GDN_OPT_CHUNK_PREP_CTAS = 5
 GDN_OPT_TEST_WITHHOLD_PREP_TASK = 101
 GDN_OPT_TEST_FAIL_SCRATCH_ALLOC = 102
+# activation types (gdn_ssm_*, gdn_block_norm)
+GDN_F32 = 0
+GDN_BF16 = 1
+GDN_F16 = 2
+_DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
 GDN_PRODUCTS_MMA = 0
 GDN_PRODUCTS_FMA = 1
 GDN_PRODUCTS_TCGEN05 = 2
@@ -58,7 +63,8 @@ _lib = None
 EXPORTS = ("gdn_recurrence", "gdn_out_norm", "gdn_last_error", "gdn_device_status",
            "gdn_release_scratch", "gdn_poison_scratch", "gdn_chunked_scratch_bytes", "gdn_launch_count",
            "gdn_recurrence_chunked_noalloc", "gdn_decode", "gdn_prestage", "gdn_recurrence_norm",
-           "gdn_set_option", "gdn_get_option")
+           "gdn_set_option", "gdn_get_option", "gdn_ssm_conv", "gdn_ssm_scan", "gdn_ssm_scan_workspace_bytes",
+           "gdn_ssm_step", "gdn_block_norm")
 
 
 class GDNError(RuntimeError):
@@ -92,6 +98,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_recurrence_norm.restype = i32
         lib.gdn_out_norm.argtypes = [vp, vp, vp, ctypes.c_float, vp, i64, i32, i32, vp]
         lib.gdn_out_norm.restype = i32
+        f32, sz = ctypes.c_float, ctypes.c_size_t
+        lib.gdn_ssm_conv.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i32, i32, vp, i64, i64, i32, i32, i32, i32, vp]
+        lib.gdn_ssm_conv.restype = i32
+        lib.gdn_ssm_scan.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32,
+                                     vp, i64, i64, i32, i32, i32, i32, i32, vp, sz, vp]
+        lib.gdn_ssm_scan.restype = i32
+        lib.gdn_ssm_scan_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
+        lib.gdn_ssm_scan_workspace_bytes.restype = sz
+        lib.gdn_ssm_step.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i64, i32, i32,
+                                     i32, i32, i32, i32, i32, i32, vp]
+        lib.gdn_ssm_step.restype = i32
+        lib.gdn_block_norm.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, f32, f32, vp, i64, vp, i64, i64, i32,
+                                       i32, i32, vp]
+        lib.gdn_block_norm.restype = i32
         lib.gdn_last_error.argtypes = []
         lib.gdn_last_error.restype = ctypes.c_char_p
         lib.gdn_device_status.argtypes = [vp]
@@ -318,6 +338,262 @@ def gdn_out_norm(out, z, w, eps: float = 1e-6, y=None, stream=None):
     rc = lib.gdn_out_norm(_ptr(out), _ptr(z), _ptr(w), float(eps), _ptr(y), T, n_vh, d, _stream_ptr(stream))
     _check(rc)
     return y
+
+
+# ---- the selective state space layer and the block norm ----
+
+def _rows(t, name, shape, dtype, device):
+    """A tensor of rows: its trailing dimensions contiguous, the rows any distance
+    apart.  Returns (address, elements between rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.data_ptr(), st[0]
+
+
+def _dense(t, name, shape, dtype, device):
+    """A contiguous tensor's address, or None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _activations(t, name, dims):
+    """Checks the tensor that fixes a call's type and device; returns its dtype number."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    return _DTYPES[t.dtype]
+
+
+class _Launch:
+    """The device and stream of one call: the tensors' device is made current if it is
+    not, and what the call allocates belongs to the stream it runs on."""
+
+    __slots__ = ("device", "stream", "ptr", "other")
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.stream = stream
+        self.other = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self.ptr = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        mine = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(self.stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(mine)  # the caller goes on to use it there
+        return t
+
+    def __call__(self, fn, *args):
+        if self.other is None:
+            rc = fn(*args, self.ptr)
+        else:
+            with self.other:
+                rc = fn(*args, self.ptr)
+        if rc != GDN_OK:
+            _check(rc)
+
+
+def _seqs(cu_seqlens, slots, has_state, pool, device):
+    """(cu, slots, has_state, n_seq, n_slots) of a packed call; pool: its states or history, or None."""
+    i32 = torch.int32
+    n = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if n < 0:
+        raise ValueError("cu_seqlens needs one element at least")
+    if has_state is not None and has_state.dtype == torch.bool:
+        has_state = has_state.view(torch.uint8)
+    n_slots = 0 if pool is None else pool.shape[0]
+    if pool is not None and slots is None and n_slots < n:
+        raise ValueError(f"{n} sequences but {n_slots} slots")
+    return (_dense(cu_seqlens, "cu_seqlens", (n + 1,), i32, device), _dense(slots, "slots", (n,), i32, device),
+            _dense(has_state, "has_state", (n,), torch.uint8, device), n, n_slots)
+
+
+def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_state=None, activation: int = 1,
+                 out=None, stream=None):
+    """Causal depthwise convolution (and SiLU) over packed sequences; updates the
+    slots of ``hist`` in place and returns ``out``.
+
+    x: [T][channels], FP32, BF16 or FP16, the rows any distance apart; w:
+    [channels][width] and bias: [channels] (FP32), width 2 to 4; hist:
+    [slots][width - 1][channels] of x's type, or None (sequences start from zeros).
+    cu_seqlens: [n + 1] int32 on the device (None: one sequence); slots: [n] int32
+    (None: sequence i has slot i; -1: no slot); has_state: [n] bool (None: all
+    continue from their slots).  ``out`` ([T][channels]) is allocated if None; rows
+    of no sequence are left as they were.
+    """
+    dt = _activations(x, "x", 2)
+    dev, (T, ch) = x.device, x.shape
+    xp, xs = _rows(x, "x", (T, ch), x.dtype, dev)
+    if w.dim() != 2:
+        raise ValueError("w must have 2 dimensions")
+    width = w.shape[1]
+    wp = _dense(w, "w", (ch, width), torch.float32, dev)
+    bp = _dense(bias, "bias", (ch,), torch.float32, dev)
+    if hist is not None and hist.dim() != 3:
+        raise ValueError("hist must have 3 dimensions")
+    hp = None if hist is None else _dense(hist, "hist", (hist.shape[0], width - 1, ch), x.dtype, dev)
+    cu, sl, has, n, n_slots = _seqs(cu_seqlens, slots, has_state, hist, dev)
+    go = _Launch(dev, stream)
+    if out is None:
+        out = go.empty((T, ch), x.dtype)
+    op, os_ = _rows(out, "out", (T, ch), x.dtype, dev)
+    go(load_library().gdn_ssm_conv, xp, xs, wp, bp, hp, cu, sl, has, n, n_slots, op, max(os_, ch) if T <= 1 else os_, T,
+       ch, width, activation, dt)
+    return out
+
+
+def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seqlens=None, slots=None, has_state=None,
+                 out=None, stream=None):
+    """Selective state space scan over packed sequences; updates the slots of
+    ``states`` in place and returns ``out``.
+
+    x: [T][n_heads][head_dim]; a: [T][n_heads]; B, C: [T][n_groups][state_dim]; z: as
+    x, or None: all of one type (FP32, BF16 or FP16), the rows any distance apart.
+    A_log, dt_bias, D (or None): [n_heads] FP32; states:
+    [slots][n_heads][state_dim][head_dim] FP32, or None (sequences start from zeros,
+    nothing is kept).  Head h reads group h % n_groups.  cu_seqlens, slots, has_state
+    as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.
+    """
+    dt = _activations(x, "x", 3)
+    if B.dim() != 3:
+        raise ValueError("B must have 3 dimensions")
+    dev, ty, f32 = x.device, x.dtype, torch.float32
+    T, H, P = shape = x.shape
+    G, N = B.shape[1], B.shape[2]
+    xp, xs = _rows(x, "x", shape, ty, dev)
+    ap, as_ = _rows(a, "a", (T, H), ty, dev)
+    bp, bs = _rows(B, "B", (T, G, N), ty, dev)
+    cp, cs = _rows(C, "C", (T, G, N), ty, dev)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", shape, ty, dev)
+    alp = _dense(A_log, "A_log", (H,), f32, dev)
+    dbp = _dense(dt_bias, "dt_bias", (H,), f32, dev)
+    dp = _dense(D, "D", (H,), f32, dev)
+    sp = None if states is None else _dense(states, "states", (states.shape[0], H, N, P), f32, dev)
+    cu, sl, has, n, n_slots = _seqs(cu_seqlens, slots, has_state, states, dev)
+    go = _Launch(dev, stream)
+    if out is None:
+        out = go.empty(shape, ty)
+    op, os_ = _rows(out, "out", shape, ty, dev)
+    lib = load_library()
+    need = lib.gdn_ssm_scan_workspace_bytes(T, n, H, P, N, dt)
+    ws = go.empty((need,), torch.uint8) if need else None
+    go(lib.gdn_ssm_scan, xp, xs, ap, as_, bp, bs, cp, cs, zp, zs, alp, dbp, dp, sp, cu, sl, has, n, n_slots, op,
+       max(os_, H * P) if T <= 1 else os_, T, H, G, P, N, dt, None if ws is None else ws.data_ptr(), need)
+    return out
+
+
+def gdn_ssm_step(xbc, a, conv_w, A_log, dt_bias, hist, states, conv_bias=None, D=None, z=None, slots=None,
+                 activation: int = 1, out=None, stream=None):
+    """One token of the convolution and the scan for each request, in one launch;
+    updates the slots of ``hist`` and ``states`` in place and returns ``out``.
+
+    xbc: [batch][n_heads head_dim + 2 n_groups state_dim], the packed x, B and C before
+    the convolution; a: [batch][n_heads]; z: [batch][n_heads][head_dim] or None; hist:
+    [slots][width - 1][channels]: all of one type.  conv_w: [channels][width];
+    conv_bias, A_log, dt_bias, D, states as in gdn_ssm_conv and gdn_ssm_scan.  slots:
+    [batch] int32 (None: request i has slot i; -1: a padding row, left out).  ``out``
+    ([batch][n_heads][head_dim]) is allocated if None.
+    """
+    dt = _activations(xbc, "xbc", 2)
+    if states.dim() != 4 or conv_w.dim() != 2 or hist.dim() != 3:
+        raise ValueError("states must have 4 dimensions, hist 3 and conv_w 2")
+    dev, ty, f32 = xbc.device, xbc.dtype, torch.float32
+    n, cw = xbc.shape
+    n_slots, H, N, P = states.shape
+    width = conv_w.shape[1]
+    G = (cw - H * P) // (2 * N) if N else 0
+    if G <= 0 or H * P + 2 * G * N != cw:
+        raise ValueError(f"xbc's row of {cw} is not n_heads * head_dim + 2 * n_groups * state_dim "
+                         f"({H} heads of {P}, state_dim {N})")
+    xp, xs = _rows(xbc, "xbc", (n, cw), ty, dev)
+    ap, as_ = _rows(a, "a", (n, H), ty, dev)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", (n, H, P), ty, dev)
+    wp = _dense(conv_w, "conv_w", (cw, width), f32, dev)
+    bp = _dense(conv_bias, "conv_bias", (cw,), f32, dev)
+    alp = _dense(A_log, "A_log", (H,), f32, dev)
+    dbp = _dense(dt_bias, "dt_bias", (H,), f32, dev)
+    dp = _dense(D, "D", (H,), f32, dev)
+    hp = _dense(hist, "hist", (n_slots, width - 1, cw), ty, dev)
+    sp = _dense(states, "states", (n_slots, H, N, P), f32, dev)
+    sl = _dense(slots, "slots", (n,), torch.int32, dev)
+    go = _Launch(dev, stream)
+    if out is None:
+        out = go.empty((n, H, P), ty)
+    op, os_ = _rows(out, "out", (n, H, P), ty, dev)
+    go(load_library().gdn_ssm_step, xp, xs, ap, as_, zp, zs, wp, bp, alp, dbp, dp, hp, sp, sl, n_slots, op,
+       max(os_, H * P) if n <= 1 else os_, n, H, G, P, N, width, activation, dt)
+    return out
+
+
+def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: bool = False, scale: float = 1.0,
+                   eps: float = 1e-6, residual_out=None, out=None, stream=None):
+    """The norms around a block, with its gate and residual scale, in one pass:
+    residual <- residual + scale * act(gate) * RMSNorm(b; w_post), out = RMSNorm(residual; w_pre).
+    Returns (residual, out).
+
+    b: [T][dim]; gate: [T][dim], [1][dim] (one row for every token) or None, both of
+    one type (FP32, BF16 or FP16); residual: [T][dim] of that type or FP32; w_pre,
+    w_post (or None: b as it is): [dim] FP32.  The residual is updated in place unless
+    ``residual_out`` is given; ``out`` ([T][dim] of b's type) is allocated if None.
+    """
+    dt = _activations(b, "b", 2)
+    rt = _activations(residual, "residual", 2)
+    dev, ty, f32 = b.device, b.dtype, torch.float32
+    shape = T, d = b.shape
+    bp, bs = _rows(b, "b", shape, ty, dev)
+    rp, rs = _rows(residual, "residual", shape, residual.dtype, dev)
+    gp = None
+    gs = 0
+    if gate is not None:
+        one = gate.dim() == 2 and gate.shape[0] == 1
+        gp, gs = _rows(gate, "gate", (1, d) if one else shape, ty, dev)
+        gs = 0 if one else gs
+    wpre = _dense(w_pre, "w_pre", (d,), f32, dev)
+    if wpre is None:
+        raise TypeError("w_pre must be a torch.Tensor")
+    wpost = _dense(w_post, "w_post", (d,), f32, dev)
+    go = _Launch(dev, stream)
+    if residual_out is None:
+        residual_out, qp, qs = residual, rp, rs
+    else:
+        qp, qs = _rows(residual_out, "residual_out", shape, residual.dtype, dev)
+    if out is None:
+        out = go.empty(shape, ty)
+    op, os_ = _rows(out, "out", shape, ty, dev)
+    if T <= 1:
+        qs, os_, rs = max(qs, d), max(os_, d), max(rs, d)
+    go(load_library().gdn_block_norm, bp, bs, rp, rs, gp, gs, 1 if gate_sigmoid else 0, wpost, wpre, scale, eps, qp, qs,
+       op, os_, T, d, dt, rt)
+    return residual_out, out
 
 
 def gdn_device_status(stream=None) -> int:
