@@ -11,6 +11,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_ssm.h"
 #include "gdn_device.cuh"
 
 namespace {
@@ -707,9 +708,13 @@ int gdn_device_status(void* cuda_stream) {
     int na_word = 0;
     e = gdn::noalloc_take_status(dev, &na_word);
     if (e != cudaSuccess) return cuda_fail(e, "status read (non-allocating entry point)");
-    if (word == 0 && na_word == 0) return GDN_OK;
-    std::string msg = "a kernel gave up a bounded wait (status word " + std::to_string(word | na_word) + ")";
+    int ssm_word = 0;
+    e = gdn::ssm_take_status(dev, &ssm_word);
+    if (e != cudaSuccess) return cuda_fail(e, "status read (selective scan)");
+    if (word == 0 && na_word == 0 && ssm_word == 0) return GDN_OK;
+    std::string msg = "a kernel gave up a bounded wait (status word " + std::to_string(word | na_word | ssm_word) + ")";
     if (na_word != 0) msg += " in gdn_recurrence_chunked_noalloc";
+    if (ssm_word != 0) msg += " in gdn_ssm_scan";
     if (word & gdn::kDevErrNormTimeout) msg += " (the fused sequential norm's exchange between CTAs)";
     if (word & gdn::kDevErrRingTimeout) msg += " (a chunk prep's wait for a free slot of the tile ring)";
     uint32_t diag[3] = {0, 0, 0};

@@ -48,6 +48,15 @@ struct SsmScanParams {
 // One token after the other, the state in registers (gdn_ssm_scan.cu).
 cudaError_t launch_ssm_scan_tokens(const SsmScanParams& p, cudaStream_t s);
 
+// Chunks of 128 tokens on the tensor cores (gdn_ssm_scan_tc.cu): 16-bit types, head_dim
+// and state_dim 64 or 128, rows of x, B and C on 16-byte boundaries.
+constexpr int kSsmTcMinTokens = 64;  // tokens per sequence from which it is taken
+bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq);
+size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count);
+cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_count, cudaStream_t s);
+// The tensor form's status word on `device`, read and cleared (0 if it never ran there).
+cudaError_t ssm_take_status(int device, int* word);
+
 // ---- one token of the convolution and the scan for each request (gdn_ssm_step.cu) ----
 struct SsmStepParams {
     const void *xbc, *a, *z;  // z may be nullptr

@@ -133,8 +133,11 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
 }
 
 size_t gdn_ssm_scan_workspace_bytes(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int dtype) {
-    (void)T; (void)n_seq; (void)n_heads; (void)head_dim; (void)state_dim; (void)dtype;
-    return 0;
+    int sms = 0;
+    if (T <= 0 || n_seq <= 0 || n_heads <= 0 || head_dim <= 0 || state_dim <= 0 ||
+        !gdn::ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) || sm_count(&sms) != GDN_OK)
+        return 0;
+    return gdn::ssm_scan_tc_workspace(T, n_seq, n_heads, head_dim, state_dim, sms);
 }
 
 int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const void* B, int64_t b_stride,
@@ -177,7 +180,19 @@ int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_strid
     const SsmScanParams p{x, a, B, C, z, y, x_stride, a_stride, b_stride, c_stride, z_stride, y_stride, A_log, dt_bias,
                           D, states, cu_seqlens, slots, has_state, n_seq, n_slots, T, n_heads, n_groups, head_dim,
                           state_dim, dtype};
-    cudaError_t err = launch_ssm_scan_tokens(p, static_cast<cudaStream_t>(cuda_stream));
+    // TMA takes rows on 16-byte boundaries that lie one after the other
+    auto tma_rows = [](const void* ptr, int64_t stride, int64_t width) {
+        return is_aligned(ptr, 16) && stride % 8 == 0 && stride >= width;
+    };
+    cudaError_t err;
+    if (ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) && tma_rows(x, x_stride, xw) &&
+        tma_rows(B, b_stride, bw) && tma_rows(C, c_stride, bw)) {
+        int sms = 0;
+        if (int rc = sm_count(&sms)) return rc;
+        err = launch_ssm_scan_tc(p, workspace, sms, static_cast<cudaStream_t>(cuda_stream));
+    } else {
+        err = launch_ssm_scan_tokens(p, static_cast<cudaStream_t>(cuda_stream));
+    }
     if (err != cudaSuccess) return cuda_bad(err, "scan launch");
     internal_count_launch();
     return GDN_OK;

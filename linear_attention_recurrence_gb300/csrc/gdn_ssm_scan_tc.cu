@@ -1,0 +1,853 @@
+// Selective state space scan of 16-bit prompts on the tensor cores (sm_103a).
+//
+// The recurrence of gdn_ssm_scan.cu over chunks of 128 tokens.  Per head and chunk, with
+// gamma_t the running sum of the log-decays inside the chunk, H the state before it and
+// 16-bit x, B, C (the products' operands as they arrive):
+//     G    = C B^T                                       128 x 128, K = state_dim
+//     M    = G o e^(gamma_t - gamma_i) dt_i  (i <= t)    rounded to 16 bits
+//     Y^T  = x^T M^T + (H^T C^T) diag(e^gamma_t)         128 x 128, K = 128 and state_dim
+//     H^T <- e^gamma_last H^T + (w o x)^T B,  w_t = dt_t e^(gamma_last - gamma_t)
+// in transposed form: head_dim is the MMA's M (tensor-memory lanes), so H^T stays in
+// tensor memory as the FP32 accumulator of its update.  Every product is a tcgen05.mma
+// of the rows' own type: H is rounded to it for the product with C (as M is: together
+// one rounding of disjoint terms of y), but the update takes w o x in parts of that type
+// (three of 8 bits for BF16, two of 11 for FP16), so the state keeps FP32's precision.
+// M is formed by exponentials of differences (never above 0), w from sums that start at
+// the chunk's end, so neither loses precision when the decay over the chunk is large.
+// FP16's range is short: there dt and w enter M and the update divided by a power of two
+// of each chunk (its largest dt, its largest w), which the output and the state's decay
+// multiply back, so neither small steps nor large ones leave the range.
+//
+// Work is one CTA per (head, segment of a sequence); it walks the segment's chunks.
+// Where sequences x heads do not fill the device, sequences are cut into segments: a
+// first launch forms, for every segment but the last, its own contribution to the state
+// behind it (the update's product alone) and its decay; the second starts each segment
+// from the sum of those before it.
+//
+// Warp roles (512 threads): warps 0-3 form M (lane = token); 4-7 the parts of w o x and
+// the state's decay and rounding (lane = column of x); 8-11 the output; 12 issues the
+// copies, 13 the MMAs, 14 forms the gates.  MMA order per chunk: H^T C^T, the second
+// half of G, the first half of Y, the update (8 blocks of 16 tokens, behind the parts),
+// the next chunk's first half of G, the second half of Y.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "gdn_ssm.cuh"
+#include "gdn_ssm.h"
+
+namespace gdn {
+namespace {
+
+constexpr int L = 128;        // tokens per chunk
+constexpr int kThreadsTc = 512;
+constexpr int kStages = 2;
+constexpr int kCopyWarp = 12, kMmaWarp = 13, kGateWarp = 14;
+
+// tensor-memory columns
+constexpr uint32_t TM_H = 0;     // H^T, FP32 [head_dim lanes][state_dim]
+constexpr uint32_t TM_HB = 128;  // H^T in 16 bits, 2 per column
+constexpr uint32_t TM_G = 192;   // G, 64 columns (tokens i) at a time [128 lanes t]
+constexpr uint32_t TM_Y1 = 256;  // x^T M^T, 64 columns (tokens t) at a time
+constexpr uint32_t TM_Y2 = 320;  // H^T C^T, 128 columns
+constexpr uint32_t TM_XW = 448;  // parts of w o x: ring of blocks of 16 tokens, 8 columns a part
+constexpr uint32_t TM_COLS = 512;
+
+// shared memory, from a 1024-byte boundary
+constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
+constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
+constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
+constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: (gamma, dt)[128] at 0, w[128] at
+constexpr uint32_t SM_GATE_STAGE = 2176;                // 256, e^gamma[128] at 384, 2^k of w and 2^j of dt at 512
+constexpr uint32_t SM_MISC = SM_GATE + kStages * SM_GATE_STAGE;
+constexpr uint32_t SM_TOTAL = SM_MISC + 512;
+static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
+
+enum {
+    B_FULL, B_GATE = B_FULL + kStages, B_EMPTY = B_GATE + kStages,
+    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_S, B_Y1, B_Y1FREE, B_Y2FREE,
+    B_XW,             // [kXwSlots <= 4]
+    B_XWFREE = B_XW + 4,
+    B_TAIL = B_XWFREE + 4,
+    B_FIN,
+    NBAR
+};
+static_assert(SM_MISC + NBAR * 8 + 16 <= SM_TOTAL, "barrier space");
+
+__device__ int g_ssm_status;  // bits of kDevErr*
+
+struct TcParams {
+    CUtensorMap tm_x, tm_b, tm_c;  // [T][n_heads head_dim], [T][n_groups state_dim] twice; box 64 x 128
+    const void *a, *z;
+    void* y;
+    int64_t a_stride, z_stride, y_stride;
+    const float *A_log, *dt_bias, *D;
+    float* states;
+    float* ws;        // [units][n_heads][state_dim][head_dim], or nullptr: no segments
+    float* ws_decay;  // [units][n_heads]
+    SsmSeqs q;
+    int64_t units;    // the grid's: no fewer than the segments of disjoint sequences
+    int seg;          // tokens per segment, a multiple of L
+    int n_heads, n_groups;
+};
+
+// ---- tcgen05, 16-bit operands ----
+__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// 128-byte swizzled operand whose rows are the K index (64 elements of M or N per row):
+// blocks of 64 elements kBox apart, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t a) {
+    return static_cast<uint64_t>((a & 0x3FFFF) >> 4) | (static_cast<uint64_t>(kBox >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// 128-byte swizzled operand whose rows are M or N (64 elements of K per row).
+__device__ __forceinline__ uint64_t desc_k(uint32_t a) {
+    return static_cast<uint64_t>((a & 0x3FFFF) >> 4) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_u8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_u16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// ---- pairs of the 16-bit types ----
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if constexpr (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <bool BF16>
+__device__ __forceinline__ float unpack1(uint16_t v) {
+    if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    return __half2float(__ushort_as_half(v));
+}
+
+// The power of two just above v, from 2^-14 (the state times its inverse stays far from
+// overflow) to 2^24.
+__device__ __forceinline__ float range_scale(float v) {
+    int e = static_cast<int>((__float_as_uint(v) >> 23) & 255) - 126;
+    e = e < -14 ? -14 : e > 24 ? 24 : e;
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+struct Sync {
+    uint64_t* bar;
+    volatile int* abort_flag;
+};
+// Waits for phase `n` (0, 1, ...) of a barrier.  False once some wait of the CTA gave up.
+__device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        if (mbar_try_wait(&s.bar[b], n & 1)) return true;
+        if ((i & 63) == 63 && *s.abort_flag) return false;
+    }
+    *s.abort_flag = 1;
+    report_timeout(&g_ssm_status);
+    return false;
+}
+// One arrival for the calling warp.
+__device__ __forceinline__ void warp_arrive(const Sync& s, int b) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&s.bar[b]);
+}
+
+// The unit (sequence, segment) of a CTA, found by its sequences' segment counts.
+struct Unit {
+    int s, k, n_seg;      // sequence, segment of it, its segments
+    int64_t begin;        // first row
+    int len;              // rows
+};
+__device__ bool find_unit(const SsmSeqs& q, int seg, int64_t units, int64_t u, Unit* out, int* warp_sum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ Unit found;
+    if (tid == 0) found.s = -1;
+    int64_t base = 0;
+    for (int s0 = 0; s0 < q.n_seq; s0 += kThreadsTc) {
+        int64_t b = 0, e = 0;
+        if (s0 + tid < q.n_seq) seq_rows(q, s0 + tid, b, e);
+        const int n = static_cast<int>((e - b + seg - 1) / seg);
+        int inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = base;
+        int total = 0;
+        for (int w = 0; w < kThreadsTc / 32; ++w) {
+            if (w < warp) before += warp_sum[w];
+            total += warp_sum[w];
+        }
+        const int64_t first = before + inc - n;
+        // (a sequence whose segments pass the grid's end, as overlapping bounds may give, is left out)
+        if (u >= first && u < first + n && first + n <= units) {
+            const int k = static_cast<int>(u - first);
+            found.s = s0 + tid;
+            found.k = k;
+            found.n_seg = n;
+            found.begin = b + static_cast<int64_t>(k) * seg;
+            found.len = static_cast<int>(e - found.begin < seg ? e - found.begin : seg);
+        }
+        base += total;
+        __syncthreads();
+        if (base > u) break;  // uniform
+    }
+    __syncthreads();
+    *out = found;
+    return found.s >= 0;
+}
+
+// PASS 0: outputs (and final states); PASS 1: the segments' contributions.
+template <bool BF16, int P, int N, int PASS>
+__global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid_constant__ TcParams p) {
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    constexpr int PARTS = BF16 ? 3 : 2;
+    constexpr int SLOTS = 64 / (8 * PARTS);
+    constexpr bool OUT = PASS == 0;
+    constexpr int NB = N / 64, PB = P / 64;
+    unsigned char* sm = aligned_dynamic_smem<unsigned char, 1024>();
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM_MISC + NBAR * 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
+    int* warp_sum = reinterpret_cast<int*>(sm + SM_GATE);  // before the gates are written
+    const Sync sy{bar, abort_flag};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const int h = blockIdx.x % p.n_heads;
+    const int64_t u = blockIdx.x / p.n_heads;
+    Unit un;
+    if (!find_unit(p.q, p.seg, p.units, u, &un, warp_sum)) return;
+    if (PASS == 1 && un.k == un.n_seg - 1) return;  // nothing reads a last segment's contribution
+    const int g = h % p.n_groups;
+    const int nch = (un.len + L - 1) / L;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bar[B_FULL + s], 1);
+            mbar_init(&bar[B_GATE + s], 1);
+            mbar_init(&bar[B_EMPTY + s], OUT ? 13 : 5);
+        }
+        const int one[] = {B_G, B_MFREE, B_S, B_Y1, B_FIN};
+        for (int b : one) mbar_init(&bar[b], 1);
+        const int four[] = {B_TAIL, B_GFREE, B_M0, B_M1, B_H, B_Y1FREE, B_Y2FREE};
+        for (int b : four) mbar_init(&bar[b], 4);
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&bar[B_XW + s], 4);
+            mbar_init(&bar[B_XWFREE + s], 1);
+        }
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_slot, TM_COLS);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = *tmem_slot;
+
+    if (warp == kCopyWarp) {
+        if (lane == 0) {
+            int c = 0;
+            for (; c < nch; ++c) {
+                const int s = c % kStages;
+                if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+                unsigned char* st = sm + s * SM_STAGE;
+                const int row = static_cast<int>(un.begin) + c * L;
+                mbar_arrive_expect_tx(&bar[B_FULL + s], (OUT ? 2 * NB + PB : NB + PB) * kBox);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (OUT) tma_load_2d(st + SM_C + i * kBox, &p.tm_c, &bar[B_FULL + s], g * N + 64 * i, row);
+                    tma_load_2d(st + SM_B + i * kBox, &p.tm_b, &bar[B_FULL + s], g * N + 64 * i, row);
+                }
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    tma_load_2d(st + SM_X + i * kBox, &p.tm_x, &bar[B_FULL + s], h * P + 64 * i, row);
+            }
+            // the copies in flight land before the CTA ends, also after a wait that gave up
+            for (int i = c > kStages ? c - kStages : 0; i < c; ++i)
+                for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(&bar[B_FULL + i % kStages], (i / kStages) & 1); ++n) {
+                }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
+            constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
+            constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 128, false, false);
+            constexpr uint32_t ID_S = idesc_f16(BF16, 128, N, false, true);     // B: N-major
+            const uint32_t sm0 = smem_addr(sm);
+            uint32_t gi = 0, yi = 0, qi = 0;
+            auto issue_g = [&](int c, int half) {  // G's columns of tokens 64 half .. +63
+                if (gi > 0 && !wait_phase(sy, B_GFREE, gi - 1)) return false;
+                tc_fence_after_sync();
+                const uint32_t st = sm0 + (c % kStages) * SM_STAGE;
+#pragma unroll
+                for (int k = 0; k < N / 16; ++k)
+                    mma_ss(tm + TM_G, desc_k(st + SM_C + (k / 4) * kBox + (k % 4) * 32),
+                           desc_k(st + SM_B + (k / 4) * kBox + half * 8192 + (k % 4) * 32), ID_G, k > 0);
+                umma_commit(&bar[B_G]);
+                ++gi;
+                return true;
+            };
+            auto issue_y1 = [&](int c, int half) {
+                if (!wait_phase(sy, half ? B_M1 : B_M0, c)) return false;
+                if (yi > 0 && !wait_phase(sy, B_Y1FREE, yi - 1)) return false;
+                tc_fence_after_sync();
+                const uint32_t x = sm0 + (c % kStages) * SM_STAGE + SM_X, m = sm0 + SM_M;
+#pragma unroll
+                for (int k = 0; k < 4 + 4 * half; ++k)
+                    mma_ss(tm + TM_Y1, desc_mn(x + k * 2048),
+                           desc_k(k < 4 ? m + half * 8192 + k * 32 : m + kBox + (k - 4) * 32), ID_Y1, k > 0);
+                umma_commit(&bar[B_Y1]);
+                ++yi;
+                return true;
+            };
+            bool ok = wait_phase(sy, B_FULL, 0);
+            if (OUT) ok = ok && issue_g(0, 0);
+            for (int c = 0; ok && c < nch; ++c) {
+                const int s = c % kStages;
+                const uint32_t st = sm0 + s * SM_STAGE;
+                if (!wait_phase(sy, B_FULL + s, c / kStages)) break;
+                if (!wait_phase(sy, B_H, c)) break;
+                if (OUT) {
+                    if (c > 0 && !wait_phase(sy, B_Y2FREE, c - 1)) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < N / 16; ++k)
+                        mma_ts(tm + TM_Y2, tm + TM_HB + 8 * k, desc_k(st + SM_C + (k / 4) * kBox + (k % 4) * 32), ID_Y2, k > 0);
+                    if (!issue_g(c, 1) || !issue_y1(c, 0)) break;
+                }
+                for (int j = 0; j < L / 16 && ok; ++j, ++qi) {
+                    const int slot = qi % SLOTS;
+                    if (!wait_phase(sy, B_XW + slot, qi / SLOTS)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t b = desc_mn(st + SM_B + j * 2048);
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) mma_ts(tm + TM_H, tm + TM_XW + (slot * PARTS + i) * 8, b, ID_S, true);
+                    umma_commit(&bar[B_XWFREE + slot]);
+                }
+                if (!ok) break;
+                umma_commit(&bar[B_S]);
+                if (OUT) {
+                    if (c + 1 < nch) {
+                        if (!wait_phase(sy, B_FULL + (c + 1) % kStages, (c + 1) / kStages)) break;
+                        if (!issue_g(c + 1, 0)) break;
+                    }
+                    if (!issue_y1(c, 1)) break;
+                    umma_commit(&bar[B_MFREE]);
+                }
+                umma_commit(&bar[B_EMPTY + s]);
+            }
+            // every MMA ends before tensor memory is freed
+            umma_commit(&bar[B_FIN]);
+            for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(&bar[B_FIN], 0); ++n) {
+            }
+        }
+    } else if (warp == kGateWarp) {
+        const float A = ssm_rate(__ldg(p.A_log + h)), bias = __ldg(p.dt_bias + h);
+        const T* a = static_cast<const T*>(p.a) + un.begin * p.a_stride + h;
+        float seg_sum = 0.f;
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % kStages;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = c * L + 4 * lane + i;
+                v[i] = t < un.len ? to_f<T>(a[t * p.a_stride]) : 0.f;
+            }
+            if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+            float dt[4], g2[4], pre[4], suf[4];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool live = c * L + 4 * lane + i < un.len;
+                dt[i] = live ? ssm_softplus(v[i] + bias) : 0.f;
+                g2[i] = fmaxf(A * dt[i] * kLog2e, kMinLog2Decay);
+                sum += g2[i];
+                pre[i] = sum;
+            }
+            float up = sum, down = sum;  // inclusive sums over the lanes, from either end
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, up, off), y = __shfl_down_sync(0xffffffffu, down, off);
+                if (lane >= off) up += x;
+                if (lane + off < 32) down += y;
+            }
+            up = __shfl_up_sync(0xffffffffu, up, 1);
+            down = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) up = 0.f;
+            if (lane == 31) down = 0.f;
+            float after = down;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                suf[i] = after;
+                after += g2[i];
+                pre[i] += up;
+            }
+            float* gt = reinterpret_cast<float*>(sm + SM_GATE + s * SM_GATE_STAGE);
+            float4* gd = reinterpret_cast<float4*>(gt);
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = dt[i] * exp2f(suf[i]);
+            if constexpr (!BF16) {
+                float wm = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), dm = fmaxf(fmaxf(dt[0], dt[1]), fmaxf(dt[2], dt[3]));
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, off));
+                    dm = fmaxf(dm, __shfl_xor_sync(0xffffffffu, dm, off));
+                }
+                const float ws = range_scale(wm), ds = range_scale(dm);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] *= 1.0f / ws;  // powers of two: exact
+                    dt[i] *= 1.0f / ds;
+                }
+                if (lane == 0) {
+                    gt[512] = ws;
+                    gt[513] = ds;
+                }
+            }
+            gd[2 * lane] = make_float4(pre[0], dt[0], pre[1], dt[1]);
+            gd[2 * lane + 1] = make_float4(pre[2], dt[2], pre[3], dt[3]);
+            reinterpret_cast<float4*>(gt + 256)[lane] =
+                make_float4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<float4*>(gt + 384)[lane] = make_float4(exp2f(pre[0]), exp2f(pre[1]), exp2f(pre[2]), exp2f(pre[3]));
+            seg_sum += pre[3];  // lane 31: the chunk's sum
+            warp_arrive(sy, B_GATE + s);
+        }
+        if (PASS == 1 && lane == 31) p.ws_decay[u * p.n_heads + h] = exp2f(seg_sum);
+    } else if (warp < 4) {
+        if constexpr (OUT) {
+            // ---- M: lane = token t ----
+            const int t = tid;
+            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+            unsigned char* m0 = sm + SM_M + t * 128;                   // columns 0-63
+            unsigned char* m1 = sm + SM_M + kBox + (t - 64) * 128;     // columns 64-127 (t >= 64)
+            // the blocks of 32 columns above the diagonal blocks stay zero
+            if ((warp & 1) == 0) {
+                unsigned char* m = warp == 0 ? m0 : m1;
+#pragma unroll
+                for (int k = 4; k < 8; ++k) *reinterpret_cast<uint4*>(m + ((k ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+            uint32_t gi = 0;
+            for (int c = 0; c < nch; ++c) {
+                const int s = c % kStages;
+                if (!wait_phase(sy, B_GATE + s, c / kStages)) break;
+                const float2* gd = reinterpret_cast<const float2*>(sm + SM_GATE + s * SM_GATE_STAGE);
+                const float gt = gd[t].x;
+                bool ok = true;
+#pragma unroll
+                for (int half = 0; half < 2; ++half, ++gi) {
+                    if (!wait_phase(sy, B_G, gi) || (half == 0 && c > 0 && !wait_phase(sy, B_MFREE, c - 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    if (half == 0 || warp >= 2) {
+#pragma unroll 1
+                        for (int cb = 0; cb < 2; ++cb) {
+                            const int c0 = 64 * half + 32 * cb;
+                            if (c0 > warp * 32) break;
+                            float v[32];
+                            tmem_ld32(tm + lanes + TM_G + 32 * cb, v);
+                            const bool diag = c0 == warp * 32;
+                            unsigned char* m = half ? m1 : m0;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int i = 0; i < 8; i += 2) {
+                                    const float4 e = *reinterpret_cast<const float4*>(&gd[c0 + j + i]);
+                                    float a0 = v[j + i] * (ex2(gt - e.x) * e.y), a1 = v[j + i + 1] * (ex2(gt - e.z) * e.w);
+                                    if (diag) {  // selected, not multiplied: what is above may be anything
+                                        if (j + i > lane) a0 = 0.f;
+                                        if (j + i + 1 > lane) a1 = 0.f;
+                                    }
+                                    o[i / 2] = pack2<BF16>(a0, a1);
+                                }
+                                *reinterpret_cast<uint4*>(m + (((4 * cb + j / 8) ^ (t & 7)) << 4)) =
+                                    make_uint4(o[0], o[1], o[2], o[3]);
+                            }
+                        }
+                    }
+                    tc_fence_before_sync();
+                    warp_arrive(sy, B_GFREE);
+                    fence_async_smem();
+                    warp_arrive(sy, half ? B_M1 : B_M0);
+                }
+                if (!ok) break;
+                warp_arrive(sy, B_EMPTY + s);
+            }
+        }
+    } else if (warp < 8) {
+        // ---- the state, and the parts of w o x: lane = column pcol of x ----
+        const int wq = warp - 4, pcol = wq * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const bool live = pcol < P;  // uniform in a warp
+        const int slot = p.states ? seq_slot(p.q, un.s) : -1;
+        float* pool = p.states + (static_cast<int64_t>(slot) * p.n_heads + h) * N * P + pcol;
+        if (live) {
+            // the state before the segment
+            const bool from_ws = OUT && un.n_seg > 1;
+            const bool old = !from_ws && un.k == 0 && slot >= 0 && seq_has_state(p.q, un.s);
+            const int64_t unit_floats = static_cast<int64_t>(p.n_heads) * N * P;
+            float* first = p.ws + ((u - un.k) * p.n_heads + h) * N * P + pcol;  // segment 0's contribution
+            float* kept = first + (un.n_seg - 1) * unit_floats;  // the state before the sequence, left by PASS 1
+#pragma unroll 1
+            for (int n0 = 0; n0 < N; n0 += 32) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                if (old) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = pool[static_cast<int64_t>(n0 + i) * P];
+                } else if (from_ws && un.k == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = kept[static_cast<int64_t>(n0 + i) * P];
+                } else if (from_ws) {
+                    float keep = 1.f;
+                    for (int k = un.k - 1; k >= 0; --k) {
+                        const float* src = first + k * unit_floats;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(keep, src[static_cast<int64_t>(n0 + i) * P], v[i]);
+                        keep *= p.ws_decay[(u - un.k + k) * p.n_heads + h];
+                    }
+                }
+                if (PASS == 1 && un.k == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) kept[static_cast<int64_t>(n0 + i) * P] = v[i];
+                }
+                tmem_st32(tm + lanes + TM_H + n0, v);
+            }
+            tmem_wait_st();
+        }
+        const int c8 = (pcol & 63) >> 3;
+        uint32_t xoff[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xoff[j] = (pcol >> 6) * kBox + j * 128 + ((c8 ^ j) << 4) + (pcol & 7) * 2;
+        uint32_t qi = 0;
+        bool ok = true;
+        float scale = 1.f;  // tensor memory holds H / scale
+        for (int c = 0; ok && c < nch; ++c) {
+            const int s = c % kStages;
+            unsigned char* st = sm + s * SM_STAGE;
+            const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
+            if (!wait_phase(sy, B_GATE + s, c / kStages)) break;
+            if (!wait_phase(sy, B_FULL + s, c / kStages)) break;
+            const int nv = un.len - c * L;
+            if (nv < L) {
+                // rows behind the segment's end (another sequence's, which may hold anything) become
+                // zeros in x and B, the operands whose rows are summed over
+                for (int i = tid - 128; i < (L - nv) * 8; i += 128) {
+                    const uint32_t off = (nv + i / 8) * 128 + (i % 8) * 16;
+#pragma unroll
+                    for (int k = 0; k < PB; ++k) *reinterpret_cast<uint4*>(st + SM_X + k * kBox + off) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) *reinterpret_cast<uint4*>(st + SM_B + k * kBox + off) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                warp_arrive(sy, B_TAIL);
+                if (!wait_phase(sy, B_TAIL, 0)) break;
+            }
+            if (c > 0 && !wait_phase(sy, B_S, c - 1)) break;
+            tc_fence_after_sync();
+            const float next_scale = BF16 ? 1.f : gt[512];
+            if (live) {
+                const float keep = gt[384 + L - 1] * (scale * (1.0f / next_scale));
+#pragma unroll 1
+                for (int n0 = 0; n0 < N; n0 += 32) {
+                    float v[32];
+                    tmem_ld32(tm + lanes + TM_H + n0, v);
+                    if constexpr (OUT) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = BF16 ? pack2<BF16>(v[2 * i], v[2 * i + 1]) : pack2<BF16>(v[2 * i] * scale, v[2 * i + 1] * scale);
+                        tmem_st_u16(tm + lanes + TM_HB + n0 / 2, o);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= keep;
+                    tmem_st32(tm + lanes + TM_H + n0, v);
+                }
+                tmem_wait_st();
+            }
+            scale = next_scale;
+            tc_fence_before_sync();
+            warp_arrive(sy, B_H);
+#pragma unroll 1
+            for (int j = 0; j < L / 16; ++j, ++qi) {
+                const int xs = qi % SLOTS;
+                if (qi >= SLOTS && !wait_phase(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                if (live) {
+                    const unsigned char* x = st + SM_X + j * 2048;
+                    const float4* w4 = reinterpret_cast<const float4*>(gt + 256 + 16 * j);
+                    uint32_t part[PARTS][8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 w = w4[i];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int r = 4 * i + 2 * k;  // rows r, r + 1 of the block
+                            const uint16_t u0 = *reinterpret_cast<const uint16_t*>(x + (r >> 3) * 1024 + xoff[r & 7]);
+                            const uint16_t u1 = *reinterpret_cast<const uint16_t*>(x + (r >> 3) * 1024 + xoff[(r + 1) & 7]);
+                            float f0 = unpack1<BF16>(u0) * (k ? w.z : w.x), f1 = unpack1<BF16>(u1) * (k ? w.w : w.y);
+#pragma unroll
+                            for (int q = 0; q < PARTS; ++q) {
+                                const uint32_t o = pack2<BF16>(f0, f1);
+                                part[q][2 * i + k] = o;
+                                const float2 back = unpack2<BF16>(o);
+                                f0 -= back.x;
+                                f1 -= back.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q) tmem_st_u8(tm + lanes + TM_XW + (xs * PARTS + q) * 8, part[q]);
+                    tmem_wait_st();
+                }
+                tc_fence_before_sync();
+                warp_arrive(sy, B_XW + xs);
+            }
+            if (!ok) break;
+            warp_arrive(sy, B_EMPTY + s);
+        }
+        // the state behind the segment
+        const bool keep_it = PASS == 1 || (slot >= 0 && un.k == un.n_seg - 1);
+        if (ok && !*abort_flag && keep_it && wait_phase(sy, B_S, nch - 1)) {
+            tc_fence_after_sync();
+            float* dst = PASS == 1 ? p.ws + (u * p.n_heads + h) * N * P + pcol : pool;
+            if (live) {
+#pragma unroll 1
+                for (int n0 = 0; n0 < N; n0 += 32) {
+                    float v[32];
+                    tmem_ld32(tm + lanes + TM_H + n0, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(n0 + i) * P] = v[i] * scale;
+                }
+            }
+        }
+        tc_fence_before_sync();
+    } else if (warp < 12) {
+        if constexpr (OUT) {
+            // ---- the output: lane = column pcol of x ----
+            const int wq = warp - 8, pcol = wq * 32 + lane;
+            const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+            const bool live = pcol < P;
+            const float D = p.D ? __ldg(p.D + h) : 0.f;
+            const T* zp = p.z ? static_cast<const T*>(p.z) + un.begin * p.z_stride + static_cast<int64_t>(h) * P + pcol : nullptr;
+            T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + static_cast<int64_t>(h) * P + pcol;
+            const int c8 = (pcol & 63) >> 3;
+            uint32_t xoff[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) xoff[j] = (pcol >> 6) * kBox + j * 128 + ((c8 ^ j) << 4) + (pcol & 7) * 2;
+            uint32_t yi = 0;
+            bool ok = true;
+            for (int c = 0; ok && c < nch; ++c) {
+                const int s = c % kStages;
+                const unsigned char* x = sm + s * SM_STAGE + SM_X;
+                const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
+                if (!wait_phase(sy, B_GATE + s, c / kStages) || !wait_phase(sy, B_FULL + s, c / kStages)) break;
+                const int nv = un.len - c * L;
+                const float m_scale = BF16 ? 1.f : eg[513 - 384];
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half, ++yi) {
+                    if (!wait_phase(sy, B_Y1, yi)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int cb = 0; cb < 4; ++cb) {
+                        const int t0 = 64 * half + 16 * cb;
+                        if (live && t0 < nv) {
+                            uint16_t zv[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                zv[j] = zp && t0 + j < nv
+                                            ? __ldcs(reinterpret_cast<const unsigned short*>(zp + static_cast<int64_t>(c * L + t0 + j) * p.z_stride))
+                                            : 0;
+                            float y1[16], y2[16];
+                            tmem_ld16x2(tm + lanes + TM_Y1 + 16 * cb, tm + lanes + TM_Y2 + t0, y1, y2);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float xv = unpack1<BF16>(
+                                    *reinterpret_cast<const uint16_t*>(x + ((t0 + j) >> 3) * 1024 + xoff[j & 7]));
+                                float o = fmaf(D, xv, fmaf(eg[t0 + j], y2[j], BF16 ? y1[j] : y1[j] * m_scale));
+                                if (zp) o *= ssm_silu(unpack1<BF16>(zv[j]));
+                                if (t0 + j < nv) yp[static_cast<int64_t>(c * L + t0 + j) * p.y_stride] = from_f<T>(o);
+                            }
+                        }
+                    }
+                    tc_fence_before_sync();
+                    warp_arrive(sy, B_Y1FREE);
+                }
+                if (!ok) break;
+                warp_arrive(sy, B_Y2FREE);
+                warp_arrive(sy, B_EMPTY + s);
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tm, TM_COLS);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+bool make_map16(CUtensorMap* m, bool bf16, const void* base, int64_t width, int64_t rows, int64_t stride) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, L}, one[2] = {1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
+               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int P, int N>
+cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
+    constexpr int bytes = SM_TOTAL + 1024;
+    const unsigned grid = static_cast<unsigned>(units * p.n_heads);
+    cudaError_t e;
+    if (p.ws) {
+        e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 1>), bytes);
+        if (e != cudaSuccess) return e;
+        ssm_scan_tc_kernel<BF16, P, N, 1><<<grid, kThreadsTc, bytes, s>>>(p);
+        internal_count_launch();
+    }
+    e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 0>), bytes);
+    if (e != cudaSuccess) return e;
+    ssm_scan_tc_kernel<BF16, P, N, 0><<<grid, kThreadsTc, bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_b(const TcParams& p, int head_dim, int state_dim, int64_t units, cudaStream_t s) {
+    if (head_dim == 128)
+        return state_dim == 128 ? launch_pn<BF16, 128, 128>(p, units, s) : launch_pn<BF16, 128, 64>(p, units, s);
+    return state_dim == 128 ? launch_pn<BF16, 64, 128>(p, units, s) : launch_pn<BF16, 64, 64>(p, units, s);
+}
+
+std::atomic<bool> g_used[64];  // devices on which the tensor form has run
+
+}  // namespace
+
+// Segments: with H heads, SMs / H segments of all tokens together fill the device; a
+// segment is at least that share of the call's chunks (and an eighth of them, so that a
+// segment sums at most 7 others).
+int64_t ssm_scan_segment(int64_t T, int n_heads, int sm_count) {
+    const int64_t chunks = (T + L - 1) / L;
+    int64_t parts = sm_count / n_heads;
+    if (parts > 8) parts = 8;
+    if (parts < 1) parts = 1;
+    return (chunks + parts - 1) / parts * L;
+}
+
+bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq) {
+    return dtype != GDN_F32 && (head_dim == 64 || head_dim == 128) && (state_dim == 64 || state_dim == 128) &&
+           T >= int64_t{kSsmTcMinTokens} * n_seq;
+}
+
+size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count) {
+    const int64_t seg = ssm_scan_segment(T, n_heads, sm_count);
+    if (seg >= T) return 0;
+    const size_t units = static_cast<size_t>(T / seg) + n_seq;
+    return units * n_heads * (static_cast<size_t>(head_dim) * state_dim + 4) * sizeof(float);
+}
+
+cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_count, cudaStream_t s) {
+    const bool bf16 = p.dtype == GDN_BF16;
+    TcParams t{};
+    if (!make_map16(&t.tm_x, bf16, p.x, static_cast<int64_t>(p.n_heads) * p.head_dim, p.T, p.x_stride) ||
+        !make_map16(&t.tm_b, bf16, p.B, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.b_stride) ||
+        !make_map16(&t.tm_c, bf16, p.C, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.c_stride))
+        return cudaErrorInvalidValue;
+    const int64_t seg = ssm_scan_segment(p.T, p.n_heads, sm_count);
+    const int64_t units = p.T / seg + p.n_seq;
+    t.a = p.a; t.z = p.z; t.y = p.y;
+    t.a_stride = p.a_stride; t.z_stride = p.z_stride; t.y_stride = p.y_stride;
+    t.A_log = p.A_log; t.dt_bias = p.dt_bias; t.D = p.D;
+    t.states = p.states;
+    if (seg < p.T) {
+        t.ws = static_cast<float*>(workspace);
+        t.ws_decay = t.ws + static_cast<size_t>(units) * p.n_heads * p.head_dim * p.state_dim;
+    }
+    t.q = SsmSeqs{p.cu, p.slots, p.has_state, p.n_seq, p.n_slots, p.T};
+    t.units = units;
+    t.seg = static_cast<int>(seg);
+    t.n_heads = p.n_heads;
+    t.n_groups = p.n_groups;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) g_used[dev].store(true);
+    return bf16 ? launch_b<true>(t, p.head_dim, p.state_dim, units, s) : launch_b<false>(t, p.head_dim, p.state_dim, units, s);
+}
+
+cudaError_t ssm_take_status(int device, int* word) {
+    *word = 0;
+    if (device < 0 || device >= 64 || !g_used[device].load()) return cudaSuccess;
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_ssm_status, sizeof(int));
+    const int zero = 0;
+    if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbol(g_ssm_status, &zero, sizeof(int));
+    return e;
+}
+
+}  // namespace gdn
