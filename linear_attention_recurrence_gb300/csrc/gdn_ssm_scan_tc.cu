@@ -170,6 +170,16 @@ __device__ __forceinline__ float range_scale(float v) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// Arrivals that complete a phase of barrier b: one where a copy, a commit or the gate warp
+// arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
+// reads it are done.
+__device__ constexpr int arrivals(int b, bool out) {
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 13 : 5;
+    if (b == B_GFREE || b == B_M0 || b == B_M1 || b == B_H || b == B_Y1FREE || b == B_Y2FREE || b == B_TAIL) return 4;
+    if (b >= B_XW && b < B_XWFREE) return 4;
+    return 1;
+}
+
 struct Sync {
     uint64_t* bar;
     volatile int* abort_flag;
@@ -183,6 +193,11 @@ __device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
     *s.abort_flag = 1;
     report_timeout(&g_ssm_status);
     return false;
+}
+// The same for a whole warp: all lanes leave together, with one answer (the tensor-memory
+// instructions behind a wait need a converged warp).
+__device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
+    return __all_sync(0xffffffffu, wait_phase(s, b, n)) != 0;
 }
 // One arrival for the calling warp.
 __device__ __forceinline__ void warp_arrive(const Sync& s, int b) {
@@ -263,19 +278,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     const int nch = (un.len + L - 1) / L;
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bar[B_FULL + s], 1);
-            mbar_init(&bar[B_GATE + s], 1);
-            mbar_init(&bar[B_EMPTY + s], OUT ? 13 : 5);
-        }
-        const int one[] = {B_G, B_MFREE, B_S, B_Y1, B_FIN};
-        for (int b : one) mbar_init(&bar[b], 1);
-        const int four[] = {B_TAIL, B_GFREE, B_M0, B_M1, B_H, B_Y1FREE, B_Y2FREE};
-        for (int b : four) mbar_init(&bar[b], 4);
-        for (int s = 0; s < SLOTS; ++s) {
-            mbar_init(&bar[B_XW + s], 4);
-            mbar_init(&bar[B_XWFREE + s], 1);
-        }
+#pragma unroll
+        for (int b = 0; b < NBAR; ++b) mbar_init(&bar[b], arrivals(b, OUT));
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const int t = c * L + 4 * lane + i;
                 v[i] = t < un.len ? to_f<T>(a[t * p.a_stride]) : 0.f;
             }
-            if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+            if (c >= kStages && !wait_warp(sy, B_EMPTY + s, c / kStages - 1)) break;
             float dt[4], g2[4], pre[4], suf[4];
             float sum = 0.f;
 #pragma unroll
@@ -474,13 +478,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             uint32_t gi = 0;
             for (int c = 0; c < nch; ++c) {
                 const int s = c % kStages;
-                if (!wait_phase(sy, B_GATE + s, c / kStages)) break;
+                if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
                 const float2* gd = reinterpret_cast<const float2*>(sm + SM_GATE + s * SM_GATE_STAGE);
                 const float gt = gd[t].x;
                 bool ok = true;
 #pragma unroll
                 for (int half = 0; half < 2; ++half, ++gi) {
-                    if (!wait_phase(sy, B_G, gi) || (half == 0 && c > 0 && !wait_phase(sy, B_MFREE, c - 1))) {
+                    if (!wait_warp(sy, B_G, gi) || (half == 0 && c > 0 && !wait_warp(sy, B_MFREE, c - 1))) {
                         ok = false;
                         break;
                     }
@@ -574,8 +578,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             const int s = c % kStages;
             unsigned char* st = sm + s * SM_STAGE;
             const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
-            if (!wait_phase(sy, B_GATE + s, c / kStages)) break;
-            if (!wait_phase(sy, B_FULL + s, c / kStages)) break;
+            if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
+            if (!wait_warp(sy, B_FULL + s, c / kStages)) break;
             const int nv = un.len - c * L;
             if (nv < L) {
                 // rows behind the segment's end (another sequence's, which may hold anything) become
@@ -589,9 +593,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
                 fence_async_smem();
                 warp_arrive(sy, B_TAIL);
-                if (!wait_phase(sy, B_TAIL, 0)) break;
+                if (!wait_warp(sy, B_TAIL, 0)) break;
             }
-            if (c > 0 && !wait_phase(sy, B_S, c - 1)) break;
+            if (c > 0 && !wait_warp(sy, B_S, c - 1)) break;
             tc_fence_after_sync();
             const float next_scale = BF16 ? 1.f : gt[512];
             if (live) {
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 #pragma unroll 1
             for (int j = 0; j < L / 16; ++j, ++qi) {
                 const int xs = qi % SLOTS;
-                if (qi >= SLOTS && !wait_phase(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
+                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
                     ok = false;
                     break;
                 }
@@ -659,7 +663,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         }
         // the state behind the segment
         const bool keep_it = PASS == 1 || (slot >= 0 && un.k == un.n_seg - 1);
-        if (ok && !*abort_flag && keep_it && wait_phase(sy, B_S, nch - 1)) {
+        if (ok && keep_it && wait_warp(sy, B_S, nch - 1)) {
             tc_fence_after_sync();
             float* dst = PASS == 1 ? p.ws + (u * p.n_heads + h) * N * P + pcol : pool;
             if (live) {
@@ -692,40 +696,60 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const int s = c % kStages;
                 const unsigned char* x = sm + s * SM_STAGE + SM_X;
                 const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
-                if (!wait_phase(sy, B_GATE + s, c / kStages) || !wait_phase(sy, B_FULL + s, c / kStages)) break;
+                if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_FULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half, ++yi) {
-                    if (!wait_phase(sy, B_Y1, yi)) {
-                        ok = false;
-                        break;
+                const T* zr = zp + static_cast<int64_t>(c) * L * p.z_stride;
+                auto load_z = [&](int t0, uint16_t (&zv)[16]) {
+                    if (!zp || !live || t0 >= nv) return;
+                    if (t0 + 16 <= nv) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (t0 + j) * p.z_stride));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (t0 + j < nv ? t0 + j : nv - 1) * p.z_stride));
                     }
-                    tc_fence_after_sync();
+                };
+                uint16_t zv[16];
+                load_z(0, zv);
 #pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
-                        const int t0 = 64 * half + 16 * cb;
-                        if (live && t0 < nv) {
-                            uint16_t zv[16];
+                for (int cb = 0; cb < 8; ++cb) {
+                    const int t0 = 16 * cb;
+                    if ((cb & 3) == 0) ok = wait_warp(sy, B_Y1, yi++);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    uint16_t zn[16];
+                    if (cb < 7) load_z(t0 + 16, zn);
+                    if (live && t0 < nv) {
+                        float o[16], y2[16];
+                        tmem_ld16x2(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, o, y2);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float xv = unpack1<BF16>(
+                                *reinterpret_cast<const uint16_t*>(x + ((t0 + j) >> 3) * 1024 + xoff[j & 7]));
+                            o[j] = fmaf(D, xv, fmaf(eg[t0 + j], y2[j], BF16 ? o[j] : o[j] * m_scale));
+                        }
+                        if (zp) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] *= ssm_silu(unpack1<BF16>(zv[j]));
+                        }
+                        T* yr = yp + static_cast<int64_t>(c * L + t0) * p.y_stride;
+                        if (t0 + 16 <= nv) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) yr[j * p.y_stride] = from_f<T>(o[j]);
+                        } else {
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                zv[j] = zp && t0 + j < nv
-                                            ? __ldcs(reinterpret_cast<const unsigned short*>(zp + static_cast<int64_t>(c * L + t0 + j) * p.z_stride))
-                                            : 0;
-                            float y1[16], y2[16];
-                            tmem_ld16x2(tm + lanes + TM_Y1 + 16 * cb, tm + lanes + TM_Y2 + t0, y1, y2);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float xv = unpack1<BF16>(
-                                    *reinterpret_cast<const uint16_t*>(x + ((t0 + j) >> 3) * 1024 + xoff[j & 7]));
-                                float o = fmaf(D, xv, fmaf(eg[t0 + j], y2[j], BF16 ? y1[j] : y1[j] * m_scale));
-                                if (zp) o *= ssm_silu(unpack1<BF16>(zv[j]));
-                                if (t0 + j < nv) yp[static_cast<int64_t>(c * L + t0 + j) * p.y_stride] = from_f<T>(o);
-                            }
+                                if (t0 + j < nv) yr[j * p.y_stride] = from_f<T>(o[j]);
                         }
                     }
-                    tc_fence_before_sync();
-                    warp_arrive(sy, B_Y1FREE);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) zv[j] = zn[j];
+                    if ((cb & 3) == 3) {
+                        tc_fence_before_sync();
+                        warp_arrive(sy, B_Y1FREE);
+                    }
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_Y2FREE);
@@ -735,6 +759,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     }
     tc_fence_before_sync();
     __syncthreads();
+    __syncwarp();
     if (warp == kMmaWarp) tmem_dealloc(tm, TM_COLS);
 }
 
