@@ -79,6 +79,7 @@ __device__ int g_ssm_status;  // bits of kDevErr*
 
 struct TcParams {
     CUtensorMap tm_x, tm_b, tm_c;  // [T][n_heads head_dim], [T][n_groups state_dim] twice; box 64 x 128
+    CUtensorMap tm_z;              // as tm_x
     const void *a, *z;
     void* y;
     int64_t a_stride, z_stride, y_stride;
@@ -134,6 +135,12 @@ __device__ __forceinline__ void tmem_st_u16(uint32_t taddr, const uint32_t (&v)[
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// Has box (x, y) fetched into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
 }
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -306,6 +313,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 #pragma unroll
                 for (int i = 0; i < PB; ++i)
                     tma_load_2d(st + SM_X + i * kBox, &p.tm_x, &bar[B_FULL + s], h * P + 64 * i, row);
+                if (OUT && p.z) {
+#pragma unroll
+                    for (int i = 0; i < PB; ++i) tma_prefetch_2d(&p.tm_z, h * P + 64 * i, row);
+                }
             }
             // the copies in flight land before the CTA ends, also after a wait that gave up
             for (int i = c > kStages ? c - kStages : 0; i < c; ++i)
@@ -690,6 +701,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             uint32_t xoff[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) xoff[j] = (pcol >> 6) * kBox + j * 128 + ((c8 ^ j) << 4) + (pcol & 7) * 2;
+            // z of the segment's rows t .. t + 15, two blocks ahead of their use (each row comes from
+            // L2, where the copy warp has it fetched with the chunk's other operands)
+            auto load_z = [&](int t, uint16_t (&zv)[16]) {
+                if (!zp || !live || t >= un.len) return;
+                const T* zr = zp + static_cast<int64_t>(t) * p.z_stride;
+                const int last = un.len - 1 - t;
+                if (last >= 15) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + j * p.z_stride));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (j < last ? j : last) * p.z_stride));
+                }
+            };
+            uint16_t z0[16], z1[16];
+            load_z(0, z0);
+            load_z(16, z1);
             uint32_t yi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
@@ -699,28 +728,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_FULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
-                const T* zr = zp + static_cast<int64_t>(c) * L * p.z_stride;
-                auto load_z = [&](int t0, uint16_t (&zv)[16]) {
-                    if (!zp || !live || t0 >= nv) return;
-                    if (t0 + 16 <= nv) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (t0 + j) * p.z_stride));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (t0 + j < nv ? t0 + j : nv - 1) * p.z_stride));
-                    }
-                };
-                uint16_t zv[16];
-                load_z(0, zv);
-#pragma unroll 1
-                for (int cb = 0; cb < 8; ++cb) {
-                    const int t0 = 16 * cb;
-                    if ((cb & 3) == 0) ok = wait_warp(sy, B_Y1, yi++);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    uint16_t zn[16];
-                    if (cb < 7) load_z(t0 + 16, zn);
+                // one block of 16 tokens: y from the two products, x and z (in zv), which then receives
+                // the block after the next one's
+                auto block = [&](int t0, uint16_t (&zv)[16]) {
                     if (live && t0 < nv) {
                         float o[16], y2[16];
                         tmem_ld16x2(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, o, y2);
@@ -744,9 +754,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 if (t0 + j < nv) yr[j * p.y_stride] = from_f<T>(o[j]);
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) zv[j] = zn[j];
-                    if ((cb & 3) == 3) {
+                    load_z(c * L + t0 + 32, zv);
+                };
+#pragma unroll 1
+                for (int t0 = 0; t0 < L; t0 += 32) {
+                    if ((t0 & 63) == 0) ok = wait_warp(sy, B_Y1, yi++);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    block(t0, z0);
+                    block(t0 + 16, z1);
+                    if ((t0 & 63) == 32) {
                         tc_fence_before_sync();
                         warp_arrive(sy, B_Y1FREE);
                     }
@@ -842,7 +859,8 @@ cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_c
     TcParams t{};
     if (!make_map16(&t.tm_x, bf16, p.x, static_cast<int64_t>(p.n_heads) * p.head_dim, p.T, p.x_stride) ||
         !make_map16(&t.tm_b, bf16, p.B, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.b_stride) ||
-        !make_map16(&t.tm_c, bf16, p.C, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.c_stride))
+        !make_map16(&t.tm_c, bf16, p.C, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.c_stride) ||
+        (p.z && !make_map16(&t.tm_z, bf16, p.z, static_cast<int64_t>(p.n_heads) * p.head_dim, p.T, p.z_stride)))
         return cudaErrorInvalidValue;
     const int64_t seg = ssm_scan_segment(p.T, p.n_heads, sm_count);
     const int64_t units = p.T / seg + p.n_seq;
