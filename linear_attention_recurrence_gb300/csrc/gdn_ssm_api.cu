@@ -187,7 +187,7 @@ int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_strid
     cudaError_t err;
     if (ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) && tma_rows(x, x_stride, xw) &&
         tma_rows(B, b_stride, bw) && tma_rows(C, c_stride, bw) &&
-        (!z || tma_rows(z, z_stride, xw))) {
+        (!z || tma_rows(z, z_stride, xw)) && tma_rows(y, y_stride, xw)) {
         int sms = 0;
         if (int rc = sm_count(&sms)) return rc;
         err = launch_ssm_scan_tc(p, workspace, sms, static_cast<cudaStream_t>(cuda_stream));

@@ -60,7 +60,8 @@ constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kB
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: (gamma, dt)[128] at 0, w[128] at
 constexpr uint32_t SM_GATE_STAGE = 2176;                // 256, e^gamma[128] at 384, 2^k of w and 2^j of dt at 512
-constexpr uint32_t SM_MISC = SM_GATE + kStages * SM_GATE_STAGE;
+constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 1 KB: 16 tokens x 32 columns
+constexpr uint32_t SM_MISC = SM_IO + 4 * 1024;
 constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
@@ -136,6 +137,50 @@ __device__ __forceinline__ void tmem_st_u16(uint32_t taddr, const uint32_t (&v)[
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// Fragments of a 16 x 16 tile, rows = columns of x (or lanes of tensor memory), columns =
+// tokens: register k of the four holds tokens 8 (k >> 1) + 2 (lane & 3), + 1 of row
+// (lane >> 2) + 8 (k & 1), 16 bits each (ldmatrix and stmatrix, transposed: in memory the
+// rows are tokens); the FP32 loads give the same pairs in register pairs 2k, 2k + 1.
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// Two FP32 tiles (16 lanes x 16 columns each) of each of two accumulators, one wait.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t b, float (&va)[2][8], float (&vb)[2][8]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+          "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
+          "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31])
+        : "r"(a), "r"(a + (16u << 16)), "r"(b), "r"(b + (16u << 16))
+        : "memory");
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            va[g][i] = __uint_as_float(r[8 * g + i]);
+            vb[g][i] = __uint_as_float(r[16 + 8 * g + i]);
+        }
+}
+// A 16-bit tile (16 lanes x 16 tokens) to 8 columns of tensor memory.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
 // Has box (x, y) fetched into L2.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
@@ -146,6 +191,22 @@ __device__ __forceinline__ float ex2(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    return upk(r);
+}
+// silu of both: z / (1 + 2^(-z log2 e)); an infinite divisor gives 0
+__device__ __forceinline__ float2 silu2(float2 z) {
+    const float2 m = fmul2(z, make_float2(-kLog2e, -kLog2e));
+    const float2 d = fadd2(make_float2(ex2(m.x), ex2(m.y)), make_float2(1.f, 1.f));
+    return fmul2(z, make_float2(rcp(d.x), rcp(d.y)));
 }
 
 // ---- pairs of the 16-bit types ----
@@ -210,6 +271,13 @@ __device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
 __device__ __forceinline__ void warp_arrive(const Sync& s, int b) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&s.bar[b]);
+}
+
+// Where a lane's row of ldmatrix tile (lane >> 3) of the 16 columns from p0 and tokens 0-15
+// lies in an x tile: token 8 (tile >> 1) + (lane & 7), columns p0 + 8 (tile & 1) .. + 7.
+__device__ __forceinline__ uint32_t frag_offset(int p0, int lane) {
+    const int p = p0 + 8 * ((lane >> 3) & 1), r = lane & 7;
+    return (p >> 6) * kBox + (8 * (lane >> 4) + r) * 128 + ((((p & 63) >> 3) ^ r) << 4);
 }
 
 // The unit (sequence, segment) of a CTA, found by its sequences' segment counts.
@@ -540,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         // ---- the state, and the parts of w o x: lane = column pcol of x ----
         const int wq = warp - 4, pcol = wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const bool live = pcol < P;  // uniform in a warp
+        const bool live = wq * 32 < P;
         const int slot = p.states ? seq_slot(p.q, un.s) : -1;
         float* pool = p.states + (static_cast<int64_t>(slot) * p.n_heads + h) * N * P + pcol;
         if (live) {
@@ -578,10 +646,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
             tmem_wait_st();
         }
-        const int c8 = (pcol & 63) >> 3;
-        uint32_t xoff[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xoff[j] = (pcol >> 6) * kBox + j * 128 + ((c8 ^ j) << 4) + (pcol & 7) * 2;
+        const uint32_t x_frag = frag_offset(wq * 32, lane), x_frag1 = frag_offset(wq * 32 + 16, lane);
         uint32_t qi = 0;
         bool ok = true;
         float scale = 1.f;  // tensor memory holds H / scale
@@ -640,30 +705,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
                 tc_fence_after_sync();
                 if (live) {
-                    const unsigned char* x = st + SM_X + j * 2048;
-                    const float4* w4 = reinterpret_cast<const float4*>(gt + 256 + 16 * j);
-                    uint32_t part[PARTS][8];
+                    const uint32_t x = smem_addr(st) + SM_X + j * 2048;
+                    const float2 w0 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 2 * (lane & 3));
+                    const float2 w1 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 8 + 2 * (lane & 3));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 w = w4[i];
+                    for (int g2 = 0; g2 < 2; ++g2) {
+                        uint32_t xr[4], part[PARTS][4];
+                        ldsm4t(x + (g2 ? x_frag1 : x_frag), xr);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int r = 4 * i + 2 * k;  // rows r, r + 1 of the block
-                            const uint16_t u0 = *reinterpret_cast<const uint16_t*>(x + (r >> 3) * 1024 + xoff[r & 7]);
-                            const uint16_t u1 = *reinterpret_cast<const uint16_t*>(x + (r >> 3) * 1024 + xoff[(r + 1) & 7]);
-                            float f0 = unpack1<BF16>(u0) * (k ? w.z : w.x), f1 = unpack1<BF16>(u1) * (k ? w.w : w.y);
+                        for (int k = 0; k < 4; ++k) {
+                            float2 f = fmul2(unpack2<BF16>(xr[k]), k < 2 ? w0 : w1);
 #pragma unroll
                             for (int q = 0; q < PARTS; ++q) {
-                                const uint32_t o = pack2<BF16>(f0, f1);
-                                part[q][2 * i + k] = o;
-                                const float2 back = unpack2<BF16>(o);
-                                f0 -= back.x;
-                                f1 -= back.y;
+                                part[q][k] = pack2<BF16>(f.x, f.y);
+                                const float2 back = unpack2<BF16>(part[q][k]);
+                                f = fadd2(f, make_float2(-back.x, -back.y));
                             }
                         }
-                    }
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q) tmem_st_u8(tm + lanes + TM_XW + (xs * PARTS + q) * 8, part[q]);
+                        for (int q = 0; q < PARTS; ++q)
+                            tmem_st_frag(tm + lanes + (g2 << 20) + TM_XW + (xs * PARTS + q) * 8, part[q]);
+                    }
                     tmem_wait_st();
                 }
                 tc_fence_before_sync();
@@ -690,69 +752,94 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         tc_fence_before_sync();
     } else if (warp < 12) {
         if constexpr (OUT) {
-            // ---- the output: lane = column pcol of x ----
-            const int wq = warp - 8, pcol = wq * 32 + lane;
+            // ---- the output: this warp's 32 columns of x ----
+            const int wq = warp - 8;
             const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-            const bool live = pcol < P;
+            const bool live = wq * 32 < P;
             const float D = p.D ? __ldg(p.D + h) : 0.f;
-            const T* zp = p.z ? static_cast<const T*>(p.z) + un.begin * p.z_stride + static_cast<int64_t>(h) * P + pcol : nullptr;
-            T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + static_cast<int64_t>(h) * P + pcol;
-            const int c8 = (pcol & 63) >> 3;
-            uint32_t xoff[8];
+            const bool gated = p.z != nullptr;
+            const uint32_t x_frag = frag_offset(wq * 32, lane), x_frag1 = frag_offset(wq * 32 + 16, lane);
+            // The warp's buffer holds 16 tokens x 32 columns, 64 bytes a token, 16-byte pieces swizzled.
+            // Global memory is read and written in pieces: this lane's are piece lane & 3 of tokens
+            // lane >> 2 and that + 8.
+            const uint32_t io = smem_addr(sm) + SM_IO + wq * 1024;
+            auto piece = [](int t, int c) { return static_cast<uint32_t>(t * 64 + ((c ^ ((t >> 1) & 3)) << 4)); };
+            const int pt = lane >> 2;
+            const uint32_t io_piece = io + piece(pt, lane & 3);  // (token + 8: 512 bytes on, the same swizzle)
+            const uint32_t io_frag = io + piece(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
+            const uint32_t io_frag1 = io + piece(8 * (lane >> 4) + (lane & 7), 2 + ((lane >> 3) & 1));
+            const int64_t col = static_cast<int64_t>(h) * P + wq * 32 + 8 * (lane & 3);
+            const T* zp = gated ? static_cast<const T*>(p.z) + un.begin * p.z_stride + col : nullptr;
+            T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + col;
+            // z of the segment's rows t .. t + 15, two blocks ahead of their use (from L2, where the copy
+            // warp has it fetched with the chunk's other operands)
+            auto load_z = [&](int t, uint4 (&zv)[2]) {
+                if (!gated || !live || t >= un.len) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xoff[j] = (pcol >> 6) * kBox + j * 128 + ((c8 ^ j) << 4) + (pcol & 7) * 2;
-            // z of the segment's rows t .. t + 15, two blocks ahead of their use (each row comes from
-            // L2, where the copy warp has it fetched with the chunk's other operands)
-            auto load_z = [&](int t, uint16_t (&zv)[16]) {
-                if (!zp || !live || t >= un.len) return;
-                const T* zr = zp + static_cast<int64_t>(t) * p.z_stride;
-                const int last = un.len - 1 - t;
-                if (last >= 15) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + j * p.z_stride));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        zv[j] = __ldcs(reinterpret_cast<const unsigned short*>(zr + (j < last ? j : last) * p.z_stride));
+                for (int i = 0; i < 2; ++i) {
+                    const int row = t + pt + 8 * i < un.len ? t + pt + 8 * i : un.len - 1;
+                    zv[i] = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
                 }
             };
-            uint16_t z0[16], z1[16];
+            uint4 z0[2], z1[2];
             load_z(0, z0);
             load_z(16, z1);
             uint32_t yi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
-                const unsigned char* x = sm + s * SM_STAGE + SM_X;
+                const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X;
                 const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
                 if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_FULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
                 // one block of 16 tokens: y from the two products, x and z (in zv), which then receives
                 // the block after the next one's
-                auto block = [&](int t0, uint16_t (&zv)[16]) {
+                auto block = [&](int t0, uint4 (&zv)[2]) {
                     if (live && t0 < nv) {
-                        float o[16], y2[16];
-                        tmem_ld16x2(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, o, y2);
+                        uint32_t zr[2][4];
+                        if (gated) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float xv = unpack1<BF16>(
-                                *reinterpret_cast<const uint16_t*>(x + ((t0 + j) >> 3) * 1024 + xoff[j & 7]));
-                            o[j] = fmaf(D, xv, fmaf(eg[t0 + j], y2[j], BF16 ? o[j] : o[j] * m_scale));
+                            for (int i = 0; i < 2; ++i)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece + 512 * i), "r"(zv[i].x),
+                                             "r"(zv[i].y), "r"(zv[i].z), "r"(zv[i].w)
+                                             : "memory");
+                            __syncwarp();
+                            ldsm4t(io_frag, zr[0]);
+                            ldsm4t(io_frag1, zr[1]);
                         }
-                        if (zp) {
+                        float y1[2][8], y2[2][8];
+                        tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
+                        const float2 e0 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
+                        const float2 e1 = *reinterpret_cast<const float2*>(eg + t0 + 8 + 2 * (lane & 3));
+                        __syncwarp();  // z is read: the buffer takes y
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] *= ssm_silu(unpack1<BF16>(zv[j]));
+                        for (int g2 = 0; g2 < 2; ++g2) {
+                            uint32_t xr[4], yr[4];
+                            ldsm4t(x + t0 * 128 + (g2 ? x_frag1 : x_frag), xr);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float2 o = make_float2(y1[g2][2 * k], y1[g2][2 * k + 1]);
+                                if constexpr (!BF16) o = fmul2(o, make_float2(m_scale, m_scale));
+                                o = ffma2(k < 2 ? e0 : e1, make_float2(y2[g2][2 * k], y2[g2][2 * k + 1]), o);
+                                o = ffma2(make_float2(D, D), unpack2<BF16>(xr[k]), o);
+                                if (gated) o = fmul2(o, silu2(unpack2<BF16>(zr[g2][k])));
+                                yr[k] = pack2<BF16>(o.x, o.y);
+                            }
+                            stsm4t(g2 ? io_frag1 : io_frag, yr);
                         }
-                        T* yr = yp + static_cast<int64_t>(c * L + t0) * p.y_stride;
-                        if (t0 + 16 <= nv) {
+                        __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) yr[j * p.y_stride] = from_f<T>(o[j]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (t0 + j < nv) yr[j * p.y_stride] = from_f<T>(o[j]);
+                        for (int i = 0; i < 2; ++i) {
+                            uint4 v;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                         : "r"(io_piece + 512 * i)
+                                         : "memory");
+                            const int t = t0 + pt + 8 * i;
+                            if (t < nv) __stcs(reinterpret_cast<uint4*>(yp + static_cast<int64_t>(c * L + t) * p.y_stride), v);
                         }
+                        __syncwarp();  // y is read: the buffer takes the next block's z
                     }
                     load_z(c * L + t0 + 32, zv);
                 };
