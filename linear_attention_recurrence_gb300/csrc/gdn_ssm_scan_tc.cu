@@ -41,9 +41,9 @@ namespace gdn {
 namespace {
 
 constexpr int L = 128;        // tokens per chunk
-constexpr int kThreadsTc = 512;
+constexpr int kThreadsTc = 640;
 constexpr int kStages = 2;
-constexpr int kCopyWarp = 12, kMmaWarp = 13, kGateWarp = 14;
+constexpr int kCopyWarp = 16, kMmaWarp = 17, kGateWarp = 18;
 
 // tensor-memory columns
 constexpr uint32_t TM_H = 0;     // H^T, FP32 [head_dim lanes][state_dim]
@@ -60,8 +60,8 @@ constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kB
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: (gamma, dt)[128] at 0, w[128] at
 constexpr uint32_t SM_GATE_STAGE = 2176;                // 256, e^gamma[128] at 384, 2^k of w and 2^j of dt at 512
-constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 1 KB: 16 tokens x 32 columns
-constexpr uint32_t SM_MISC = SM_IO + 4 * 1024;
+constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
+constexpr uint32_t SM_MISC = SM_IO + 8 * 512;
 constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
@@ -152,28 +152,25 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-// Two FP32 tiles (16 lanes x 16 columns each) of each of two accumulators, one wait.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t b, float (&va)[2][8], float (&vb)[2][8]) {
-    uint32_t r[32];
+// 8 FP32 columns of 32 lanes of each of two accumulators, one wait: pair k of a result holds
+// columns 2 (lane & 3), + 1 of row 8 k + (lane >> 2).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t a, uint32_t b, float2 (&va)[4], float2 (&vb)[4]) {
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%32];\n"
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%33];\n"
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%16,%17,%18,%19,%20,%21,%22,%23}, [%34];\n"
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%24,%25,%26,%27,%28,%29,%30,%31}, [%35];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%16];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%4,%5,%6,%7}, [%17];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%8,%9,%10,%11}, [%18];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%12,%13,%14,%15}, [%19];\n"
         "tcgen05.wait::ld.sync.aligned;"
         : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
-          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
-          "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]),
-          "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31])
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15])
         : "r"(a), "r"(a + (16u << 16)), "r"(b), "r"(b + (16u << 16))
         : "memory");
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            va[g][i] = __uint_as_float(r[8 * g + i]);
-            vb[g][i] = __uint_as_float(r[16 + 8 * g + i]);
-        }
+    for (int k = 0; k < 4; ++k) {
+        va[k] = make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+        vb[k] = make_float2(__uint_as_float(r[8 + 2 * k]), __uint_as_float(r[8 + 2 * k + 1]));
+    }
 }
 // A 16-bit tile (16 lanes x 16 tokens) to 8 columns of tensor memory.
 __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&v)[4]) {
@@ -242,8 +239,9 @@ __device__ __forceinline__ float range_scale(float v) {
 // arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 13 : 5;
-    if (b == B_GFREE || b == B_M0 || b == B_M1 || b == B_H || b == B_Y1FREE || b == B_Y2FREE || b == B_TAIL) return 4;
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 17 : 5;
+    if (b == B_GFREE || b == B_M0 || b == B_M1 || b == B_H || b == B_TAIL) return 4;
+    if (b == B_Y1FREE || b == B_Y2FREE) return 8;
     if (b >= B_XW && b < B_XWFREE) return 4;
     return 1;
 }
@@ -750,110 +748,95 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
         }
         tc_fence_before_sync();
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         if constexpr (OUT) {
-            // ---- the output: this warp's 32 columns of x ----
-            const int wq = warp - 8;
+            // ---- the output: this warp's 32 columns of x, every other block of 8 tokens ----
+            const int wq = warp & 3, odd = (warp - 8) >> 2;
             const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
             const bool live = wq * 32 < P;
             const float D = p.D ? __ldg(p.D + h) : 0.f;
             const bool gated = p.z != nullptr;
-            const uint32_t x_frag = frag_offset(wq * 32, lane), x_frag1 = frag_offset(wq * 32 + 16, lane);
-            // The warp's buffer holds 16 tokens x 32 columns, 64 bytes a token, 16-byte pieces swizzled.
-            // Global memory is read and written in pieces: this lane's are piece lane & 3 of tokens
-            // lane >> 2 and that + 8.
-            const uint32_t io = smem_addr(sm) + SM_IO + wq * 1024;
+            const int pf = wq * 32 + 8 * (lane >> 3), r8 = lane & 7;  // this lane's row of an 8 x 32 tile's ldmatrix
+            const uint32_t x_frag = (pf >> 6) * kBox + r8 * 128 + ((((pf & 63) >> 3) ^ r8) << 4);
+            // The warp's buffer holds 8 tokens x 32 columns, 64 bytes a token, 16-byte pieces swizzled;
+            // global memory is read and written in pieces, this lane's piece lane & 3 of token lane >> 2.
+            const uint32_t io = smem_addr(sm) + SM_IO + (warp - 8) * 512;
             auto piece = [](int t, int c) { return static_cast<uint32_t>(t * 64 + ((c ^ ((t >> 1) & 3)) << 4)); };
             const int pt = lane >> 2;
-            const uint32_t io_piece = io + piece(pt, lane & 3);  // (token + 8: 512 bytes on, the same swizzle)
-            const uint32_t io_frag = io + piece(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
-            const uint32_t io_frag1 = io + piece(8 * (lane >> 4) + (lane & 7), 2 + ((lane >> 3) & 1));
+            const uint32_t io_piece = io + piece(pt, lane & 3), io_frag = io + piece(r8, lane >> 3);
             const int64_t col = static_cast<int64_t>(h) * P + wq * 32 + 8 * (lane & 3);
             const T* zp = gated ? static_cast<const T*>(p.z) + un.begin * p.z_stride + col : nullptr;
             T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + col;
-            // z of the segment's rows t .. t + 15, two blocks ahead of their use (from L2, where the copy
-            // warp has it fetched with the chunk's other operands)
-            auto load_z = [&](int t, uint4 (&zv)[2]) {
-                if (!gated || !live || t >= un.len) return;
+            // z of this warp's 4 blocks of a half chunk, a half ahead of their use (from L2, where the copy
+            // warp has them fetched with the chunk's other operands): one batch, because a wait for the
+            // oldest of several loads is a wait for all of them
+            uint4 zn[4], zc[4];
+            auto load_z = [&](int t) {
+                if (!gated || !live) return;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = t + pt + 8 * i < un.len ? t + pt + 8 * i : un.len - 1;
-                    zv[i] = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
+                for (int i = 0; i < 4; ++i) {
+                    const int row = t + 16 * i + pt < un.len ? t + 16 * i + pt : un.len - 1;
+                    zn[i] = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
                 }
             };
-            uint4 z0[2], z1[2];
-            load_z(0, z0);
-            load_z(16, z1);
+            load_z(8 * odd);
             uint32_t yi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
-                const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X;
+                const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X + x_frag;
                 const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
                 if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_FULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
-                // one block of 16 tokens: y from the two products, x and z (in zv), which then receives
-                // the block after the next one's
-                auto block = [&](int t0, uint4 (&zv)[2]) {
-                    if (live && t0 < nv) {
-                        uint32_t zr[2][4];
-                        if (gated) {
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    ok = wait_warp(sy, B_Y1, yi++);
+                    if (!ok) break;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece + 512 * i), "r"(zv[i].x),
-                                             "r"(zv[i].y), "r"(zv[i].z), "r"(zv[i].w)
+                    for (int i = 0; i < 4; ++i) zc[i] = zn[i];
+                    load_z(c * L + 64 * half + 64 + 8 * odd);
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t0 = 64 * half + 16 * i + 8 * odd;
+                        if (live && t0 < nv) {
+                            uint32_t zr[4], xr[4], yr[4];
+                            if (gated) {
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[i].x), "r"(zc[i].y),
+                                             "r"(zc[i].z), "r"(zc[i].w)
                                              : "memory");
-                            __syncwarp();
-                            ldsm4t(io_frag, zr[0]);
-                            ldsm4t(io_frag1, zr[1]);
-                        }
-                        float y1[2][8], y2[2][8];
-                        tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
-                        const float2 e0 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
-                        const float2 e1 = *reinterpret_cast<const float2*>(eg + t0 + 8 + 2 * (lane & 3));
-                        __syncwarp();  // z is read: the buffer takes y
-#pragma unroll
-                        for (int g2 = 0; g2 < 2; ++g2) {
-                            uint32_t xr[4], yr[4];
-                            ldsm4t(x + t0 * 128 + (g2 ? x_frag1 : x_frag), xr);
+                                __syncwarp();
+                                ldsm4t(io_frag, zr);
+                            }
+                            ldsm4t(x + t0 * 128, xr);
+                            const float2 e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
+                            float2 y1[4], y2[4];
+                            tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                float2 o = make_float2(y1[g2][2 * k], y1[g2][2 * k + 1]);
+                                float2 o = y1[k];
                                 if constexpr (!BF16) o = fmul2(o, make_float2(m_scale, m_scale));
-                                o = ffma2(k < 2 ? e0 : e1, make_float2(y2[g2][2 * k], y2[g2][2 * k + 1]), o);
+                                o = ffma2(e2, y2[k], o);
                                 o = ffma2(make_float2(D, D), unpack2<BF16>(xr[k]), o);
-                                if (gated) o = fmul2(o, silu2(unpack2<BF16>(zr[g2][k])));
+                                if (gated) o = fmul2(o, silu2(unpack2<BF16>(zr[k])));
                                 yr[k] = pack2<BF16>(o.x, o.y);
                             }
-                            stsm4t(g2 ? io_frag1 : io_frag, yr);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                            __syncwarp();  // z is read: the buffer takes y
+                            stsm4t(io_frag, yr);
+                            __syncwarp();
                             uint4 v;
                             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                         : "r"(io_piece + 512 * i)
+                                         : "r"(io_piece)
                                          : "memory");
-                            const int t = t0 + pt + 8 * i;
+                            const int t = t0 + pt;
                             if (t < nv) __stcs(reinterpret_cast<uint4*>(yp + static_cast<int64_t>(c * L + t) * p.y_stride), v);
+                            __syncwarp();  // y is read: the buffer takes the next block's z
                         }
-                        __syncwarp();  // y is read: the buffer takes the next block's z
                     }
-                    load_z(c * L + t0 + 32, zv);
-                };
-#pragma unroll 1
-                for (int t0 = 0; t0 < L; t0 += 32) {
-                    if ((t0 & 63) == 0) ok = wait_warp(sy, B_Y1, yi++);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    block(t0, z0);
-                    block(t0 + 16, z1);
-                    if ((t0 & 63) == 32) {
-                        tc_fence_before_sync();
-                        warp_arrive(sy, B_Y1FREE);
-                    }
+                    tc_fence_before_sync();
+                    warp_arrive(sy, B_Y1FREE);
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_Y2FREE);
