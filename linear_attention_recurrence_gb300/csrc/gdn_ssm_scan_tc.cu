@@ -26,9 +26,7 @@
 //
 // Warp roles (512 threads): warps 0-3 form M (lane = token); 4-7 the parts of w o x and
 // the state's decay and rounding (lane = column of x); 8-11 the output; 12 issues the
-// copies, 13 the MMAs, 14 forms the gates.  MMA order per chunk: H^T C^T, the second
-// half of G, the first half of Y, the update (8 blocks of 16 tokens, behind the parts),
-// the next chunk's first half of G, the second half of Y.
+// copies, 13 the MMAs, 14 forms the gates.  MMA order
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -43,7 +41,7 @@ namespace {
 constexpr int L = 128;        // tokens per chunk
 constexpr int kThreadsTc = 640;
 constexpr int kStages = 2;
-constexpr int kCopyWarp = 16, kMmaWarp = 17, kGateWarp = 18;
+constexpr int kCopyWarp = 16, kMmaWarp = 17, kGateWarp = 18, kStateMmaWarp = 19;
 
 // tensor-memory columns
 constexpr uint32_t TM_H = 0;     // H^T, FP32 [head_dim lanes][state_dim]
@@ -67,7 +65,7 @@ static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form")
 
 enum {
     B_FULL, B_GATE = B_FULL + kStages, B_EMPTY = B_GATE + kStages,
-    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_S, B_Y1, B_Y1FREE, B_Y2FREE,
+    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE, B_Y2FREE,
     B_XW,             // [kXwSlots <= 4]
     B_XWFREE = B_XW + 4,
     B_TAIL = B_XWFREE + 4,
@@ -239,9 +237,10 @@ __device__ __forceinline__ float range_scale(float v) {
 // arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 17 : 5;
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 18 : 5;
     if (b == B_GFREE || b == B_M0 || b == B_M1 || b == B_H || b == B_TAIL) return 4;
     if (b == B_Y1FREE || b == B_Y2FREE) return 8;
+    if (b == B_FIN) return out ? 2 : 1;
     if (b >= B_XW && b < B_XWFREE) return 4;
     return 1;
 }
@@ -264,6 +263,12 @@ __device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
 // instructions behind a wait need a converged warp).
 __device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
     return __all_sync(0xffffffffu, wait_phase(s, b, n)) != 0;
+}
+// Every MMA of the CTA ends before tensor memory is freed.
+__device__ __forceinline__ void finish_mma(uint64_t* bar) {
+    umma_commit(bar);
+    for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(bar, 0); ++n) {
+    }
 }
 // One arrival for the calling warp.
 __device__ __forceinline__ void warp_arrive(const Sync& s, int b) {
@@ -390,13 +395,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        if (OUT && lane == 0) {
             constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
             constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
             constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 128, false, false);
-            constexpr uint32_t ID_S = idesc_f16(BF16, 128, N, false, true);     // B: N-major
             const uint32_t sm0 = smem_addr(sm);
-            uint32_t gi = 0, yi = 0, qi = 0;
+            uint32_t gi = 0, yi = 0;
             auto issue_g = [&](int c, int half) {  // G's columns of tokens 64 half .. +63
                 if (gi > 0 && !wait_phase(sy, B_GFREE, gi - 1)) return false;
                 tc_fence_after_sync();
@@ -422,49 +426,52 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 ++yi;
                 return true;
             };
-            bool ok = wait_phase(sy, B_FULL, 0);
-            if (OUT) ok = ok && issue_g(0, 0);
-            for (int c = 0; ok && c < nch; ++c) {
-                const int s = c % kStages;
-                const uint32_t st = sm0 + s * SM_STAGE;
-                if (!wait_phase(sy, B_FULL + s, c / kStages)) break;
-                if (!wait_phase(sy, B_H, c)) break;
-                if (OUT) {
-                    if (c > 0 && !wait_phase(sy, B_Y2FREE, c - 1)) break;
+            if (wait_phase(sy, B_FULL, 0) && issue_g(0, 0)) {
+                for (int c = 0; c < nch; ++c) {
+                    const int s = c % kStages;
+                    const uint32_t st = sm0 + s * SM_STAGE;
+                    // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
+                    if (!wait_phase(sy, B_H, c) || (c > 0 && !wait_phase(sy, B_Y2FREE, c - 1))) break;
                     tc_fence_after_sync();
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k)
                         mma_ts(tm + TM_Y2, tm + TM_HB + 8 * k, desc_k(st + SM_C + (k / 4) * kBox + (k % 4) * 32), ID_Y2, k > 0);
+                    umma_commit(&bar[B_HBFREE]);
                     if (!issue_g(c, 1) || !issue_y1(c, 0)) break;
-                }
-                for (int j = 0; j < L / 16 && ok; ++j, ++qi) {
-                    const int slot = qi % SLOTS;
-                    if (!wait_phase(sy, B_XW + slot, qi / SLOTS)) {
-                        ok = false;
-                        break;
+                    if (c + 1 < nch) {
+                        if (!wait_phase(sy, B_FULL + (c + 1) % kStages, (c + 1) / kStages) || !issue_g(c + 1, 0)) break;
                     }
+                    if (!issue_y1(c, 1)) break;
+                    umma_commit(&bar[B_MFREE]);
+                    umma_commit(&bar[B_EMPTY + s]);
+                }
+            }
+            finish_mma(&bar[B_FIN]);
+        }
+    } else if (warp == kStateMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t ID_S = idesc_f16(BF16, 128, N, false, true);     // B: N-major
+            const uint32_t sm0 = smem_addr(sm);
+            uint32_t qi = 0;
+            bool ok = true;
+            for (int c = 0; ok && c < nch; ++c) {
+                const int s = c % kStages;
+                if (!wait_phase(sy, B_FULL + s, c / kStages) || !wait_phase(sy, B_H, c)) break;
+                for (int j = 0; j < L / 16; ++j, ++qi) {
+                    const int slot = qi % SLOTS;
+                    ok = wait_phase(sy, B_XW + slot, qi / SLOTS);
+                    if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t b = desc_mn(st + SM_B + j * 2048);
+                    const uint64_t b = desc_mn(sm0 + s * SM_STAGE + SM_B + j * 2048);
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) mma_ts(tm + TM_H, tm + TM_XW + (slot * PARTS + i) * 8, b, ID_S, true);
                     umma_commit(&bar[B_XWFREE + slot]);
                 }
                 if (!ok) break;
                 umma_commit(&bar[B_S]);
-                if (OUT) {
-                    if (c + 1 < nch) {
-                        if (!wait_phase(sy, B_FULL + (c + 1) % kStages, (c + 1) / kStages)) break;
-                        if (!issue_g(c + 1, 0)) break;
-                    }
-                    if (!issue_y1(c, 1)) break;
-                    umma_commit(&bar[B_MFREE]);
-                }
                 umma_commit(&bar[B_EMPTY + s]);
             }
-            // every MMA ends before tensor memory is freed
-            umma_commit(&bar[B_FIN]);
-            for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(&bar[B_FIN], 0); ++n) {
-            }
+            finish_mma(&bar[B_FIN]);
         }
     } else if (warp == kGateWarp) {
         const float A = ssm_rate(__ldg(p.A_log + h)), bias = __ldg(p.dt_bias + h);
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 warp_arrive(sy, B_TAIL);
                 if (!wait_warp(sy, B_TAIL, 0)) break;
             }
-            if (c > 0 && !wait_warp(sy, B_S, c - 1)) break;
+            if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) break;
             tc_fence_after_sync();
             const float next_scale = BF16 ? 1.f : gt[512];
             if (live) {
@@ -800,8 +807,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int t0 = 64 * half + 16 * i + 8 * odd;
-                        if (live && t0 < nv) {
-                            uint32_t zr[4], xr[4], yr[4];
+                        const bool some = live && t0 < nv;
+                        uint32_t zr[4], xr[4], yr[4];
+                        float2 e2, y1[4], y2[4];
+                        if (some) {
                             if (gated) {
                                 asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[i].x), "r"(zc[i].y),
                                              "r"(zc[i].z), "r"(zc[i].w)
@@ -810,9 +819,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 ldsm4t(io_frag, zr);
                             }
                             ldsm4t(x + t0 * 128, xr);
-                            const float2 e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
-                            float2 y1[4], y2[4];
+                            e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
+                        }
+                        if (i == 3) {  // the products are read
+                            tc_fence_before_sync();
+                            warp_arrive(sy, B_Y1FREE);
+                            if (half) warp_arrive(sy, B_Y2FREE);
+                        }
+                        if (some) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 float2 o = y1[k];
@@ -835,11 +850,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             __syncwarp();  // y is read: the buffer takes the next block's z
                         }
                     }
-                    tc_fence_before_sync();
-                    warp_arrive(sy, B_Y1FREE);
                 }
                 if (!ok) break;
-                warp_arrive(sy, B_Y2FREE);
                 warp_arrive(sy, B_EMPTY + s);
             }
         }
