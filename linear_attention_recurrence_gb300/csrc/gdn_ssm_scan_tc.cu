@@ -249,11 +249,26 @@ struct Sync {
     uint64_t* bar;
     volatile int* abort_flag;
 };
+// A poll suspends its thread for up to this long, so that waiting warps take few issue
+// slots from the working ones; a wait gives up after kTcPolls of them (seconds).
+constexpr uint32_t kSuspendNs = 20000, kTcPolls = 1u << 17;
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
 // Waits for phase `n` (0, 1, ...) of a barrier.  False once some wait of the CTA gave up.
 __device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
-        if (mbar_try_wait(&s.bar[b], n & 1)) return true;
-        if ((i & 63) == 63 && *s.abort_flag) return false;
+    if (poll(&s.bar[b], n & 1)) return true;
+    for (uint32_t i = 0; i < kTcPolls; ++i) {
+        if (poll(&s.bar[b], n & 1)) return true;
+        if (*s.abort_flag) return false;
     }
     *s.abort_flag = 1;
     report_timeout(&g_ssm_status);
@@ -267,7 +282,7 @@ __device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
 // Every MMA of the CTA ends before tensor memory is freed.
 __device__ __forceinline__ void finish_mma(uint64_t* bar) {
     umma_commit(bar);
-    for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(bar, 0); ++n) {
+    for (uint32_t n = 0; n < kTcPolls && !poll(bar, 0); ++n) {
     }
 }
 // One arrival for the calling warp.
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
             // the copies in flight land before the CTA ends, also after a wait that gave up
             for (int i = c > kStages ? c - kStages : 0; i < c; ++i)
-                for (uint32_t n = 0; n < kWaitPolls && !mbar_try_wait(&bar[B_FULL + i % kStages], (i / kStages) & 1); ++n) {
+                for (uint32_t n = 0; n < kTcPolls && !poll(&bar[B_FULL + i % kStages], (i / kStages) & 1); ++n) {
                 }
         }
     } else if (warp == kMmaWarp) {
@@ -566,39 +581,34 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const float2* gd = reinterpret_cast<const float2*>(sm + SM_GATE + s * SM_GATE_STAGE);
                 const float gt = gd[t].x;
                 bool ok = true;
-#pragma unroll
-                for (int half = 0; half < 2; ++half, ++gi) {
-                    if (!wait_warp(sy, B_G, gi) || (half == 0 && c > 0 && !wait_warp(sy, B_MFREE, c - 1))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    if (half == 0 || warp >= 2) {
 #pragma unroll 1
-                        for (int cb = 0; cb < 2; ++cb) {
-                            const int c0 = 64 * half + 32 * cb;
-                            if (c0 > warp * 32) break;
-                            float v[32];
-                            tmem_ld32(tm + lanes + TM_G + 32 * cb, v);
-                            const bool diag = c0 == warp * 32;
-                            unsigned char* m = half ? m1 : m0;
+                for (int half = 0; half < 2; ++half, ++gi) {
+                    ok = wait_warp(sy, B_G, gi) && (half || c == 0 || wait_warp(sy, B_MFREE, c - 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    unsigned char* m = half ? m1 : m0;
+                    // 16 columns at a time, up to the block of 32 on the diagonal
+                    const int stop = half == 0 && warp >= 2 ? 64 : 32 * (warp + 1) - 64 * half;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < stop; j0 += 16) {
+                        float v[16];
+                        tmem_ld16(tm + lanes + TM_G + j0, v);
+                        const int above = t - 64 * half - j0;  // columns past it are above the diagonal
+                        const float4* e4 = reinterpret_cast<const float4*>(gd + 64 * half + j0);
+                        uint32_t o[8];
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int i = 0; i < 8; i += 2) {
-                                    const float4 e = *reinterpret_cast<const float4*>(&gd[c0 + j + i]);
-                                    float a0 = v[j + i] * (ex2(gt - e.x) * e.y), a1 = v[j + i + 1] * (ex2(gt - e.z) * e.w);
-                                    if (diag) {  // selected, not multiplied: what is above may be anything
-                                        if (j + i > lane) a0 = 0.f;
-                                        if (j + i + 1 > lane) a1 = 0.f;
-                                    }
-                                    o[i / 2] = pack2<BF16>(a0, a1);
-                                }
-                                *reinterpret_cast<uint4*>(m + (((4 * cb + j / 8) ^ (t & 7)) << 4)) =
-                                    make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 e = e4[i];
+                            const float2 d = fadd2(make_float2(gt, gt), make_float2(-e.x, -e.z));
+                            float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(e.y, e.w));
+                            a = fmul2(a, make_float2(v[2 * i], v[2 * i + 1]));
+                            // selected, not multiplied: what is above may be anything
+                            o[i] = pack2<BF16>(2 * i > above ? 0.f : a.x, 2 * i + 1 > above ? 0.f : a.y);
                         }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint4*>(m + (((j0 / 8 + i) ^ (t & 7)) << 4)) =
+                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     tc_fence_before_sync();
                     warp_arrive(sy, B_GFREE);
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     for (int i = 0; i < 4; ++i) zc[i] = zn[i];
                     load_z(c * L + 64 * half + 64 + 8 * odd);
                     tc_fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
                         const int t0 = 64 * half + 16 * i + 8 * odd;
                         const bool some = live && t0 < nv;
@@ -812,11 +822,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         float2 e2, y1[4], y2[4];
                         if (some) {
                             if (gated) {
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[i].x), "r"(zc[i].y),
-                                             "r"(zc[i].z), "r"(zc[i].w)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[0].x), "r"(zc[0].y),
+                                             "r"(zc[0].z), "r"(zc[0].w)
                                              : "memory");
                                 __syncwarp();
                                 ldsm4t(io_frag, zr);
+#pragma unroll
+                                for (int k = 0; k < 3; ++k) zc[k] = zc[k + 1];  // (a rolled loop: the code of all roles has to fit the caches)
                             }
                             ldsm4t(x + t0 * 128, xr);
                             e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
