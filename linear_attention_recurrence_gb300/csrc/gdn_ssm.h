@@ -27,7 +27,7 @@ struct SsmConvParams {
     int n_seq, n_slots;
     int64_t T;
     int channels, width, activation, dtype;
-    bool vector;                 // every row and parameter row starts on a 16-byte boundary
+    bool vector;                 // rows are whole pieces of 4 elements on boundaries of that size, w on 16 bytes
 };
 cudaError_t launch_ssm_conv(const SsmConvParams& p, int sm_count, cudaStream_t s);
 
@@ -54,7 +54,9 @@ constexpr int kSsmTcMinTokens = 64;  // tokens per sequence from which it is tak
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq);
 size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count);
 cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_count, cudaStream_t s);
-// The tensor form's status word on `device`, read and cleared (0 if it never ran there).
+// The status word of the bounded waits of the tensor form and the block norm: its address
+// on the current device, and its value there, read and cleared (0 if none of them ran).
+cudaError_t ssm_status_word(int** word);
 cudaError_t ssm_take_status(int device, int* word);
 
 // ---- one token of the convolution and the scan for each request (gdn_ssm_step.cu) ----
@@ -80,8 +82,10 @@ struct BlockNormParams {
     float scale, eps;
     int64_t T;
     int dim, gate_sigmoid, dtype, stream_dtype;
-    int vec;  // elements that every row's start is a multiple of (8, 4, 2 or 1)
+    int vec;      // elements that every row's start is a multiple of (8, 4, 2 or 1)
+    int* status;
+    bool rows16;  // rows start on 16-byte boundaries and are whole 16-byte pieces (and 8 elements)
 };
-cudaError_t launch_block_norm(const BlockNormParams& p, cudaStream_t s);
+cudaError_t launch_block_norm(const BlockNormParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace gdn

@@ -120,10 +120,9 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
     if (any_overlap(ins, outs)) return bad("an output overlaps another argument");
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
-    const int v = 16 / e;
-    const bool vector = is_aligned(x, 16) && is_aligned(y, 16) && is_aligned(hist, 16) && channels % v == 0 &&
-                        x_stride % v == 0 && y_stride % v == 0;
-    if (channels > (vector ? v : 1) * 128 * 65535) return unsupported("too many channels");
+    const bool vector = is_aligned(x, 4 * e) && is_aligned(y, 4 * e) && is_aligned(hist, 4 * e) && is_aligned(w, 16) &&
+                        channels % 4 == 0 && x_stride % 4 == 0 && y_stride % 4 == 0;
+    if (channels > (vector ? 4 : 1) * 128 * 65535) return unsupported("too many channels");
     const SsmConvParams p{x, y, x_stride, y_stride, w, bias, hist, cu_seqlens, slots, has_state, n_seq, n_slots, T,
                           channels, width, activation, dtype, vector};
     cudaError_t err = launch_ssm_conv(p, sms, static_cast<cudaStream_t>(cuda_stream));
@@ -290,10 +289,13 @@ int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_
                         fits(residual_out, residual_out_stride, er) && fits(y, y_stride, e) &&
                         (!gate || fits(gate, gate_stride, e))))
         vec /= 2;
-    const BlockNormParams p{b, residual, gate, residual_out, y, b_stride, residual_stride, gate_stride,
+    BlockNormParams p{b, residual, gate, residual_out, y, b_stride, residual_stride, gate_stride,
                             residual_out_stride, y_stride, w_post, w_pre, scale, eps, T, dim, gate_sigmoid, dtype,
-                            residual_dtype, vec};
-    cudaError_t err = launch_block_norm(p, static_cast<cudaStream_t>(cuda_stream));
+                            residual_dtype, vec, nullptr, vec == 8};
+    int sms = 0;
+    if (int rc = sm_count(&sms)) return rc;
+    if (cudaError_t err = ssm_status_word(&p.status); err != cudaSuccess) return cuda_bad(err, "block norm set-up");
+    cudaError_t err = launch_block_norm(p, sms, static_cast<cudaStream_t>(cuda_stream));
     if (err != cudaSuccess) return cuda_bad(err, "block norm launch");
     internal_count_launch();
     return GDN_OK;

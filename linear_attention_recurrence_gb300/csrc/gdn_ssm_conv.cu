@@ -3,10 +3,10 @@
 // the K - 1 rows before a sequence's first token taken from its slot of the history
 // (zeros for a new sequence); the slot then receives the sequence's last K - 1 rows.
 //
-// Bound by HBM: every row is read once and written once.  A thread holds 16 bytes of
-// channels (its taps and bias in registers) and walks a tile of rows with the last
-// K - 1 rows in registers, so a row is fetched once per tile; the K - 1 rows before a
-// tile are fetched again (3 in 16 or 32, from L2).
+// Bound by HBM: every row is read once and written once.  A thread holds 4 channels
+// (their taps and bias in registers) and walks a tile of rows with the last K - 1 rows in
+// registers and 8 rows' loads in flight, so a row is fetched once per tile; the K - 1 rows
+// before a tile are fetched again (3 in 16 to 64, from L2).
 //
 // History without a race: the tile that holds a sequence's first row also owns the
 // rows at positions 1 .. K - 2 (a tile boundary that would fall there moves behind
@@ -19,7 +19,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // rows whose loads are in flight together
+constexpr int kAhead = 8;  // rows whose loads are in flight together
 
 // Sequences whose begin is at or before rows r0 and r1 (all lanes get both counts; one
 // pass of independent loads instead of two binary searches of dependent ones).
@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t tile_edge(const SsmSeqs& q, int64_t r, int co
 }
 
 template <class T, int K, int VEC>
-__global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams p, const SsmSeqs q, int tile_rows) {
+__global__ void __launch_bounds__(kThreads, 5) ssm_conv_kernel(const SsmConvParams p, const SsmSeqs q, int tile_rows) {
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * tile_rows;
     const int64_t r1 = r0 + tile_rows < q.T ? r0 + tile_rows : q.T;
     int c0, c1;
@@ -57,12 +57,26 @@ __global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams 
     if (c >= p.channels) return;
 
     float w[VEC][K], bias[VEC];
+    if constexpr (VEC > 1) {  // the thread's VEC K taps lie together, on a 16-byte boundary
+        float flat[VEC * K];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
+        for (int i = 0; i < VEC * K; i += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(p.w + static_cast<int64_t>(c) * K + i));
+            flat[i] = f.x;
+            flat[i + 1] = f.y;
+            flat[i + 2] = f.z;
+            flat[i + 3] = f.w;
+        }
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[v][j] = __ldg(p.w + static_cast<int64_t>(c + v) * K + j);
-        bias[v] = p.bias ? __ldg(p.bias + c + v) : 0.f;
+        for (int v = 0; v < VEC; ++v)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[v][j] = flat[v * K + j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[0][j] = __ldg(p.w + static_cast<int64_t>(c) * K + j);
     }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) bias[v] = p.bias ? __ldg(p.bias + c + v) : 0.f;
     const T* x = static_cast<const T*>(p.x) + c;
     T* y = static_cast<T*>(p.y) + c;
     T* hist = static_cast<T*>(p.hist);
@@ -98,13 +112,10 @@ __global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams 
                     float f[VEC];
                     if (at >= 0) {
                         load_vec<T, VEC>(x + (b + at) * p.x_stride, f);
-                    } else {
+                    } else {  // a short sequence keeps rows of the old history, each behind the one written here
 #pragma unroll
-                        for (int i = 0; i < K - 1; ++i)
-                            if (i == at + (K - 1)) {
-#pragma unroll
-                                for (int v = 0; v < VEC; ++v) f[v] = win[i][v];
-                            }
+                        for (int v = 0; v < VEC; ++v) f[v] = 0.f;
+                        if (old) load_vec<T, VEC>(h + (at + (K - 1)) * p.channels, f);
                     }
                     store_vec<T, VEC>(h + static_cast<int64_t>(j) * p.channels, f);
                 }
@@ -114,27 +125,33 @@ __global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams 
             for (int j = 0; j < K - 1; ++j) load_vec<T, VEC>(x + (r - (K - 1) + j) * p.x_stride, win[j]);
         }
         const int64_t stop = e < hi ? e : hi;
-        for (; r < stop; r += kAhead) {
-            float cur[kAhead][VEC];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (r + u < stop) load_vec<T, VEC>(x + (r + u) * p.x_stride, cur[u]);
+        const T* xr = x + r * p.x_stride;
+        T* yr = y + r * p.y_stride;
+        for (int left = static_cast<int>(stop - r); left > 0; left -= kAhead) {
+            Vec<T, VEC> raw[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (r + u >= stop) break;
+                if (u < left) raw[u] = *reinterpret_cast<const Vec<T, VEC>*>(xr);
+                xr += p.x_stride;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (u >= left) break;
                 float f[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     float acc = bias[v];
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) acc = fmaf(w[v][j], win[j][v], acc);
-                    acc = fmaf(w[v][K - 1], cur[u][v], acc);
+                    const float cur = to_f<T>(raw[u].v[v]);
+                    acc = fmaf(w[v][K - 1], cur, acc);
                     f[v] = p.activation ? ssm_silu(acc) : acc;
 #pragma unroll
                     for (int j = 0; j + 1 < K - 1; ++j) win[j][v] = win[j + 1][v];
-                    win[K - 2][v] = cur[u][v];
+                    win[K - 2][v] = cur;
                 }
-                store_vec<T, VEC>(y + (r + u) * p.y_stride, f);
+                store_vec<T, VEC>(yr, f);
+                yr += p.y_stride;
             }
         }
         r = stop;
@@ -143,12 +160,13 @@ __global__ void __launch_bounds__(kThreads) ssm_conv_kernel(const SsmConvParams 
 
 template <class T, int K>
 void launch_k(const SsmConvParams& p, const SsmSeqs& q, int sm_count, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 4;
     const int vec = p.vector ? V : 1;
     const int blocks_y = (p.channels + kThreads * vec - 1) / (kThreads * vec);
-    // 32-row tiles re-read a tenth of the rows, 16-row tiles a fifth but give twice the
-    // CTAs: short calls take the latter (fewer than 8 CTAs per SM otherwise).
-    const int tile = (q.T / 32) * blocks_y >= static_cast<int64_t>(8) * sm_count ? 32 : 16;
+    // A tile re-reads its 3 first rows' predecessors and the taps: 64 rows where that leaves
+    // 8 CTAs per SM, else 32 (4 per SM), else 16.
+    const int64_t rows_y = q.T * blocks_y;
+    const int tile = rows_y >= int64_t{64} * 8 * sm_count ? 64 : rows_y >= int64_t{32} * 4 * sm_count ? 32 : 16;
     const dim3 grid(static_cast<unsigned>((q.T + tile - 1) / tile), blocks_y);
     if (vec == V)
         ssm_conv_kernel<T, K, V><<<grid, kThreads, 0, s>>>(p, q, tile);

@@ -116,26 +116,55 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
         }
         const bool more = t0 + TB < e;
         if (more) fetch(t0 + TB);
-#pragma unroll 2
-        for (int t = 0; t < nv; ++t) {
+        // one token: the state's update and this thread's part of its two outputs
+        auto token = [&](int t, float& r0, float& r1) {
             const float2 gt = gate[buf][t];
             const float2 xv = *reinterpret_cast<const float2*>(&xs[buf][t][2 * cp]);
             const float2 a2 = make_float2(gt.x, gt.x);
             const float x0 = gt.y * xv.x, x1 = gt.y * xv.y;
             float2 y0 = make_float2(0.f, 0.f), y1 = y0;
+            constexpr int W = NR >= 4 ? 4 : 2;  // rows per shared-memory load
 #pragma unroll
-            for (int i = 0; i < NR / 2; ++i) {
-                const float2 bb = *reinterpret_cast<const float2*>(&Bs[buf][t][NR * rg + 2 * i]);
-                const float2 cc = *reinterpret_cast<const float2*>(&Cs[buf][t][NR * rg + 2 * i]);
-                S[0][i] = ffma2(a2, S[0][i], fmul2(bb, make_float2(x0, x0)));
-                S[1][i] = ffma2(a2, S[1][i], fmul2(bb, make_float2(x1, x1)));
-                y0 = ffma2(cc, S[0][i], y0);
-                y1 = ffma2(cc, S[1][i], y1);
+            for (int i = 0; i < NR; i += W) {
+                float bb[W], cc[W];
+                if constexpr (W == 4) {
+                    const float4 b4 = *reinterpret_cast<const float4*>(&Bs[buf][t][NR * rg + i]);
+                    const float4 c4 = *reinterpret_cast<const float4*>(&Cs[buf][t][NR * rg + i]);
+                    bb[0] = b4.x; bb[1] = b4.y; bb[2] = b4.z; bb[3] = b4.w;
+                    cc[0] = c4.x; cc[1] = c4.y; cc[2] = c4.z; cc[3] = c4.w;
+                } else {
+                    const float2 b2 = *reinterpret_cast<const float2*>(&Bs[buf][t][NR * rg + i]);
+                    const float2 c2 = *reinterpret_cast<const float2*>(&Cs[buf][t][NR * rg + i]);
+                    bb[0] = b2.x; bb[1] = b2.y;
+                    cc[0] = c2.x; cc[1] = c2.y;
+                }
+#pragma unroll
+                for (int j = 0; j < W; j += 2) {
+                    const float2 b2 = make_float2(bb[j], bb[j + 1]), c2 = make_float2(cc[j], cc[j + 1]);
+                    float2 &s0 = S[0][(i + j) / 2], &s1 = S[1][(i + j) / 2];
+                    s0 = ffma2(a2, s0, fmul2(b2, make_float2(x0, x0)));
+                    s1 = ffma2(a2, s1, fmul2(b2, make_float2(x1, x1)));
+                    y0 = ffma2(c2, s0, y0);
+                    y1 = ffma2(c2, s1, y1);
+                }
             }
-            float r0 = y0.x + y0.y, r1 = y1.x + y1.y;
-            r0 += __shfl_xor_sync(0xffffffffu, r0, 16);
-            r1 += __shfl_xor_sync(0xffffffffu, r1, 16);
-            if (lane < 16) *reinterpret_cast<float2*>(&yp[warp][t][2 * cp]) = make_float2(r0, r1);
+            r0 = y0.x + y0.y;
+            r1 = y1.x + y1.y;
+        };
+        // 4 tokens between the sums over the warp's two row groups, so that those overlap
+        for (int t = 0; t < nv; t += 4) {
+            float r0[4], r1[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                r0[k] = r1[k] = 0.f;
+                if (t + k < nv) token(t + k, r0[k], r1[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                r0[k] += __shfl_xor_sync(0xffffffffu, r0[k], 16);
+                r1[k] += __shfl_xor_sync(0xffffffffu, r1[k], 16);
+                if (lane < 16) *reinterpret_cast<float2*>(&yp[warp][t + k][2 * cp]) = make_float2(r0[k], r1[k]);
+            }
         }
         if (more) stage(buf ^ 1);
         __syncthreads();

@@ -87,6 +87,7 @@ struct TcParams {
     float* ws;        // [units][n_heads][state_dim][head_dim], or nullptr: no segments
     float* ws_decay;  // [units][n_heads]
     SsmSeqs q;
+    int* status;
     int64_t units;    // the grid's: no fewer than the segments of disjoint sequences
     int seg;          // tokens per segment, a multiple of L
     int n_heads, n_groups;
@@ -248,6 +249,7 @@ __device__ constexpr int arrivals(int b, bool out) {
 struct Sync {
     uint64_t* bar;
     volatile int* abort_flag;
+    int* status;
 };
 // A poll suspends its thread for up to this long, so that waiting warps take few issue
 // slots from the working ones; a wait gives up after kTcPolls of them (seconds).
@@ -271,7 +273,7 @@ __device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
         if (*s.abort_flag) return false;
     }
     *s.abort_flag = 1;
-    report_timeout(&g_ssm_status);
+    report_timeout(s.status);
     return false;
 }
 // The same for a whole warp: all lanes leave together, with one answer (the tensor-memory
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM_MISC + NBAR * 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
     int* warp_sum = reinterpret_cast<int*>(sm + SM_GATE);  // before the gates are written
-    const Sync sy{bar, abort_flag};
+    const Sync sy{bar, abort_flag, p.status};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int h = blockIdx.x % p.n_heads;
@@ -921,7 +923,7 @@ cudaError_t launch_b(const TcParams& p, int head_dim, int state_dim, int64_t uni
     return state_dim == 128 ? launch_pn<BF16, 64, 128>(p, units, s) : launch_pn<BF16, 64, 64>(p, units, s);
 }
 
-std::atomic<bool> g_used[64];  // devices on which the tensor form has run
+std::atomic<int*> g_status_word[64];  // its address on the devices it was asked for
 
 }  // namespace
 
@@ -971,19 +973,32 @@ cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_c
     t.seg = static_cast<int>(seg);
     t.n_heads = p.n_heads;
     t.n_groups = p.n_groups;
+    cudaError_t e = ssm_status_word(&t.status);
+    if (e != cudaSuccess) return e;
+    return bf16 ? launch_b<true>(t, p.head_dim, p.state_dim, units, s) : launch_b<false>(t, p.head_dim, p.state_dim, units, s);
+}
+
+cudaError_t ssm_status_word(int** word) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) g_used[dev].store(true);
-    return bf16 ? launch_b<true>(t, p.head_dim, p.state_dim, units, s) : launch_b<false>(t, p.head_dim, p.state_dim, units, s);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    *word = g_status_word[dev].load();
+    if (*word) return cudaSuccess;
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_ssm_status);
+    if (e != cudaSuccess) return e;
+    *word = static_cast<int*>(p);
+    g_status_word[dev].store(*word);
+    return cudaSuccess;
 }
 
 cudaError_t ssm_take_status(int device, int* word) {
     *word = 0;
-    if (device < 0 || device >= 64 || !g_used[device].load()) return cudaSuccess;
-    cudaError_t e = cudaMemcpyFromSymbol(word, g_ssm_status, sizeof(int));
-    const int zero = 0;
-    if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbol(g_ssm_status, &zero, sizeof(int));
+    int* at = device >= 0 && device < 64 ? g_status_word[device].load() : nullptr;
+    if (!at) return cudaSuccess;
+    cudaError_t e = cudaMemcpy(word, at, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && *word != 0) e = cudaMemset(at, 0, sizeof(int));
     return e;
 }
 

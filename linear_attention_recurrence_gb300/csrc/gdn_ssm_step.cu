@@ -26,7 +26,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int COLS = 32;
 constexpr int kMaxN = 128;
-constexpr int kBatchRows = 8;  // load instructions in flight per warp (4 rows each)
+// Load instructions in flight per warp (4 rows each), and the next as many: with 4 CTAs per
+// SM that is 5.8 TB/s at 250 requests; 8 with 2 CTAs 5.3, 16 with 2 4.2 (the latency of a
+// CTA's start and of its convolution is hidden by the other CTAs, not by more loads).
+constexpr int kBatchRows = 4;
 
 template <class T>
 __device__ __forceinline__ float conv_channel(const SsmStepParams& p, int64_t cw, const T* row, T* hist, bool owner, int64_t c,
@@ -53,7 +56,7 @@ __device__ __forceinline__ float conv_channel(const SsmStepParams& p, int64_t cw
 }
 
 template <class T, int WPT>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams p) {
+__global__ void __launch_bounds__(kThreads, 4) ssm_step_kernel(const SsmStepParams p) {
     namespace cg = cooperative_groups;
     extern __shared__ float x_s[];  // this CTA's x columns
     __shared__ float B_s[kMaxN], C_s[kMaxN];
@@ -70,6 +73,29 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
     // the group's tiles of 32 columns, r heads x P / 32 each; this CTA's are [t0, t1)
     const int per_head = P / COLS, tiles = r * per_head;
     const int t0 = tiles * rank / ranks, t1 = tiles * (rank + 1) / ranks;
+
+    // A warp's work is a list of rounds: 16 rows (4 load instructions of 4 rows x 8 float4
+    // columns) of its share of a tile's rows, tile after tile.  The next round's loads are
+    // issued before a round is worked on, the first ones before the convolution.
+    const int sub = lane >> 3, quad = lane & 7;  // row within a load instruction, float4 column
+    constexpr int kTilesPerPass = kWarps / WPT;
+    const int share = N / WPT, rounds = (share + 4 * kBatchRows - 1) / (4 * kBatchRows);
+    const int n0 = (warp % WPT) * share;
+    const int passes = (t1 - t0 + kTilesPerPass - 1) / kTilesPerPass;
+    auto state_at = [&](int tile, int k) {
+        const int h = (tile / per_head) * p.n_groups + g, col = (tile % per_head) * COLS + 4 * quad;
+        return p.states + ((static_cast<int64_t>(slot) * p.n_heads + h) * N + n0 + k + sub) * P + col;
+    };
+    float4 v[kBatchRows], next[kBatchRows];
+    auto fetch = [&](int pass, int round) {
+        const int tile = t0 + pass * kTilesPerPass + warp / WPT, k = round * 4 * kBatchRows;
+        if (tile >= t1) return;
+        const float* st = state_at(tile, k);
+#pragma unroll
+        for (int i = 0; i < kBatchRows; ++i)
+            if (k + 4 * i < share) next[i] = __ldcs(reinterpret_cast<const float4*>(st + static_cast<int64_t>(4 * i) * P));
+    };
+    fetch(0, 0);
 
     float old[4];
     const int64_t bc = static_cast<int64_t>(p.n_heads) * P;
@@ -91,11 +117,8 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
     if (ranks > 1) cluster.barrier_arrive();  // this CTA has read the B and C history
     __syncthreads();
 
-    const int sub = lane >> 3, quad = lane & 7;  // row within a load instruction, float4 column
-    constexpr int kTilesPerPass = kWarps / WPT;
-    const int share = N / WPT;  // rows of a tile per warp
-    for (int base = t0; base < t1; base += kTilesPerPass) {
-        const int tile = base + warp / WPT;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int tile = t0 + pass * kTilesPerPass + warp / WPT;
         const bool live = tile < t1;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         int h = 0, col = 0;
@@ -106,13 +129,13 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
             const float keep = expf(ssm_rate(__ldg(p.A_log + h)) * dt);
             const float4 x4 = *reinterpret_cast<const float4*>(&x_s[(tile - t0) * COLS + 4 * quad]);
             const float4 dx = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
-            const int n0 = (warp % WPT) * share;
-            float* st = p.states + ((static_cast<int64_t>(slot) * p.n_heads + h) * N + n0 + sub) * P + col;
-            for (int k = 0; k < share; k += 4 * kBatchRows) {
-                float4 v[kBatchRows];
+            for (int round = 0; round < rounds; ++round) {
+                const int k = round * 4 * kBatchRows;
 #pragma unroll
-                for (int i = 0; i < kBatchRows; ++i)
-                    if (k + 4 * i < share) v[i] = __ldcs(reinterpret_cast<const float4*>(st + static_cast<int64_t>(k + 4 * i) * P));
+                for (int i = 0; i < kBatchRows; ++i) v[i] = next[i];
+                if (round + 1 < rounds) fetch(pass, round + 1);
+                else if (pass + 1 < passes) fetch(pass + 1, 0);
+                float* st = state_at(tile, k);
 #pragma unroll
                 for (int i = 0; i < kBatchRows; ++i) {
                     if (k + 4 * i >= share) break;
@@ -125,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(const SsmStepParams 
                     acc.y = fmaf(cn, v[i].y, acc.y);
                     acc.z = fmaf(cn, v[i].z, acc.z);
                     acc.w = fmaf(cn, v[i].w, acc.w);
-                    __stcs(reinterpret_cast<float4*>(st + static_cast<int64_t>(k + 4 * i) * P), v[i]);
+                    __stcs(reinterpret_cast<float4*>(st + static_cast<int64_t>(4 * i) * P), v[i]);
                 }
             }
 #pragma unroll

@@ -342,99 +342,101 @@ def gdn_out_norm(out, z, w, eps: float = 1e-6, y=None, stream=None):
 
 # ---- the selective state space layer and the block norm ----
 
-def _rows(t, name, shape, dtype, device):
-    """A tensor of rows: its trailing dimensions contiguous, the rows any distance
-    apart.  Returns (address, elements between rows)."""
+# The checks run on every call, a small one's whole cost: device numbers are compared
+# rather than device objects, and what is wrong is looked up only once something is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(t, name, shape, dtype, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(t, name, shape, dtype, index):
+    """A tensor of rows: its trailing dimensions contiguous, the rows any distance
+    apart.  Returns (address, elements between rows)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(t, name, shape, dtype, index)
     st = t.stride()
-    if (shape[-1] > 1 and st[-1] != 1) or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
+    if (st[-1] != 1 and shape[-1] > 1) or (len(st) == 3 and st[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}'s rows must be contiguous")
     return t.data_ptr(), st[0]
 
 
-def _dense(t, name, shape, dtype, device):
+def _dense(t, name, shape, dtype, index):
     """A contiguous tensor's address, or None for None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(t, name, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _activations(t, name, dims):
-    """Checks the tensor that fixes a call's type and device; returns its dtype number."""
+    """Checks the tensor that fixes a call's type and device; returns its dtype and device numbers."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
-    return _DTYPES[t.dtype]
+    return dt, t.get_device()
 
 
-class _Launch:
-    """The device and stream of one call: the tensors' device is made current if it is
-    not, and what the call allocates belongs to the stream it runs on."""
-
-    __slots__ = ("device", "stream", "ptr", "other")
-
-    def __init__(self, device, stream):
-        self.device = device
-        self.stream = stream
-        self.other = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.ptr = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        mine = torch.cuda.current_stream(self.device)
-        with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(mine)  # the caller goes on to use it there
-        return t
-
-    def __call__(self, fn, *args):
-        if self.other is None:
-            rc = fn(*args, self.ptr)
-        else:
-            with self.other:
-                rc = fn(*args, self.ptr)
-        if rc != GDN_OK:
-            _check(rc)
+def _empty(shape, dtype, index, stream):
+    """Memory that belongs to the stream a call runs on (None: the current one)."""
+    device = torch.device("cuda", index)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    mine = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(mine)  # the caller goes on to use it there
+    return t
 
 
-def _seqs(cu_seqlens, slots, has_state, pool, device):
+def _launch(fn, index, stream, *args):
+    """Calls fn(*args, stream) with the tensors' device current."""
+    if stream is None:
+        ptr = _raw_stream(index)
+    else:
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+        ptr = stream.cuda_stream
+    if _current_device() == index:
+        rc = fn(*args, ptr)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, ptr)
+    if rc != GDN_OK:
+        _check(rc)
+
+
+def _seqs(cu_seqlens, slots, has_state, pool, index):
     """(cu, slots, has_state, n_seq, n_slots) of a packed call; pool: its states or history, or None."""
     i32 = torch.int32
     n = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     if n < 0:
         raise ValueError("cu_seqlens needs one element at least")
-    if has_state is not None and has_state.dtype == torch.bool:
+    if has_state is not None and has_state.dtype is torch.bool:
         has_state = has_state.view(torch.uint8)
     n_slots = 0 if pool is None else pool.shape[0]
     if pool is not None and slots is None and n_slots < n:
         raise ValueError(f"{n} sequences but {n_slots} slots")
-    return (_dense(cu_seqlens, "cu_seqlens", (n + 1,), i32, device), _dense(slots, "slots", (n,), i32, device),
-            _dense(has_state, "has_state", (n,), torch.uint8, device), n, n_slots)
+    return (_dense(cu_seqlens, "cu_seqlens", (n + 1,), i32, index), _dense(slots, "slots", (n,), i32, index),
+            _dense(has_state, "has_state", (n,), torch.uint8, index), n, n_slots)
 
 
 def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_state=None, activation: int = 1,
@@ -450,8 +452,8 @@ def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_st
     continue from their slots).  ``out`` ([T][channels]) is allocated if None; rows
     of no sequence are left as they were.
     """
-    dt = _activations(x, "x", 2)
-    dev, (T, ch) = x.device, x.shape
+    dt, dev = _activations(x, "x", 2)
+    T, ch = x.shape
     xp, xs = _rows(x, "x", (T, ch), x.dtype, dev)
     if w.dim() != 2:
         raise ValueError("w must have 2 dimensions")
@@ -462,12 +464,12 @@ def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_st
         raise ValueError("hist must have 3 dimensions")
     hp = None if hist is None else _dense(hist, "hist", (hist.shape[0], width - 1, ch), x.dtype, dev)
     cu, sl, has, n, n_slots = _seqs(cu_seqlens, slots, has_state, hist, dev)
-    go = _Launch(dev, stream)
     if out is None:
-        out = go.empty((T, ch), x.dtype)
+        out = _empty((T, ch), x.dtype, dev, stream)
     op, os_ = _rows(out, "out", (T, ch), x.dtype, dev)
-    go(load_library().gdn_ssm_conv, xp, xs, wp, bp, hp, cu, sl, has, n, n_slots, op, max(os_, ch) if T <= 1 else os_, T,
-       ch, width, activation, dt)
+    lib = _lib or load_library()
+    _launch(lib.gdn_ssm_conv, dev, stream, xp, xs, wp, bp, hp, cu, sl, has, n, n_slots, op,
+            max(os_, ch) if T <= 1 else os_, T, ch, width, activation, dt)
     return out
 
 
@@ -483,10 +485,10 @@ def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seq
     nothing is kept).  Head h reads group h % n_groups.  cu_seqlens, slots, has_state
     as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.
     """
-    dt = _activations(x, "x", 3)
+    dt, dev = _activations(x, "x", 3)
     if B.dim() != 3:
         raise ValueError("B must have 3 dimensions")
-    dev, ty, f32 = x.device, x.dtype, torch.float32
+    ty, f32 = x.dtype, torch.float32
     T, H, P = shape = x.shape
     G, N = B.shape[1], B.shape[2]
     xp, xs = _rows(x, "x", shape, ty, dev)
@@ -499,15 +501,21 @@ def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seq
     dp = _dense(D, "D", (H,), f32, dev)
     sp = None if states is None else _dense(states, "states", (states.shape[0], H, N, P), f32, dev)
     cu, sl, has, n, n_slots = _seqs(cu_seqlens, slots, has_state, states, dev)
-    go = _Launch(dev, stream)
     if out is None:
-        out = go.empty(shape, ty)
+        out = _empty(shape, ty, dev, stream)
     op, os_ = _rows(out, "out", shape, ty, dev)
-    lib = load_library()
-    need = lib.gdn_ssm_scan_workspace_bytes(T, n, H, P, N, dt)
-    ws = go.empty((need,), torch.uint8) if need else None
-    go(lib.gdn_ssm_scan, xp, xs, ap, as_, bp, bs, cp, cs, zp, zs, alp, dbp, dp, sp, cu, sl, has, n, n_slots, op,
-       max(os_, H * P) if T <= 1 else os_, T, H, G, P, N, dt, None if ws is None else ws.data_ptr(), need)
+    lib = _lib or load_library()
+    need = 0
+    if dt != GDN_F32:  # (asked with the tensors' device current: it goes by its multiprocessors)
+        if _current_device() == dev:
+            need = lib.gdn_ssm_scan_workspace_bytes(T, n, H, P, N, dt)
+        else:
+            with torch.cuda.device(dev):
+                need = lib.gdn_ssm_scan_workspace_bytes(T, n, H, P, N, dt)
+    ws = _empty((need,), torch.uint8, dev, stream) if need else None
+    _launch(lib.gdn_ssm_scan, dev, stream, xp, xs, ap, as_, bp, bs, cp, cs, zp, zs, alp, dbp, dp, sp, cu, sl, has, n,
+            n_slots, op, max(os_, H * P) if T <= 1 else os_, T, H, G, P, N, dt,
+            None if ws is None else ws.data_ptr(), need)
     return out
 
 
@@ -523,10 +531,10 @@ def gdn_ssm_step(xbc, a, conv_w, A_log, dt_bias, hist, states, conv_bias=None, D
     [batch] int32 (None: request i has slot i; -1: a padding row, left out).  ``out``
     ([batch][n_heads][head_dim]) is allocated if None.
     """
-    dt = _activations(xbc, "xbc", 2)
+    dt, dev = _activations(xbc, "xbc", 2)
     if states.dim() != 4 or conv_w.dim() != 2 or hist.dim() != 3:
         raise ValueError("states must have 4 dimensions, hist 3 and conv_w 2")
-    dev, ty, f32 = xbc.device, xbc.dtype, torch.float32
+    ty, f32 = xbc.dtype, torch.float32
     n, cw = xbc.shape
     n_slots, H, N, P = states.shape
     width = conv_w.shape[1]
@@ -545,12 +553,12 @@ def gdn_ssm_step(xbc, a, conv_w, A_log, dt_bias, hist, states, conv_bias=None, D
     hp = _dense(hist, "hist", (n_slots, width - 1, cw), ty, dev)
     sp = _dense(states, "states", (n_slots, H, N, P), f32, dev)
     sl = _dense(slots, "slots", (n,), torch.int32, dev)
-    go = _Launch(dev, stream)
     if out is None:
-        out = go.empty((n, H, P), ty)
+        out = _empty((n, H, P), ty, dev, stream)
     op, os_ = _rows(out, "out", (n, H, P), ty, dev)
-    go(load_library().gdn_ssm_step, xp, xs, ap, as_, zp, zs, wp, bp, alp, dbp, dp, hp, sp, sl, n_slots, op,
-       max(os_, H * P) if n <= 1 else os_, n, H, G, P, N, width, activation, dt)
+    lib = _lib or load_library()
+    _launch(lib.gdn_ssm_step, dev, stream, xp, xs, ap, as_, zp, zs, wp, bp, alp, dbp, dp, hp, sp, sl, n_slots, op,
+            max(os_, H * P) if n <= 1 else os_, n, H, G, P, N, width, activation, dt)
     return out
 
 
@@ -565,9 +573,9 @@ def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: boo
     w_post (or None: b as it is): [dim] FP32.  The residual is updated in place unless
     ``residual_out`` is given; ``out`` ([T][dim] of b's type) is allocated if None.
     """
-    dt = _activations(b, "b", 2)
-    rt = _activations(residual, "residual", 2)
-    dev, ty, f32 = b.device, b.dtype, torch.float32
+    dt, dev = _activations(b, "b", 2)
+    rt, _ = _activations(residual, "residual", 2)
+    ty, f32 = b.dtype, torch.float32
     shape = T, d = b.shape
     bp, bs = _rows(b, "b", shape, ty, dev)
     rp, rs = _rows(residual, "residual", shape, residual.dtype, dev)
@@ -581,18 +589,18 @@ def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: boo
     if wpre is None:
         raise TypeError("w_pre must be a torch.Tensor")
     wpost = _dense(w_post, "w_post", (d,), f32, dev)
-    go = _Launch(dev, stream)
     if residual_out is None:
         residual_out, qp, qs = residual, rp, rs
     else:
         qp, qs = _rows(residual_out, "residual_out", shape, residual.dtype, dev)
     if out is None:
-        out = go.empty(shape, ty)
+        out = _empty(shape, ty, dev, stream)
     op, os_ = _rows(out, "out", shape, ty, dev)
     if T <= 1:
         qs, os_, rs = max(qs, d), max(os_, d), max(rs, d)
-    go(load_library().gdn_block_norm, bp, bs, rp, rs, gp, gs, 1 if gate_sigmoid else 0, wpost, wpre, scale, eps, qp, qs,
-       op, os_, T, d, dt, rt)
+    lib = _lib or load_library()
+    _launch(lib.gdn_block_norm, dev, stream, bp, bs, rp, rs, gp, gs, 1 if gate_sigmoid else 0, wpost, wpre, scale, eps,
+            qp, qs, op, os_, T, d, dt, rt)
     return residual_out, out
 
 
