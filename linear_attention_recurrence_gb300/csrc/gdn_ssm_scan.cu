@@ -6,21 +6,21 @@
 //
 // This form takes every type and size; the tensor-core form (gdn_ssm_scan_tc.cu) takes
 // long 16-bit prompts.  Bound by FP32 arithmetic: 3 packed operations per 2 state
-// elements and token (decay, update, output).  The columns of S are independent, so a
-// CTA of 128 threads holds 32 columns of one head's state in registers: thread
-// (row group rg, column pair cp) has state_dim / 8 rows of 2 columns, packed along the
-// rows, so B and C come as pairs from shared memory and serve both columns.  Tokens
-// are staged in blocks of 16, double-buffered; there is no feedback from the output,
-// so a block's partial sums over the 8 row groups meet once per block (a shuffle, then
-// 4 partials in shared memory, in a fixed order).  A token's arithmetic does not depend
-// on its place in the call: a sequence split over calls gives the same bits.
+// elements and token (decay, update, output), and by their latency where sequences x heads
+// are few.  The columns of S are independent, so a CTA holds 32 columns of one head's state
+// in registers: thread (row group rg, column pair cp) has 8 rows (4 or 2 of a small state)
+// of 2 columns, packed along the rows, so B and C come as vectors from shared memory and
+// serve both columns.  Tokens are staged in blocks of 16, double-buffered; there is no
+// feedback from the output, so a block's partial sums over the row groups meet once per
+// block (a shuffle, then one partial per warp in shared memory, in a fixed order).  A
+// token's arithmetic does not depend on its place in the call: a sequence split over calls
+// gives the same bits.  48 heads of 128 x 128, 77 tokens in FP32: see kRows.
 #include "gdn_ssm.cuh"
 #include "gdn_ssm.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 128;
 constexpr int TB = 16;   // tokens per staged block
 constexpr int COLS = 32;  // state columns per CTA
 
@@ -37,10 +37,14 @@ __device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
     }
 }
 
-template <class T, int NR, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScanParams p, const SsmSeqs q) {
-    constexpr int N = 8 * NR;
-    __shared__ __align__(16) float Bs[2][TB][N], Cs[2][TB][N], xs[2][TB][COLS], yp[4][TB][COLS];
+// N: state_dim, NR: rows of it a thread holds.
+template <class T, int N, int NR, bool ALIGNED>
+__global__ void __launch_bounds__(N / NR * 16) ssm_scan_tokens_kernel(const SsmScanParams p, const SsmSeqs q) {
+    constexpr int kThreads = N / NR * 16, kWarps = kThreads / 32;
+    constexpr int TPT = kThreads / TB;               // threads that stage a token,
+    constexpr int SN = N / TPT, SX = COLS / TPT;     // this many state rows and columns each
+    static_assert(SN % 2 == 0 && SX % 2 == 0 && NR % 2 == 0, "staged and held in pairs");
+    __shared__ __align__(16) float Bs[2][TB][N], Cs[2][TB][N], xs[2][TB][COLS], yp[kWarps][TB][COLS];
     __shared__ float2 gate[2][TB];  // decay, dt
     const int slices = p.head_dim / COLS;
     int64_t id = blockIdx.x;
@@ -54,12 +58,12 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = tid >> 4, cp = tid & 15;
-    const int lt = tid >> 3, lc = tid & 7;  // staging: token lt, NR state rows / 4 columns from lc
-    const T* x = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * p.head_dim + c0 + 4 * lc;
-    const T* z = p.z ? static_cast<const T*>(p.z) + static_cast<int64_t>(h) * p.head_dim + c0 + 4 * lc : nullptr;
-    T* y = static_cast<T*>(p.y) + static_cast<int64_t>(h) * p.head_dim + c0 + 4 * lc;
-    const T* Bp = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * N + NR * lc;
-    const T* Cp = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * N + NR * lc;
+    const int lt = tid / TPT, lc = tid % TPT;
+    const T* x = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * p.head_dim + c0 + SX * lc;
+    const T* z = p.z ? static_cast<const T*>(p.z) + static_cast<int64_t>(h) * p.head_dim + c0 + SX * lc : nullptr;
+    T* y = static_cast<T*>(p.y) + static_cast<int64_t>(h) * p.head_dim + c0 + SX * lc;
+    const T* Bp = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * N + SN * lc;
+    const T* Cp = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * N + SN * lc;
     const T* ap = static_cast<const T*>(p.a) + h;
     const float A = ssm_rate(__ldg(p.A_log + h)), bias = __ldg(p.dt_bias + h), D = p.D ? __ldg(p.D + h) : 0.f;
 
@@ -78,15 +82,15 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
         S[1][i] = make_float2(u.y, v.y);
     }
 
-    float fb[NR], fc[NR], fx[4], fz[4];
+    float fb[SN], fc[SN], fx[SX], fz[SX];
     float2 fg = make_float2(1.f, 0.f);
     auto fetch = [&](int64_t t0) {
         const int64_t t = t0 + lt;
         if (t < e) {
-            load_n<T, NR, ALIGNED>(Bp + t * p.b_stride, fb);
-            load_n<T, NR, ALIGNED>(Cp + t * p.c_stride, fc);
-            load_n<T, 4, ALIGNED>(x + t * p.x_stride, fx);
-            if (z) load_n<T, 4, ALIGNED>(z + t * p.z_stride, fz);
+            load_n<T, SN, ALIGNED>(Bp + t * p.b_stride, fb);
+            load_n<T, SN, ALIGNED>(Cp + t * p.c_stride, fc);
+            load_n<T, SX, ALIGNED>(x + t * p.x_stride, fx);
+            if (z) load_n<T, SX, ALIGNED>(z + t * p.z_stride, fz);
         }
         if (tid < TB && t0 + tid < e) {
             const float dt = ssm_softplus(to_f<T>(ap[(t0 + tid) * p.a_stride]) + bias);
@@ -95,11 +99,12 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
     };
     auto stage = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < NR; i += 2) {
-            *reinterpret_cast<float2*>(&Bs[buf][lt][NR * lc + i]) = make_float2(fb[i], fb[i + 1]);
-            *reinterpret_cast<float2*>(&Cs[buf][lt][NR * lc + i]) = make_float2(fc[i], fc[i + 1]);
+        for (int i = 0; i < SN; i += 2) {
+            *reinterpret_cast<float2*>(&Bs[buf][lt][SN * lc + i]) = make_float2(fb[i], fb[i + 1]);
+            *reinterpret_cast<float2*>(&Cs[buf][lt][SN * lc + i]) = make_float2(fc[i], fc[i + 1]);
         }
-        *reinterpret_cast<float4*>(&xs[buf][lt][4 * lc]) = make_float4(fx[0], fx[1], fx[2], fx[3]);
+#pragma unroll
+        for (int i = 0; i < SX; i += 2) *reinterpret_cast<float2*>(&xs[buf][lt][SX * lc + i]) = make_float2(fx[i], fx[i + 1]);
         if (tid < TB) gate[buf][tid] = fg;
     };
     fetch(b);
@@ -108,9 +113,9 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
     int buf = 0;
     for (int64_t t0 = b; t0 < e; t0 += TB, buf ^= 1) {
         const int nv = e - t0 < TB ? static_cast<int>(e - t0) : TB;
-        float dx[4], zc[4];  // this thread's outputs of the block: D x and z
+        float dx[SX], zc[SX];  // this thread's outputs of the block: D x and z
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < SX; ++j) {
             dx[j] = D * fx[j];
             zc[j] = fz[j];
         }
@@ -153,11 +158,14 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
         };
         // 4 tokens between the sums over the warp's two row groups, so that those overlap
         for (int t = 0; t < nv; t += 4) {
-            float r0[4], r1[4];
+            float r0[4] = {}, r1[4] = {};
+            if (t + 4 <= nv) {  // (no branch between the tokens: their loads move up)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                r0[k] = r1[k] = 0.f;
-                if (t + k < nv) token(t + k, r0[k], r1[k]);
+                for (int k = 0; k < 4; ++k) token(t + k, r0[k], r1[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (t + k < nv) token(t + k, r0[k], r1[k]);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -169,19 +177,22 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
         if (more) stage(buf ^ 1);
         __syncthreads();
         if (lt < nv) {
-            float o[4];
+            float o[SX];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = 4 * lc + j;
-                o[j] = ((yp[0][lt][k] + yp[1][lt][k]) + (yp[2][lt][k] + yp[3][lt][k])) + dx[j];
+            for (int j = 0; j < SX; ++j) {
+                const int k = SX * lc + j;
+                float sum = yp[0][lt][k];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) sum += yp[w][lt][k];
+                o[j] = sum + dx[j];
                 if (z) o[j] *= ssm_silu(zc[j]);
             }
             T* out = y + (t0 + lt) * p.y_stride;
             if constexpr (ALIGNED) {
-                store_vec<T, 4>(out, o);
+                store_vec<T, SX>(out, o);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) out[j] = from_f<T>(o[j]);
+                for (int j = 0; j < SX; ++j) out[j] = from_f<T>(o[j]);
             }
         }
         __syncthreads();  // yp is read; the next block may overwrite it
@@ -196,9 +207,9 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_tokens_kernel(const SsmScan
     }
 }
 
-template <class T, int NR>
+template <class T, int N, int NR>
 void launch_n(const SsmScanParams& p, const SsmSeqs& q, cudaStream_t s) {
-    // rows start on 16-byte boundaries: the 4-column and NR-row pieces are then aligned vectors
+    // rows start on 16-byte boundaries: the pieces that threads stage are then aligned vectors
     auto fits = [](const void* ptr, int64_t stride) {
         return (reinterpret_cast<uintptr_t>(ptr) | static_cast<uintptr_t>(stride * static_cast<int64_t>(sizeof(T)))) % 16 == 0;
     };
@@ -206,18 +217,21 @@ void launch_n(const SsmScanParams& p, const SsmSeqs& q, cudaStream_t s) {
                          fits(p.y, p.y_stride) && (!p.z || fits(p.z, p.z_stride));
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.n_seq) * p.n_heads * (p.head_dim / COLS));
     if (aligned)
-        ssm_scan_tokens_kernel<T, NR, true><<<grid, kThreads, 0, s>>>(p, q);
+        ssm_scan_tokens_kernel<T, N, NR, true><<<grid, N / NR * 16, 0, s>>>(p, q);
     else
-        ssm_scan_tokens_kernel<T, NR, false><<<grid, kThreads, 0, s>>>(p, q);
+        ssm_scan_tokens_kernel<T, N, NR, false><<<grid, N / NR * 16, 0, s>>>(p, q);
 }
 
+// Rows a thread holds of a large state: 8, so that a lone sequence's CTAs have 8 warps (16 rows
+// and 4 warps take a fifth longer there, and a tenth less with many sequences).
+constexpr int kRows = 8;
 template <class T>
 void launch_t(const SsmScanParams& p, const SsmSeqs& q, cudaStream_t s) {
     switch (p.state_dim) {
-        case 16: launch_n<T, 2>(p, q, s); break;
-        case 32: launch_n<T, 4>(p, q, s); break;
-        case 64: launch_n<T, 8>(p, q, s); break;
-        default: launch_n<T, 16>(p, q, s); break;
+        case 16: launch_n<T, 16, 2>(p, q, s); break;
+        case 32: launch_n<T, 32, 4>(p, q, s); break;
+        case 64: launch_n<T, 64, kRows / 2>(p, q, s); break;
+        default: launch_n<T, 128, kRows>(p, q, s); break;
     }
 }
 
