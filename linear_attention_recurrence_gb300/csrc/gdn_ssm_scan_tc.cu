@@ -66,9 +66,9 @@ static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form")
 enum {
     B_FULL, B_GATE = B_FULL + kStages, B_EMPTY = B_GATE + kStages,
     B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE, B_Y2FREE,
-    B_XW,             // [kXwSlots <= 4]
-    B_XWFREE = B_XW + 4,
-    B_TAIL = B_XWFREE + 4,
+    B_XW,             // [8]
+    B_XWFREE = B_XW + 8,
+    B_TAIL = B_XWFREE + 8,
     B_FIN,
     NBAR
 };
@@ -238,8 +238,9 @@ __device__ __forceinline__ float range_scale(float v) {
 // arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 18 : 5;
-    if (b == B_GFREE || b == B_M0 || b == B_M1 || b == B_H || b == B_TAIL) return 4;
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 18 : 17;
+    if (b == B_H || b == B_TAIL) return out ? 4 : 16;
+    if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
     if (b == B_Y1FREE || b == B_Y2FREE) return 8;
     if (b == B_FIN) return out ? 2 : 1;
     if (b >= B_XW && b < B_XWFREE) return 4;
@@ -280,6 +281,13 @@ __device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
 // instructions behind a wait need a converged warp).
 __device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
     return __all_sync(0xffffffffu, wait_phase(s, b, n)) != 0;
+}
+// True in one lane of a converged warp.  (Not `lane == 0`: behind this predicate the compiler
+// knows one lane runs and keeps the operands of MMAs and copies in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 // Every MMA of the CTA ends before tensor memory is freed.
 __device__ __forceinline__ void finish_mma(uint64_t* bar) {
@@ -353,8 +361,11 @@ template <bool BF16, int P, int N, int PASS>
 __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid_constant__ TcParams p) {
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     constexpr int PARTS = BF16 ? 3 : 2;
-    constexpr int SLOTS = 64 / (8 * PARTS);
     constexpr bool OUT = PASS == 0;
+    // PASS 1 has tensor memory for 8 blocks' parts, and all 16 working warps to form them
+    constexpr int SLOTS = OUT ? 64 / (8 * PARTS) : 8;
+    constexpr uint32_t TM_PARTS = OUT ? TM_XW : TM_HB;
+    constexpr int X_FIRST = OUT ? 1 : 0, X_GROUPS = OUT ? 1 : 4;
     constexpr int NB = N / 64, PB = P / 64;
     unsigned char* sm = aligned_dynamic_smem<unsigned char, 1024>();
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
     int* warp_sum = reinterpret_cast<int*>(sm + SM_GATE);  // before the gates are written
     const Sync sy{bar, abort_flag, p.status};
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     const int h = blockIdx.x % p.n_heads;
     const int64_t u = blockIdx.x / p.n_heads;
@@ -382,10 +393,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tm = *tmem_slot;
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp == kCopyWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             int c = 0;
             for (; c < nch; ++c) {
                 const int s = c % kStages;
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
         }
     } else if (warp == kMmaWarp) {
-        if (OUT && lane == 0) {
+        if (OUT && elect_one()) {
             constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
             constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
             constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 128, false, false);
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             finish_mma(&bar[B_FIN]);
         }
     } else if (warp == kStateMmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ID_S = idesc_f16(BF16, 128, N, false, true);     // B: N-major
             const uint32_t sm0 = smem_addr(sm);
             uint32_t qi = 0;
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     tc_fence_after_sync();
                     const uint64_t b = desc_mn(sm0 + s * SM_STAGE + SM_B + j * 2048);
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) mma_ts(tm + TM_H, tm + TM_XW + (slot * PARTS + i) * 8, b, ID_S, true);
+                    for (int i = 0; i < PARTS; ++i) mma_ts(tm + TM_H, tm + TM_PARTS + (slot * PARTS + i) * 8, b, ID_S, true);
                     umma_commit(&bar[B_XWFREE + slot]);
                 }
                 if (!ok) break;
@@ -563,7 +574,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             warp_arrive(sy, B_GATE + s);
         }
         if (PASS == 1 && lane == 31) p.ws_decay[u * p.n_heads + h] = exp2f(seg_sum);
-    } else if (warp < 4) {
+    } else if (OUT && warp < 4) {
         if constexpr (OUT) {
             // ---- M: lane = token t ----
             const int t = tid;
@@ -621,11 +632,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 warp_arrive(sy, B_EMPTY + s);
             }
         }
-    } else if (warp < 8) {
-        // ---- the state, and the parts of w o x: lane = column pcol of x ----
-        const int wq = warp - 4, pcol = wq * 32 + lane;
+    } else if (warp < 4 * (X_FIRST + X_GROUPS)) {
+        // ---- the state, and the parts of w o x: X_GROUPS groups of 4 warps, lane = column pcol of x.
+        // Group xg takes every X_GROUPS-th block of 16 tokens and the state rows n0, n0 + 32 X_GROUPS, .. ----
+        const int wq = warp & 3, xg = (warp >> 2) - X_FIRST, pcol = wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const bool live = wq * 32 < P;
+        const bool live = wq * 32 < P;  // uniform in a warp
         const int slot = p.states ? seq_slot(p.q, un.s) : -1;
         float* pool = p.states + (static_cast<int64_t>(slot) * p.n_heads + h) * N * P + pcol;
         if (live) {
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             float* first = p.ws + ((u - un.k) * p.n_heads + h) * N * P + pcol;  // segment 0's contribution
             float* kept = first + (un.n_seg - 1) * unit_floats;  // the state before the sequence, left by PASS 1
 #pragma unroll 1
-            for (int n0 = 0; n0 < N; n0 += 32) {
+            for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -664,7 +676,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             tmem_wait_st();
         }
         const uint32_t x_frag = frag_offset(wq * 32, lane), x_frag1 = frag_offset(wq * 32 + 16, lane);
-        uint32_t qi = 0;
         bool ok = true;
         float scale = 1.f;  // tensor memory holds H / scale
         for (int c = 0; ok && c < nch; ++c) {
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             if (nv < L) {
                 // rows behind the segment's end (another sequence's, which may hold anything) become
                 // zeros in x and B, the operands whose rows are summed over
-                for (int i = tid - 128; i < (L - nv) * 8; i += 128) {
+                for (int i = tid - 128 * X_FIRST; i < (L - nv) * 8; i += 128 * X_GROUPS) {
                     const uint32_t off = (nv + i / 8) * 128 + (i % 8) * 16;
 #pragma unroll
                     for (int k = 0; k < PB; ++k) *reinterpret_cast<uint4*>(st + SM_X + k * kBox + off) = make_uint4(0, 0, 0, 0);
@@ -688,67 +699,82 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 warp_arrive(sy, B_TAIL);
                 if (!wait_warp(sy, B_TAIL, 0)) break;
             }
-            if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) break;
-            tc_fence_after_sync();
             const float next_scale = BF16 ? 1.f : gt[512];
-            if (live) {
-                const float keep = gt[384 + L - 1] * (scale * (1.0f / next_scale));
-#pragma unroll 1
-                for (int n0 = 0; n0 < N; n0 += 32) {
-                    float v[32];
-                    tmem_ld32(tm + lanes + TM_H + n0, v);
-                    if constexpr (OUT) {
-                        uint32_t o[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = BF16 ? pack2<BF16>(v[2 * i], v[2 * i + 1]) : pack2<BF16>(v[2 * i] * scale, v[2 * i + 1] * scale);
-                        tmem_st_u16(tm + lanes + TM_HB + n0 / 2, o);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= keep;
-                    tmem_st32(tm + lanes + TM_H + n0, v);
-                }
-                tmem_wait_st();
-            }
-            scale = next_scale;
-            tc_fence_before_sync();
-            warp_arrive(sy, B_H);
-#pragma unroll 1
-            for (int j = 0; j < L / 16; ++j, ++qi) {
-                const int xs = qi % SLOTS;
-                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
-                    ok = false;
-                    break;
-                }
+            // the state's decay, and its rounding for the product with C
+            auto state_step = [&]() {
+                if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) return false;
                 tc_fence_after_sync();
+                if (live) {
+                    const float keep = gt[384 + L - 1] * (scale * (1.0f / next_scale));
+#pragma unroll 1
+                    for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
+                        float v[32];
+                        tmem_ld32(tm + lanes + TM_H + n0, v);
+                        if constexpr (OUT) {
+                            uint32_t o[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = BF16 ? pack2<BF16>(v[2 * i], v[2 * i + 1]) : pack2<BF16>(v[2 * i] * scale, v[2 * i + 1] * scale);
+                            tmem_st_u16(tm + lanes + TM_HB + n0 / 2, o);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= keep;
+                        tmem_st32(tm + lanes + TM_H + n0, v);
+                    }
+                    tmem_wait_st();
+                }
+                scale = next_scale;
+                tc_fence_before_sync();
+                warp_arrive(sy, B_H);
+                return true;
+            };
+            // with few slots the state goes first, with many the parts (they then wait for no update)
+            if (OUT && !state_step()) break;
+#pragma unroll 1
+            for (int j = xg; j < L / 16; j += X_GROUPS) {
+                // the parts are formed before the wait for their slot
+                uint32_t part[2][PARTS][4];
                 if (live) {
                     const uint32_t x = smem_addr(st) + SM_X + j * 2048;
                     const float2 w0 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 2 * (lane & 3));
                     const float2 w1 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 8 + 2 * (lane & 3));
 #pragma unroll
                     for (int g2 = 0; g2 < 2; ++g2) {
-                        uint32_t xr[4], part[PARTS][4];
+                        uint32_t xr[4];
                         ldsm4t(x + (g2 ? x_frag1 : x_frag), xr);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float2 f = fmul2(unpack2<BF16>(xr[k]), k < 2 ? w0 : w1);
 #pragma unroll
                             for (int q = 0; q < PARTS; ++q) {
-                                part[q][k] = pack2<BF16>(f.x, f.y);
-                                const float2 back = unpack2<BF16>(part[q][k]);
+                                part[g2][q][k] = pack2<BF16>(f.x, f.y);
+                                const float2 back = unpack2<BF16>(part[g2][q][k]);
                                 f = fadd2(f, make_float2(-back.x, -back.y));
                             }
                         }
+                    }
+                }
+                const uint32_t qi = c * (L / 16) + j, xs = qi % SLOTS;
+                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                if (live) {
+#pragma unroll
+                    for (int g2 = 0; g2 < 2; ++g2)
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q)
-                            tmem_st_frag(tm + lanes + (g2 << 20) + TM_XW + (xs * PARTS + q) * 8, part[q]);
-                    }
+                            tmem_st_frag(tm + lanes + (g2 << 20) + TM_PARTS + (xs * PARTS + q) * 8, part[g2][q]);
                     tmem_wait_st();
                 }
                 tc_fence_before_sync();
                 warp_arrive(sy, B_XW + xs);
             }
-            if (!ok) break;
+            if (!ok || (!OUT && !state_step())) {
+                ok = false;
+                break;
+            }
             warp_arrive(sy, B_EMPTY + s);
         }
         // the state behind the segment
@@ -758,7 +784,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             float* dst = PASS == 1 ? p.ws + (u * p.n_heads + h) * N * P + pcol : pool;
             if (live) {
 #pragma unroll 1
-                for (int n0 = 0; n0 < N; n0 += 32) {
+                for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                     float v[32];
                     tmem_ld32(tm + lanes + TM_H + n0, v);
 #pragma unroll
@@ -789,7 +815,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             // z of this warp's 4 blocks of a half chunk, a half ahead of their use (from L2, where the copy
             // warp has them fetched with the chunk's other operands): one batch, because a wait for the
             // oldest of several loads is a wait for all of them
-            uint4 zn[4], zc[4];
+            uint4 zn[4];
             auto load_z = [&](int t) {
                 if (!gated || !live) return;
 #pragma unroll
@@ -810,28 +836,33 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
+                    // silu(z) of the half's 4 blocks, while the products are on their way
+                    float2 gz[4][4];
+                    if (gated && live) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t zr[4];
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zn[i].x), "r"(zn[i].y),
+                                         "r"(zn[i].z), "r"(zn[i].w)
+                                         : "memory");
+                            __syncwarp();
+                            ldsm4t(io_frag, zr);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) gz[i][k] = silu2(unpack2<BF16>(zr[k]));
+                            __syncwarp();
+                        }
+                        load_z(c * L + 64 * half + 64 + 8 * odd);
+                    }
                     ok = wait_warp(sy, B_Y1, yi++);
                     if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) zc[i] = zn[i];
-                    load_z(c * L + 64 * half + 64 + 8 * odd);
                     tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int t0 = 64 * half + 16 * i + 8 * odd;
                         const bool some = live && t0 < nv;
-                        uint32_t zr[4], xr[4], yr[4];
+                        uint32_t xr[4], yr[4];
                         float2 e2, y1[4], y2[4];
                         if (some) {
-                            if (gated) {
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[0].x), "r"(zc[0].y),
-                                             "r"(zc[0].z), "r"(zc[0].w)
-                                             : "memory");
-                                __syncwarp();
-                                ldsm4t(io_frag, zr);
-#pragma unroll
-                                for (int k = 0; k < 3; ++k) zc[k] = zc[k + 1];  // (a rolled loop: the code of all roles has to fit the caches)
-                            }
                             ldsm4t(x + t0 * 128, xr);
                             e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
@@ -848,10 +879,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 if constexpr (!BF16) o = fmul2(o, make_float2(m_scale, m_scale));
                                 o = ffma2(e2, y2[k], o);
                                 o = ffma2(make_float2(D, D), unpack2<BF16>(xr[k]), o);
-                                if (gated) o = fmul2(o, silu2(unpack2<BF16>(zr[k])));
+                                if (gated) o = fmul2(o, gz[i][k]);
                                 yr[k] = pack2<BF16>(o.x, o.y);
                             }
-                            __syncwarp();  // z is read: the buffer takes y
                             stsm4t(io_frag, yr);
                             __syncwarp();
                             uint4 v;
@@ -861,7 +891,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                          : "memory");
                             const int t = t0 + pt;
                             if (t < nv) __stcs(reinterpret_cast<uint4*>(yp + static_cast<int64_t>(c * L + t) * p.y_stride), v);
-                            __syncwarp();  // y is read: the buffer takes the next block's z
+                            __syncwarp();  // y is read: the buffer is free
                         }
                     }
                 }
