@@ -65,8 +65,9 @@ static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form")
 
 enum {
     B_FULL, B_GATE = B_FULL + kStages, B_EMPTY = B_GATE + kStages,
-    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE, B_Y2FREE,
-    B_XW,             // [8]
+    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE,
+    B_Y2FREE,         // [2], by half
+    B_XW = B_Y2FREE + 2,  // [8]
     B_XWFREE = B_XW + 8,
     B_TAIL = B_XWFREE + 8,
     B_FIN,
@@ -122,11 +123,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
-}
-__device__ __forceinline__ void tmem_st_u8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_u16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -241,11 +237,14 @@ __device__ constexpr int arrivals(int b, bool out) {
     if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 18 : 17;
     if (b == B_H || b == B_TAIL) return out ? 4 : 16;
     if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
-    if (b == B_Y1FREE || b == B_Y2FREE) return 8;
+    if (b == B_Y1FREE || b == B_Y2FREE || b == B_Y2FREE + 1) return 8;
     if (b == B_FIN) return out ? 2 : 1;
-    if (b >= B_XW && b < B_XWFREE) return 4;
+    if (b >= B_XW && b < B_XWFREE) return out ? 4 : 16;
     return 1;
 }
+
+// (out of line: its 4 uses per lane would be most of the gate warp's code)
+__device__ __noinline__ float softplus_call(float v) { return ssm_softplus(v); }
 
 struct Sync {
     uint64_t* bar;
@@ -267,15 +266,18 @@ __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 // Waits for phase `n` (0, 1, ...) of a barrier.  False once some wait of the CTA gave up.
-__device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
-    if (poll(&s.bar[b], n & 1)) return true;
+// (All but the first poll out of line: the code of all roles has to fit the caches.)
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
     for (uint32_t i = 0; i < kTcPolls; ++i) {
-        if (poll(&s.bar[b], n & 1)) return true;
-        if (*s.abort_flag) return false;
+        if (poll(bar, parity)) return true;
+        if (*abort_flag) return false;
     }
-    *s.abort_flag = 1;
-    report_timeout(s.status);
+    *abort_flag = 1;
+    report_timeout(status);
     return false;
+}
+__device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
+    return poll(&s.bar[b], n & 1) || wait_more(&s.bar[b], n & 1, s.abort_flag, s.status);
 }
 // The same for a whole warp: all lanes leave together, with one answer (the tensor-memory
 // instructions behind a wait need a converged warp).
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     constexpr int SLOTS = OUT ? 64 / (8 * PARTS) : 8;
     constexpr uint32_t TM_PARTS = OUT ? TM_XW : TM_HB;
     constexpr int X_FIRST = OUT ? 1 : 0, X_GROUPS = OUT ? 1 : 4;
+    constexpr int GROUP = OUT ? 1 : 4;  // blocks whose parts share a barrier
     constexpr int NB = N / 64, PB = P / 64;
     unsigned char* sm = aligned_dynamic_smem<unsigned char, 1024>();
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
@@ -426,17 +429,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         if (OUT && elect_one()) {
             constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
             constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
-            constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 128, false, false);
+            constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 64, false, false);
             const uint32_t sm0 = smem_addr(sm);
             uint32_t gi = 0, yi = 0;
             auto issue_g = [&](int c, int half) {  // G's columns of tokens 64 half .. +63
                 if (gi > 0 && !wait_phase(sy, B_GFREE, gi - 1)) return false;
                 tc_fence_after_sync();
                 const uint32_t st = sm0 + (c % kStages) * SM_STAGE;
-#pragma unroll
-                for (int k = 0; k < N / 16; ++k)
-                    mma_ss(tm + TM_G, desc_k(st + SM_C + (k / 4) * kBox + (k % 4) * 32),
-                           desc_k(st + SM_B + (k / 4) * kBox + half * 8192 + (k % 4) * 32), ID_G, k > 0);
+#pragma unroll 1
+                for (int k = 0; k < N / 16; ++k) {
+                    const uint32_t at = (k >> 2) * kBox + (k & 3) * 32;
+                    mma_ss(tm + TM_G, desc_k(st + SM_C + at), desc_k(st + SM_B + half * 8192 + at), ID_G, k > 0);
+                }
                 umma_commit(&bar[B_G]);
                 ++gi;
                 return true;
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if (yi > 0 && !wait_phase(sy, B_Y1FREE, yi - 1)) return false;
                 tc_fence_after_sync();
                 const uint32_t x = sm0 + (c % kStages) * SM_STAGE + SM_X, m = sm0 + SM_M;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 4 + 4 * half; ++k)
                     mma_ss(tm + TM_Y1, desc_mn(x + k * 2048),
                            desc_k(k < 4 ? m + half * 8192 + k * 32 : m + kBox + (k - 4) * 32), ID_Y1, k > 0);
@@ -454,24 +458,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 ++yi;
                 return true;
             };
-            if (wait_phase(sy, B_FULL, 0) && issue_g(0, 0)) {
-                for (int c = 0; c < nch; ++c) {
-                    const int s = c % kStages;
-                    const uint32_t st = sm0 + s * SM_STAGE;
-                    // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
-                    if (!wait_phase(sy, B_H, c) || (c > 0 && !wait_phase(sy, B_Y2FREE, c - 1))) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        mma_ts(tm + TM_Y2, tm + TM_HB + 8 * k, desc_k(st + SM_C + (k / 4) * kBox + (k % 4) * 32), ID_Y2, k > 0);
-                    umma_commit(&bar[B_HBFREE]);
-                    if (!issue_g(c, 1) || !issue_y1(c, 0)) break;
-                    if (c + 1 < nch) {
-                        if (!wait_phase(sy, B_FULL + (c + 1) % kStages, (c + 1) / kStages) || !issue_g(c + 1, 0)) break;
-                    }
-                    if (!issue_y1(c, 1)) break;
+            auto issue_y2 = [&](int c, int half) {
+                if (c > 0 && !wait_phase(sy, B_Y2FREE + half, c - 1)) return false;
+                tc_fence_after_sync();
+                const uint32_t st = sm0 + (c % kStages) * SM_STAGE + SM_C + half * 8192;
+#pragma unroll 1
+                for (int k = 0; k < N / 16; ++k)
+                    mma_ts(tm + TM_Y2 + 64 * half, tm + TM_HB + 8 * k, desc_k(st + (k >> 2) * kBox + (k & 3) * 32), ID_Y2, k > 0);
+                return true;
+            };
+            // Order: H^T C^T, the second half of G, the first half of Y1, H^T C^T, the next chunk's first
+            // half of G, the second half of Y1: what a half of the output needs as soon as the
+            // buffers of the half before are read.  (A loop over the halves: the code of all roles
+            // has to fit the instruction caches.)
+            bool ok = wait_phase(sy, B_FULL, 0) && issue_g(0, 0);
+#pragma unroll 1
+            for (int n = 0; ok && n < 2 * nch; ++n) {
+                const int c = n >> 1, half = n & 1, next = c + half;
+                // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
+                if (half == 0) ok = wait_phase(sy, B_H, c);
+                ok = ok && issue_y2(c, half);
+                if (!ok) break;
+                if (half) umma_commit(&bar[B_HBFREE]);
+                if (next < nch) {
+                    if (half) ok = wait_phase(sy, B_FULL + next % kStages, next / kStages);
+                    ok = ok && issue_g(next, half ^ 1);
+                }
+                ok = ok && issue_y1(c, half);
+                if (half && ok) {
                     umma_commit(&bar[B_MFREE]);
-                    umma_commit(&bar[B_EMPTY + s]);
+                    umma_commit(&bar[B_EMPTY + c % kStages]);
                 }
             }
             finish_mma(&bar[B_FIN]);
@@ -480,19 +496,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         if (elect_one()) {
             constexpr uint32_t ID_S = idesc_f16(BF16, 128, N, false, true);     // B: N-major
             const uint32_t sm0 = smem_addr(sm);
-            uint32_t qi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
                 if (!wait_phase(sy, B_FULL + s, c / kStages) || !wait_phase(sy, B_H, c)) break;
-                for (int j = 0; j < L / 16; ++j, ++qi) {
-                    const int slot = qi % SLOTS;
-                    ok = wait_phase(sy, B_XW + slot, qi / SLOTS);
+#pragma unroll 1
+                for (int j = 0; j < L / 16; j += GROUP) {  // GROUP blocks to a barrier
+                    const uint32_t group = (c * (L / 16) + j) / GROUP, slot = group % (SLOTS / GROUP);
+                    ok = wait_phase(sy, B_XW + slot, group / (SLOTS / GROUP));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t b = desc_mn(sm0 + s * SM_STAGE + SM_B + j * 2048);
+#pragma unroll 1
+                    for (int i = 0; i < GROUP; ++i) {
+                        const uint64_t b = desc_mn(sm0 + s * SM_STAGE + SM_B + (j + i) * 2048);
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) mma_ts(tm + TM_H, tm + TM_PARTS + (slot * PARTS + i) * 8, b, ID_S, true);
+                        for (int q = 0; q < PARTS; ++q)
+                            mma_ts(tm + TM_H, tm + TM_PARTS + ((slot * GROUP + i) * PARTS + q) * 8, b, ID_S, true);
+                    }
                     umma_commit(&bar[B_XWFREE + slot]);
                 }
                 if (!ok) break;
@@ -519,7 +539,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool live = c * L + 4 * lane + i < un.len;
-                dt[i] = live ? ssm_softplus(v[i] + bias) : 0.f;
+                dt[i] = live ? softplus_call(v[i] + bias) : 0.f;
                 g2[i] = fmaxf(A * dt[i] * kLog2e, kMinLog2Decay);
                 sum += g2[i];
                 pre[i] = sum;
@@ -546,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             float4* gd = reinterpret_cast<float4*>(gt);
             float w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = dt[i] * exp2f(suf[i]);
+            for (int i = 0; i < 4; ++i) w[i] = dt[i] * ex2(suf[i]);
             if constexpr (!BF16) {
                 float wm = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), dm = fmaxf(fmaxf(dt[0], dt[1]), fmaxf(dt[2], dt[3]));
 #pragma unroll
@@ -569,7 +589,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             gd[2 * lane + 1] = make_float4(pre[2], dt[2], pre[3], dt[3]);
             reinterpret_cast<float4*>(gt + 256)[lane] =
                 make_float4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<float4*>(gt + 384)[lane] = make_float4(exp2f(pre[0]), exp2f(pre[1]), exp2f(pre[2]), exp2f(pre[3]));
+            reinterpret_cast<float4*>(gt + 384)[lane] = make_float4(ex2(pre[0]), ex2(pre[1]), ex2(pre[2]), ex2(pre[3]));
             seg_sum += pre[3];  // lane 31: the chunk's sum
             warp_arrive(sy, B_GATE + s);
         }
@@ -754,8 +774,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         }
                     }
                 }
-                const uint32_t qi = c * (L / 16) + j, xs = qi % SLOTS;
-                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xs, qi / SLOTS - 1)) {
+                const uint32_t qi = c * (L / 16) + j, xs = qi % SLOTS, xb = xs / GROUP;
+                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xb, qi / SLOTS - 1)) {
                     ok = false;
                     break;
                 }
@@ -769,7 +789,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     tmem_wait_st();
                 }
                 tc_fence_before_sync();
-                warp_arrive(sy, B_XW + xs);
+                warp_arrive(sy, B_XW + xb);
             }
             if (!ok || (!OUT && !state_step())) {
                 ok = false;
@@ -825,6 +845,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
             };
             load_z(8 * odd);
+            float2 gz[4];
             uint32_t yi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
@@ -836,52 +857,54 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    // silu(z) of the half's 4 blocks, while the products are on their way
-                    float2 gz[4][4];
-                    if (gated && live) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t zr[4];
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zn[i].x), "r"(zn[i].y),
-                                         "r"(zn[i].z), "r"(zn[i].w)
-                                         : "memory");
-                            __syncwarp();
-                            ldsm4t(io_frag, zr);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) gz[i][k] = silu2(unpack2<BF16>(zr[k]));
-                            __syncwarp();
-                        }
-                        load_z(c * L + 64 * half + 64 + 8 * odd);
-                    }
-                    ok = wait_warp(sy, B_Y1, yi++);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    // blocks i = 0 .. 3 in a rolled loop (the code of all roles has to fit the instruction
+                    // caches); the gates of a block are formed in the iteration before its own, those of
+                    // the first one while its products are on their way
+#pragma unroll 1
+                    for (int i = -1; i < 4; ++i) {
                         const int t0 = 64 * half + 16 * i + 8 * odd;
-                        const bool some = live && t0 < nv;
-                        uint32_t xr[4], yr[4];
-                        float2 e2, y1[4], y2[4];
+                        const bool some = i >= 0 && live && t0 < nv;
+                        uint32_t yr[4];
+                        if (i == 0) {
+                            ok = wait_warp(sy, B_Y1, yi++);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                        }
                         if (some) {
+                            uint32_t xr[4];
+                            float2 y1[4], y2[4];
                             ldsm4t(x + t0 * 128, xr);
-                            e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
+                            const float2 e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
-                        }
-                        if (i == 3) {  // the products are read
-                            tc_fence_before_sync();
-                            warp_arrive(sy, B_Y1FREE);
-                            if (half) warp_arrive(sy, B_Y2FREE);
-                        }
-                        if (some) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 float2 o = y1[k];
                                 if constexpr (!BF16) o = fmul2(o, make_float2(m_scale, m_scale));
                                 o = ffma2(e2, y2[k], o);
                                 o = ffma2(make_float2(D, D), unpack2<BF16>(xr[k]), o);
-                                if (gated) o = fmul2(o, gz[i][k]);
+                                if (gated) o = fmul2(o, gz[k]);
                                 yr[k] = pack2<BF16>(o.x, o.y);
                             }
+                        }
+                        if (i == 3) {  // the products are read
+                            tc_fence_before_sync();
+                            warp_arrive(sy, B_Y1FREE);
+                            warp_arrive(sy, B_Y2FREE + half);
+                        } else if (gated && live) {
+                            uint32_t zr[4];
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zn[0].x), "r"(zn[0].y),
+                                         "r"(zn[0].z), "r"(zn[0].w)
+                                         : "memory");
+                            __syncwarp();
+                            ldsm4t(io_frag, zr);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) zn[k] = zn[k + 1];
+                            if (i == 2) load_z(c * L + 64 * half + 64 + 8 * odd);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) gz[k] = silu2(unpack2<BF16>(zr[k]));
+                            __syncwarp();
+                        }
+                        if (some) {
                             stsm4t(io_frag, yr);
                             __syncwarp();
                             uint4 v;
@@ -894,6 +917,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             __syncwarp();  // y is read: the buffer is free
                         }
                     }
+                    if (!ok) break;
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_EMPTY + s);
