@@ -64,7 +64,9 @@ constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
 enum {
-    B_FULL, B_GATE = B_FULL + kStages, B_EMPTY = B_GATE + kStages,
+    B_FULL, B_XFULL = B_FULL + kStages,                       // B and C, and x, of a stage landed
+    B_GATE = B_XFULL + kStages,
+    B_BCFREE = B_GATE + kStages, B_EMPTY = B_BCFREE + kStages,  // B and C, and x and the gates, are read
     B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE,
     B_Y2FREE,         // [2], by half
     B_XW = B_Y2FREE + 2,  // [8]
@@ -234,7 +236,8 @@ __device__ __forceinline__ float range_scale(float v) {
 // arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 18 : 17;
+    if (b >= B_BCFREE && b < B_EMPTY) return out ? 2 : 1;
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 17 : 16;
     if (b == B_H || b == B_TAIL) return out ? 4 : 16;
     if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
     if (b == B_Y1FREE || b == B_Y2FREE || b == B_Y2FREE + 1) return 8;
@@ -290,6 +293,11 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
     return p != 0;
+}
+// Waits (with a limit) until phase n of a copy's barrier has completed, whatever else happened.
+__device__ __forceinline__ void land(uint64_t* bar, uint32_t n) {
+    for (uint32_t i = 0; i < kTcPolls && !poll(bar, n & 1); ++i) {
+    }
 }
 // Every MMA of the CTA ends before tensor memory is freed.
 __device__ __forceinline__ void finish_mma(uint64_t* bar) {
@@ -400,30 +408,38 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 
     if (warp == kCopyWarp) {
         if (elect_one()) {
-            int c = 0;
-            for (; c < nch; ++c) {
-                const int s = c % kStages;
-                if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+            // B and C are free earlier than x (whose last reader is the output); what is to come is
+            // fetched into L2 two chunks ahead, as is z, which the output reads itself
+            auto rows = [&](const CUtensorMap* map, int x0, int boxes, int row, unsigned char* dst, int b) {
+                for (int i = 0; i < boxes; ++i) {
+                    if (dst) tma_load_2d(dst + i * kBox, map, &bar[b], x0 + 64 * i, row);
+                    else tma_prefetch_2d(map, x0 + 64 * i, row);
+                }
+            };
+            const int row0 = static_cast<int>(un.begin);
+            int bc = 0, xc = 0;
+            for (int c = 0; c < nch; ++c) {
+                const int s = c % kStages, row = row0 + c * L;
                 unsigned char* st = sm + s * SM_STAGE;
-                const int row = static_cast<int>(un.begin) + c * L;
-                mbar_arrive_expect_tx(&bar[B_FULL + s], (OUT ? 2 * NB + PB : NB + PB) * kBox);
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    if (OUT) tma_load_2d(st + SM_C + i * kBox, &p.tm_c, &bar[B_FULL + s], g * N + 64 * i, row);
-                    tma_load_2d(st + SM_B + i * kBox, &p.tm_b, &bar[B_FULL + s], g * N + 64 * i, row);
+                if (c + kStages < nch) {
+                    rows(&p.tm_b, g * N, NB, row + kStages * L, nullptr, 0);
+                    if (OUT) rows(&p.tm_c, g * N, NB, row + kStages * L, nullptr, 0);
+                    rows(&p.tm_x, h * P, PB, row + kStages * L, nullptr, 0);
                 }
-#pragma unroll
-                for (int i = 0; i < PB; ++i)
-                    tma_load_2d(st + SM_X + i * kBox, &p.tm_x, &bar[B_FULL + s], h * P + 64 * i, row);
-                if (OUT && p.z) {
-#pragma unroll
-                    for (int i = 0; i < PB; ++i) tma_prefetch_2d(&p.tm_z, h * P + 64 * i, row);
-                }
+                if (OUT && p.z) rows(&p.tm_z, h * P, PB, row, nullptr, 0);
+                if (c >= kStages && !wait_phase(sy, B_BCFREE + s, c / kStages - 1)) break;
+                mbar_arrive_expect_tx(&bar[B_FULL + s], (OUT ? 2 : 1) * NB * kBox);
+                rows(&p.tm_b, g * N, NB, row, st + SM_B, B_FULL + s);
+                if (OUT) rows(&p.tm_c, g * N, NB, row, st + SM_C, B_FULL + s);
+                ++bc;
+                if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+                mbar_arrive_expect_tx(&bar[B_XFULL + s], PB * kBox);
+                rows(&p.tm_x, h * P, PB, row, st + SM_X, B_XFULL + s);
+                ++xc;
             }
             // the copies in flight land before the CTA ends, also after a wait that gave up
-            for (int i = c > kStages ? c - kStages : 0; i < c; ++i)
-                for (uint32_t n = 0; n < kTcPolls && !poll(&bar[B_FULL + i % kStages], (i / kStages) & 1); ++n) {
-                }
+            for (int i = bc > kStages ? bc - kStages : 0; i < bc; ++i) land(&bar[B_FULL + i % kStages], i / kStages);
+            for (int i = xc > kStages ? xc - kStages : 0; i < xc; ++i) land(&bar[B_XFULL + i % kStages], i / kStages);
         }
     } else if (warp == kMmaWarp) {
         if (OUT && elect_one()) {
@@ -476,10 +492,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int n = 0; ok && n < 2 * nch; ++n) {
                 const int c = n >> 1, half = n & 1, next = c + half;
                 // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
-                if (half == 0) ok = wait_phase(sy, B_H, c);
+                if (half == 0) ok = wait_phase(sy, B_XFULL + c % kStages, c / kStages) && wait_phase(sy, B_H, c);
                 ok = ok && issue_y2(c, half);
                 if (!ok) break;
-                if (half) umma_commit(&bar[B_HBFREE]);
+                if (half) {
+                    umma_commit(&bar[B_HBFREE]);
+                    umma_commit(&bar[B_BCFREE + c % kStages]);
+                }
                 if (next < nch) {
                     if (half) ok = wait_phase(sy, B_FULL + next % kStages, next / kStages);
                     ok = ok && issue_g(next, half ^ 1);
@@ -517,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
                 if (!ok) break;
                 umma_commit(&bar[B_S]);
-                umma_commit(&bar[B_EMPTY + s]);
+                umma_commit(&bar[B_BCFREE + s]);
             }
             finish_mma(&bar[B_FIN]);
         }
@@ -703,9 +722,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             unsigned char* st = sm + s * SM_STAGE;
             const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
             if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
-            if (!wait_warp(sy, B_FULL + s, c / kStages)) break;
+            if (!wait_warp(sy, B_XFULL + s, c / kStages)) break;
             const int nv = un.len - c * L;
             if (nv < L) {
+                if (!wait_warp(sy, B_FULL + s, c / kStages)) break;
                 // rows behind the segment's end (another sequence's, which may hold anything) become
                 // zeros in x and B, the operands whose rows are summed over
                 for (int i = tid - 128 * X_FIRST; i < (L - nv) * 8; i += 128 * X_GROUPS) {
@@ -835,7 +855,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             // z of this warp's 4 blocks of a half chunk, a half ahead of their use (from L2, where the copy
             // warp has them fetched with the chunk's other operands): one batch, because a wait for the
             // oldest of several loads is a wait for all of them
-            uint4 zn[4];
+            uint4 zn[4], zc[4];
             auto load_z = [&](int t) {
                 if (!gated || !live) return;
 #pragma unroll
@@ -845,34 +865,56 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
             };
             load_z(8 * odd);
+            uint32_t zr[4] = {};
             float2 gz[4];
+            auto next_z = [&]() {  // the next block's z as a fragment
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[0].x), "r"(zc[0].y), "r"(zc[0].z),
+                             "r"(zc[0].w)
+                             : "memory");
+                __syncwarp();
+                ldsm4t(io_frag, zr);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) zc[k] = zc[k + 1];
+            };
+            auto gates = [&]() {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gz[k] = silu2(unpack2<BF16>(zr[k]));
+            };
             uint32_t yi = 0;
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
                 const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X + x_frag;
                 const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
-                if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_FULL + s, c / kStages)) break;
+                if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_XFULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : eg[513 - 384];
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    // blocks i = 0 .. 3 in a rolled loop (the code of all roles has to fit the instruction
-                    // caches); the gates of a block are formed in the iteration before its own, those of
-                    // the first one while its products are on their way
+                    // Blocks i = 0 .. 3 in a rolled loop (the code of all roles has to fit the instruction
+                    // caches).  The gates of a block are formed in the step before its own, those of the
+                    // first one while its products are on their way; a step's loads come first, so that
+                    // the arithmetic of both overlaps their latency.  (z and y take turns in the buffer.)
+                    if (gated && live) {
+                        // (the loads for the next half stay out of the loop: a register of its own for each,
+                        // or the loop would move them, and wait)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) zc[k] = zn[k];
+                        load_z(c * L + 64 * half + 64 + 8 * odd);
+                        next_z();
+                        gates();
+                        __syncwarp();
+                    }
+                    ok = wait_warp(sy, B_Y1, yi++);
+                    if (!ok) break;
+                    tc_fence_after_sync();
 #pragma unroll 1
-                    for (int i = -1; i < 4; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         const int t0 = 64 * half + 16 * i + 8 * odd;
-                        const bool some = i >= 0 && live && t0 < nv;
-                        uint32_t yr[4];
-                        if (i == 0) {
-                            ok = wait_warp(sy, B_Y1, yi++);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                        }
-                        if (some) {
-                            uint32_t xr[4];
+                        if (live && t0 < nv) {
+                            uint32_t xr[4], yr[4];
                             float2 y1[4], y2[4];
+                            if (gated && i < 3) next_z();
                             ldsm4t(x + t0 * 128, xr);
                             const float2 e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
@@ -885,26 +927,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 if (gated) o = fmul2(o, gz[k]);
                                 yr[k] = pack2<BF16>(o.x, o.y);
                             }
-                        }
-                        if (i == 3) {  // the products are read
-                            tc_fence_before_sync();
-                            warp_arrive(sy, B_Y1FREE);
-                            warp_arrive(sy, B_Y2FREE + half);
-                        } else if (gated && live) {
-                            uint32_t zr[4];
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zn[0].x), "r"(zn[0].y),
-                                         "r"(zn[0].z), "r"(zn[0].w)
-                                         : "memory");
+                            if (gated) gates();  // (after the last block: of a z that is not used)
                             __syncwarp();
-                            ldsm4t(io_frag, zr);
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) zn[k] = zn[k + 1];
-                            if (i == 2) load_z(c * L + 64 * half + 64 + 8 * odd);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) gz[k] = silu2(unpack2<BF16>(zr[k]));
-                            __syncwarp();
-                        }
-                        if (some) {
                             stsm4t(io_frag, yr);
                             __syncwarp();
                             uint4 v;
@@ -917,7 +941,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             __syncwarp();  // y is read: the buffer is free
                         }
                     }
-                    if (!ok) break;
+                    tc_fence_before_sync();  // the products are read
+                    warp_arrive(sy, B_Y1FREE);
+                    warp_arrive(sy, B_Y2FREE + half);
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_EMPTY + s);
