@@ -75,7 +75,7 @@ enum {
     B_FIN,
     NBAR
 };
-static_assert(SM_MISC + NBAR * 8 + 16 <= SM_TOTAL, "barrier space");
+static_assert(SM_MISC + NBAR * 8 + 24 <= SM_TOTAL, "barrier space");
 
 __device__ int g_ssm_status;  // bits of kDevErr*
 
@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM_MISC + NBAR * 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
+    float* decay_sum = reinterpret_cast<float*>(sm + SM_MISC + NBAR * 8 + 16);  // (PASS 1) by gate warp
     int* warp_sum = reinterpret_cast<int*>(sm + SM_GATE);  // before the gates are written
     const Sync sy{bar, abort_flag, p.status};
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -441,8 +442,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int i = bc > kStages ? bc - kStages : 0; i < bc; ++i) land(&bar[B_FULL + i % kStages], i / kStages);
             for (int i = xc > kStages ? xc - kStages : 0; i < xc; ++i) land(&bar[B_XFULL + i % kStages], i / kStages);
         }
-    } else if (warp == kMmaWarp) {
-        if (OUT && elect_one()) {
+    } else if (OUT && warp == kMmaWarp) {
+        if (elect_one()) {
             constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
             constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
             constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 64, false, false);
@@ -540,11 +541,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
             finish_mma(&bar[B_FIN]);
         }
-    } else if (warp == kGateWarp) {
+    } else if (warp == kGateWarp || (!OUT && warp == kMmaWarp)) {
         const float A = ssm_rate(__ldg(p.A_log + h)), bias = __ldg(p.dt_bias + h);
         const T* a = static_cast<const T*>(p.a) + un.begin * p.a_stride + h;
+        // PASS 1 has two gate warps, a chunk each in turn
+        constexpr int GATES = OUT ? 1 : 2;
         float seg_sum = 0.f;
-        for (int c = 0; c < nch; ++c) {
+        for (int c = warp != kGateWarp ? 1 : 0; c < nch; c += GATES) {
             const int s = c % kStages;
             float v[4];
 #pragma unroll
@@ -558,7 +561,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool live = c * L + 4 * lane + i < un.len;
-                dt[i] = live ? softplus_call(v[i] + bias) : 0.f;
+                dt[i] = live ? (OUT ? softplus_call(v[i] + bias) : ssm_softplus(v[i] + bias)) : 0.f;
                 g2[i] = fmaxf(A * dt[i] * kLog2e, kMinLog2Decay);
                 sum += g2[i];
                 pre[i] = sum;
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             seg_sum += pre[3];  // lane 31: the chunk's sum
             warp_arrive(sy, B_GATE + s);
         }
-        if (PASS == 1 && lane == 31) p.ws_decay[u * p.n_heads + h] = exp2f(seg_sum);
+        if (PASS == 1 && lane == 31) decay_sum[warp == kGateWarp] = seg_sum;
     } else if (OUT && warp < 4) {
         if constexpr (OUT) {
             // ---- M: lane = token t ----
@@ -953,6 +956,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     tc_fence_before_sync();
     __syncthreads();
     __syncwarp();
+    if (PASS == 1 && tid == 0) p.ws_decay[u * p.n_heads + h] = exp2f(decay_sum[0] + decay_sum[1]);
     if (warp == kMmaWarp) tmem_dealloc(tm, TM_COLS);
 }
 
