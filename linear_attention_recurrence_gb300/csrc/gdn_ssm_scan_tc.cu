@@ -39,9 +39,10 @@ namespace gdn {
 namespace {
 
 constexpr int L = 128;        // tokens per chunk
-constexpr int kThreadsTc = 640;
+constexpr int kThreadsTc = 768;
+constexpr int kOutGroups = 3;  // groups of 4 output warps
 constexpr int kStages = 2;
-constexpr int kCopyWarp = 16, kMmaWarp = 17, kGateWarp = 18, kStateMmaWarp = 19;
+constexpr int kCopyWarp = 20, kMmaWarp = 21, kGateWarp = 22, kStateMmaWarp = 23;
 
 // tensor-memory columns
 constexpr uint32_t TM_H = 0;     // H^T, FP32 [head_dim lanes][state_dim]
@@ -57,9 +58,9 @@ constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: (gamma, dt)[128] at 0, w[128] at
-constexpr uint32_t SM_GATE_STAGE = 2176;                // 256, e^gamma[128] at 384, 2^k of w and 2^j of dt at 512
+constexpr uint32_t SM_GATE_STAGE = 1664;                // 256, 2^k of w and 2^j of dt at 384
 constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
-constexpr uint32_t SM_MISC = SM_IO + 8 * 512;
+constexpr uint32_t SM_MISC = SM_IO + 4 * kOutGroups * 512;
 constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
@@ -72,9 +73,10 @@ enum {
     B_XW = B_Y2FREE + 2,  // [8]
     B_XWFREE = B_XW + 8,
     B_TAIL = B_XWFREE + 8,
-    B_FIN,
+    B_INIT, B_FIN,
     NBAR
 };
+static_assert(kOutGroups >= 3, "the output warps bring the state's rows 32 .. 127");
 static_assert(SM_MISC + NBAR * 8 + 24 <= SM_TOTAL, "barrier space");
 
 __device__ int g_ssm_status;  // bits of kDevErr*
@@ -237,10 +239,11 @@ __device__ __forceinline__ float range_scale(float v) {
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
     if (b >= B_BCFREE && b < B_EMPTY) return out ? 2 : 1;
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 17 : 16;
+    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 9 + 4 * kOutGroups : 16;
     if (b == B_H || b == B_TAIL) return out ? 4 : 16;
+    if (b == B_INIT) return 4 * kOutGroups;
     if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
-    if (b == B_Y1FREE || b == B_Y2FREE || b == B_Y2FREE + 1) return 8;
+    if (b == B_Y1FREE || b == B_Y2FREE || b == B_Y2FREE + 1) return 4 * kOutGroups;
     if (b == B_FIN) return out ? 2 : 1;
     if (b >= B_XW && b < B_XWFREE) return out ? 4 : 16;
     return 1;
@@ -406,6 +409,40 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+
+    // Rows n0 .. + 31 of the state before the segment, columns 32 wq + lane, to tensor memory.
+    auto init_state = [&](int wq, int n0) {
+        const int slot = p.states ? seq_slot(p.q, un.s) : -1, pcol = wq * 32 + lane;
+        const bool from_ws = OUT && un.n_seg > 1;
+        const bool old = !from_ws && un.k == 0 && slot >= 0 && seq_has_state(p.q, un.s);
+        const int64_t unit_floats = static_cast<int64_t>(p.n_heads) * N * P;
+        float* first = p.ws + ((u - un.k) * p.n_heads + h) * N * P + static_cast<int64_t>(n0) * P + pcol;  // segment 0's contribution
+        float* kept = first + (un.n_seg - 1) * unit_floats;  // the state before the sequence, left by PASS 1
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        if (old) {
+            const float* src = p.states + ((static_cast<int64_t>(slot) * p.n_heads + h) * N + n0) * P + pcol;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = src[i * P];
+        } else if (from_ws && un.k == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = kept[i * P];
+        } else if (from_ws) {
+            float keep = 1.f;
+            for (int k = un.k - 1; k >= 0; --k) {
+                const float* src = first + k * unit_floats;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(keep, src[i * P], v[i]);
+                keep *= p.ws_decay[(u - un.k + k) * p.n_heads + h];
+            }
+        }
+        if (PASS == 1 && un.k == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) kept[i * P] = v[i];
+        }
+        tmem_st32(tm + (static_cast<uint32_t>(wq * 32) << 16) + TM_H + n0, v);
+    };
 
     if (warp == kCopyWarp) {
         if (elect_one()) {
@@ -603,15 +640,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     dt[i] *= 1.0f / ds;
                 }
                 if (lane == 0) {
-                    gt[512] = ws;
-                    gt[513] = ds;
+                    gt[384] = ws;
+                    gt[385] = ds;
                 }
             }
             gd[2 * lane] = make_float4(pre[0], dt[0], pre[1], dt[1]);
             gd[2 * lane + 1] = make_float4(pre[2], dt[2], pre[3], dt[3]);
             reinterpret_cast<float4*>(gt + 256)[lane] =
                 make_float4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<float4*>(gt + 384)[lane] = make_float4(ex2(pre[0]), ex2(pre[1]), ex2(pre[2]), ex2(pre[3]));
             seg_sum += pre[3];  // lane 31: the chunk's sum
             warp_arrive(sy, B_GATE + s);
         }
@@ -683,38 +719,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         const int slot = p.states ? seq_slot(p.q, un.s) : -1;
         float* pool = p.states + (static_cast<int64_t>(slot) * p.n_heads + h) * N * P + pcol;
         if (live) {
-            // the state before the segment
-            const bool from_ws = OUT && un.n_seg > 1;
-            const bool old = !from_ws && un.k == 0 && slot >= 0 && seq_has_state(p.q, un.s);
-            const int64_t unit_floats = static_cast<int64_t>(p.n_heads) * N * P;
-            float* first = p.ws + ((u - un.k) * p.n_heads + h) * N * P + pcol;  // segment 0's contribution
-            float* kept = first + (un.n_seg - 1) * unit_floats;  // the state before the sequence, left by PASS 1
 #pragma unroll 1
-            for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                if (old) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = pool[static_cast<int64_t>(n0 + i) * P];
-                } else if (from_ws && un.k == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = kept[static_cast<int64_t>(n0 + i) * P];
-                } else if (from_ws) {
-                    float keep = 1.f;
-                    for (int k = un.k - 1; k >= 0; --k) {
-                        const float* src = first + k * unit_floats;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = fmaf(keep, src[static_cast<int64_t>(n0 + i) * P], v[i]);
-                        keep *= p.ws_decay[(u - un.k + k) * p.n_heads + h];
-                    }
-                }
-                if (PASS == 1 && un.k == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) kept[static_cast<int64_t>(n0 + i) * P] = v[i];
-                }
-                tmem_st32(tm + lanes + TM_H + n0, v);
-            }
+            for (int n0 = 32 * xg; n0 < (OUT ? 32 : N); n0 += 32 * X_GROUPS) init_state(wq, n0);
             tmem_wait_st();
         }
         const uint32_t x_frag = frag_offset(wq * 32, lane), x_frag1 = frag_offset(wq * 32 + 16, lane);
@@ -742,13 +748,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 warp_arrive(sy, B_TAIL);
                 if (!wait_warp(sy, B_TAIL, 0)) break;
             }
-            const float next_scale = BF16 ? 1.f : gt[512];
+            const float next_scale = BF16 ? 1.f : gt[384];
             // the state's decay, and its rounding for the product with C
             auto state_step = [&]() {
+                if (OUT && c == 0 && !wait_warp(sy, B_INIT, 0)) return false;
                 if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) return false;
                 tc_fence_after_sync();
                 if (live) {
-                    const float keep = gt[384 + L - 1] * (scale * (1.0f / next_scale));
+                    const float keep = ex2(gt[2 * (L - 1)]) * (scale * (1.0f / next_scale));
 #pragma unroll 1
                     for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                         float v[32];
@@ -836,10 +843,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
         }
         tc_fence_before_sync();
-    } else if (warp < 16) {
+    } else if (warp < 8 + 4 * kOutGroups) {
         if constexpr (OUT) {
-            // ---- the output: this warp's 32 columns of x, every other block of 8 tokens ----
-            const int wq = warp & 3, odd = (warp - 8) >> 2;
+            // ---- the output: this warp's 32 columns of x, every kOutGroups-th block of 8 tokens ----
+            const int wq = warp & 3, og = (warp - 8) >> 2;
+            // the state's rows from 32 on, beside the state's own warps
+            if (wq * 32 < P && 32 * (og + 1) < N) {
+                init_state(wq, 32 * (og + 1));
+                tmem_wait_st();
+            }
+            tc_fence_before_sync();
+            warp_arrive(sy, B_INIT);
+            constexpr int BLOCKS = (8 + kOutGroups - 1) / kOutGroups;  // of a half chunk, at most
             const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
             const bool live = wq * 32 < P;
             const float D = p.D ? __ldg(p.D + h) : 0.f;
@@ -858,16 +873,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             // z of this warp's 4 blocks of a half chunk, a half ahead of their use (from L2, where the copy
             // warp has them fetched with the chunk's other operands): one batch, because a wait for the
             // oldest of several loads is a wait for all of them
-            uint4 zn[4], zc[4];
+            uint4 zn[BLOCKS], zc[BLOCKS];
             auto load_z = [&](int t) {
                 if (!gated || !live) return;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = t + 16 * i + pt < un.len ? t + 16 * i + pt : un.len - 1;
+                for (int i = 0; i < BLOCKS; ++i) {
+                    const int row = t + 8 * kOutGroups * i + pt < un.len ? t + 8 * kOutGroups * i + pt : un.len - 1;
                     zn[i] = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
                 }
             };
-            load_z(8 * odd);
+            load_z(8 * og);
             uint32_t zr[4] = {};
             float2 gz[4];
             auto next_z = [&]() {  // the next block's z as a fragment
@@ -877,7 +892,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 __syncwarp();
                 ldsm4t(io_frag, zr);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) zc[k] = zc[k + 1];
+                for (int k = 0; k < BLOCKS - 1; ++k) zc[k] = zc[k + 1];
             };
             auto gates = [&]() {
 #pragma unroll
@@ -888,13 +903,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
                 const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X + x_frag;
-                const float* eg = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE) + 384;
+                const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
                 if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_XFULL + s, c / kStages)) break;
                 const int nv = un.len - c * L;
-                const float m_scale = BF16 ? 1.f : eg[513 - 384];
+                const float m_scale = BF16 ? 1.f : gt[385];
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    // Blocks i = 0 .. 3 in a rolled loop (the code of all roles has to fit the instruction
+                    // Blocks i = og, og + kOutGroups, .. in a rolled loop (the code of all roles has to fit the instruction
                     // caches).  The gates of a block are formed in the step before its own, those of the
                     // first one while its products are on their way; a step's loads come first, so that
                     // the arithmetic of both overlaps their latency.  (z and y take turns in the buffer.)
@@ -902,8 +917,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         // (the loads for the next half stay out of the loop: a register of its own for each,
                         // or the loop would move them, and wait)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) zc[k] = zn[k];
-                        load_z(c * L + 64 * half + 64 + 8 * odd);
+                        for (int k = 0; k < BLOCKS; ++k) zc[k] = zn[k];
+                        load_z(c * L + 64 * half + 64 + 8 * og);
                         next_z();
                         gates();
                         __syncwarp();
@@ -912,14 +927,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     if (!ok) break;
                     tc_fence_after_sync();
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const int t0 = 64 * half + 16 * i + 8 * odd;
+                    for (int i = og; i < 8; i += kOutGroups) {
+                        const int t0 = 64 * half + 8 * i;
                         if (live && t0 < nv) {
                             uint32_t xr[4], yr[4];
                             float2 y1[4], y2[4];
-                            if (gated && i < 3) next_z();
+                            if (gated && i + kOutGroups < 8) next_z();
                             ldsm4t(x + t0 * 128, xr);
-                            const float2 e2 = *reinterpret_cast<const float2*>(eg + t0 + 2 * (lane & 3));
+                            const float4 gd = *reinterpret_cast<const float4*>(gt + 2 * t0 + 4 * (lane & 3));  // of 2 tokens
+                            const float2 e2 = make_float2(ex2(gd.x), ex2(gd.z));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
