@@ -289,8 +289,10 @@ int gdn_recurrence_chunked_noalloc(const float* q, const float* k, const float* 
  * may have stride 0; no output may overlap an input or another output, as address
  * ranges.  Elements need their own alignment, states 16 bytes; rows that start on
  * 16-byte boundaries are faster.  Calls keep nothing between them, use no memory of
- * the library's and may run at the same time on different streams (on different
- * slots and workspaces), and may be captured into a graph.
+ * the library's but a status word, and may run at the same time on different streams
+ * (on different slots and workspaces).  They may be captured into a graph, after one
+ * call of the same kind on the device (which has the runtime load its kernels).
+ * gdn_device_status() reports a wait inside a kernel that gave up.
  */
 
 /*
@@ -322,6 +324,17 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
  * up to 256; state_dim: 16, 32, 64 or 128.
  * workspace: gdn_ssm_scan_workspace_bytes() bytes, 16-byte aligned, the call's own
  * until it has finished (NULL where that is 0).
+ *
+ * Two forms.  Token after token, the state in registers: any call; a sequence split
+ * over calls gives the same bits.  Chunks of 128 tokens on the tensor cores: GDN_BF16
+ * and GDN_F16 with head_dim and state_dim 64 or 128, at least 32 tokens per sequence
+ * on average, and x, B, C, z and y in rows of 16-byte pieces on 16-byte boundaries.
+ * There the decayed scores and the state (for its product with C) are rounded once to
+ * `dtype`, while the state itself keeps FP32's precision.  For GDN_F16 this asks that
+ * C . B and the state stay in FP16's range (below 65504; beyond it y is not finite),
+ * and it keeps the state to 2^-24 of a chunk's largest step.  A NaN or infinity in x
+ * reaches, besides its own and later tokens, the outputs of the up to 127 tokens of
+ * the same sequence before it that share its chunk.
  */
 int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const void* B, int64_t b_stride,
                  const void* C, int64_t c_stride, const void* z, int64_t z_stride, const float* A_log,

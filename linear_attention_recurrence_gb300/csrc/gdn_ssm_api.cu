@@ -184,7 +184,8 @@ int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_strid
         return is_aligned(ptr, 16) && stride % 8 == 0 && stride >= width;
     };
     cudaError_t err;
-    if (ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) && tma_rows(x, x_stride, xw) &&
+    if (ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) && (T / 512 + n_seq) * n_heads <= INT32_MAX &&
+        tma_rows(x, x_stride, xw) &&
         tma_rows(B, b_stride, bw) && tma_rows(C, c_stride, bw) &&
         (!z || tma_rows(z, z_stride, xw)) && tma_rows(y, y_stride, xw)) {
         int sms = 0;

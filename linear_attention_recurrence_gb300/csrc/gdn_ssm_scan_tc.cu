@@ -24,9 +24,23 @@
 // behind it (the update's product alone) and its decay; the second starts each segment
 // from the sum of those before it.
 //
-// Warp roles (512 threads): warps 0-3 form M (lane = token); 4-7 the parts of w o x and
-// the state's decay and rounding (lane = column of x); 8-11 the output; 12 issues the
-// copies, 13 the MMAs, 14 forms the gates.  MMA order
+// Warp roles (768 threads): warps 0-3 form M (lane = token); 4-7 the parts of w o x and the
+// state's decay and rounding (lane = column of x); 8-19 the output; 20 issues the copies, 21
+// the MMAs of the output's chain, 23 those of the state's (a tcgen05.mma waits in its thread
+// while the tensor pipe is full, and the two chains wait for different roles), 22 forms the
+// gates.  In the first launch warps 0-15 all form parts and 21 and 22 the gates.  A role's
+// 16 x 16 tiles come and go as fragments (ldmatrix, stmatrix and the 16-lane forms of the
+// tensor-memory accesses), so that x, z and y cross shared and global memory 16 bytes at a
+// time although a lane's row is a column of x.
+//
+// What bounds it: the instructions of the roles around the products, 6500 per scheduler and
+// chunk at about one in two cycles (the tensor pipe is busy a fifth of the time); memory
+// next.  48 heads of 128 x 128, BF16, z: 32768 tokens of one sequence 629 us (the first
+// launch 141 us, 1.6 us a chunk; the second 487 us, 5.7 us a chunk; 1.48 GB: 219 us at the
+// copy rate).  Steps on the way, 32768 tokens: z by 2-byte loads in the output 1052 us;
+// fragments 883; eight output warps and z a half chunk ahead 792; the MMA chains apart and
+// elected issuing lanes 691; code that fits the instruction caches (81 -> 55 KB: rolled
+// loops, waits out of line) 670; x freed apart from B and C 652; twelve output warps 629.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -1028,14 +1042,16 @@ std::atomic<int*> g_status_word[64];  // its address on the devices it was asked
 }  // namespace
 
 // Segments: with H heads, SMs / H segments of all tokens together fill the device; a
-// segment is at least that share of the call's chunks (and an eighth of them, so that a
-// segment sums at most 7 others).
+// segment is at least that share of the call's chunks, an eighth of them (so that a
+// segment sums at most 7 others) and 4 chunks (the first launch then costs more than it
+// saves: about 12 us against 6 us for each chunk that a segment is shorter).
 int64_t ssm_scan_segment(int64_t T, int n_heads, int sm_count) {
     const int64_t chunks = (T + L - 1) / L;
     int64_t parts = sm_count / n_heads;
     if (parts > 8) parts = 8;
     if (parts < 1) parts = 1;
-    return (chunks + parts - 1) / parts * L;
+    const int64_t share = (chunks + parts - 1) / parts;
+    return (share < 4 ? 4 : share) * L;
 }
 
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq) {

@@ -483,7 +483,8 @@ def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seq
     A_log, dt_bias, D (or None): [n_heads] FP32; states:
     [slots][n_heads][state_dim][head_dim] FP32, or None (sequences start from zeros,
     nothing is kept).  Head h reads group h % n_groups.  cu_seqlens, slots, has_state
-    as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.
+    as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.  16-bit prompts run on the
+    tensor cores where their sizes and alignment allow (see gdn.h).
     """
     dt, dev = _activations(x, "x", 3)
     if B.dim() != 3:
