@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "gdn_device.cuh"
 
@@ -45,14 +46,52 @@ __device__ __forceinline__ void load_vec(const T* p, float (&f)[N]) {
 template <class T, int N>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[N]) {
     Vec<T, N> x;
+    if constexpr (N > 1 && sizeof(T) == 2) {  // two roundings per instruction
+        uint32_t* u = reinterpret_cast<uint32_t*>(x.v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x.v[i] = from_f<T>(f[i]);
+        for (int i = 0; i < N; i += 2) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(f[i], f[i + 1]);
+                u[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[i], f[i + 1]);
+                u[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x.v[i] = from_f<T>(f[i]);
+    }
     *reinterpret_cast<Vec<T, N>*>(p) = x;
 }
 
-// silu(z) = z / (1 + e^-z), with the fast exponential and division (relative error a
-// few FP32 ulp; an infinite divisor gives 0).
-__device__ __forceinline__ float ssm_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The hardware's 2^v and 1 / v (relative error below 2^-22 and 2^-23; subnormals are 0).
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
+    return upk(r);
+}
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) and silu(z) = z sigmoid(z) (an infinite divisor
+// gives 0), and silu of two: the same operations, the same bits.
+__device__ __forceinline__ float ssm_sigmoid(float z) { return rcp(1.0f + ex2(__fmul_rn(z, -kLog2e))); }
+__device__ __forceinline__ float ssm_silu(float z) { return z * ssm_sigmoid(z); }
+__device__ __forceinline__ float2 silu2(float2 z) {
+    const float2 m = fmul2(z, make_float2(-kLog2e, -kLog2e));
+    const float2 d = fadd2(make_float2(ex2(m.x), ex2(m.y)), make_float2(1.f, 1.f));
+    return fmul2(z, make_float2(rcp(d.x), rcp(d.y)));
+}
 
 // softplus(v) = log(1 + e^v), accurate for small e^v too (log1p); v itself once e^-v
 // is below half an FP32 ulp of v.
@@ -61,7 +100,6 @@ __device__ __forceinline__ float ssm_softplus(float v) { return v > 20.0f ? v : 
 // -exp(A_log), finite (so that no step, dt = 0, stays no decay).
 __device__ __forceinline__ float ssm_rate(float A_log) { return fmaxf(-expf(A_log), -3.402823466e38f); }
 
-constexpr float kLog2e = 1.4426950408889634f;
 // A token's decay is e^g = 2^(g log2 e).  The exponent is held at -256 or above: such a
 // factor is 0 in FP32 either way, and running sums of the exponents stay finite.
 constexpr float kMinLog2Decay = -256.0f;

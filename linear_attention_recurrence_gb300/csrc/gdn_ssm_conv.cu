@@ -5,8 +5,11 @@
 //
 // Bound by HBM: every row is read once and written once.  A thread holds 4 channels
 // (their taps and bias in registers) and walks a tile of rows with the last K - 1 rows in
-// registers and 8 rows' loads in flight, so a row is fetched once per tile; the K - 1 rows
-// before a tile are fetched again (3 in 16 to 64, from L2).
+// registers and 8 rows' loads in flight, so a row is fetched once per tile.  The 8 rows are
+// formed without a branch between them, in packed FP32 pairs: what a 16-bit row waits for is
+// the latency of its arithmetic (BF16, 16384 x 10240: 172 us with a branch and single
+// operations, 124 us so; 8 channels a thread 134 us, 4 rows in flight with 8 CTAs per SM 125,
+// 16 rows 131).  16384 x 10240 in FP32 takes 205 us (6.5 TB/s), in BF16 124 us (5.4 TB/s).
 //
 // History without a race: the tile that holds a sequence's first row also owns the
 // rows at positions 1 .. K - 2 (a tile boundary that would fall there moves behind
@@ -44,6 +47,38 @@ __device__ __forceinline__ int64_t tile_edge(const SsmSeqs& q, int64_t r, int co
         if (b < r && r < e && r - b < K - 1) r = b + (K - 1) < e ? b + (K - 1) : e;
     }
     return r;
+}
+
+// f = act(bias + the taps over the window and the row cur), and the window one row on.
+// Pairs of channels in packed instructions, which round as single ones do.
+template <int K, int VEC>
+__device__ __forceinline__ void conv_row(const float (&w)[VEC][K], const float (&bias)[VEC], float (&win)[K - 1][VEC],
+                                         const float (&cur)[VEC], int activation, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        float acc = bias[0];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) acc = fmaf(w[0][j], win[j][0], acc);
+        acc = fmaf(w[0][K - 1], cur[0], acc);
+        f[0] = activation ? ssm_silu(acc) : acc;
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 2) {
+            float2 acc = make_float2(bias[v], bias[v + 1]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                acc = ffma2(make_float2(w[v][j], w[v + 1][j]), make_float2(win[j][v], win[j][v + 1]), acc);
+            acc = ffma2(make_float2(w[v][K - 1], w[v + 1][K - 1]), make_float2(cur[v], cur[v + 1]), acc);
+            if (activation) acc = silu2(acc);
+            f[v] = acc.x;
+            f[v + 1] = acc.y;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) win[j][v] = win[j + 1][v];
+        win[K - 2][v] = cur[v];
+    }
 }
 
 template <class T, int K, int VEC>
@@ -128,29 +163,20 @@ __global__ void __launch_bounds__(kThreads, 5) ssm_conv_kernel(const SsmConvPara
         const T* xr = x + r * p.x_stride;
         T* yr = y + r * p.y_stride;
         for (int left = static_cast<int>(stop - r); left > 0; left -= kAhead) {
+            // (rows past the last are formed from it and left out: no branch between the rows)
             Vec<T, VEC> raw[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (u < left) raw[u] = *reinterpret_cast<const Vec<T, VEC>*>(xr);
-                xr += p.x_stride;
+                raw[u] = *reinterpret_cast<const Vec<T, VEC>*>(xr);
+                if (u + 1 < left) xr += p.x_stride;
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (u >= left) break;
-                float f[VEC];
+                float cur[VEC], f[VEC];
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float acc = bias[v];
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) acc = fmaf(w[v][j], win[j][v], acc);
-                    const float cur = to_f<T>(raw[u].v[v]);
-                    acc = fmaf(w[v][K - 1], cur, acc);
-                    f[v] = p.activation ? ssm_silu(acc) : acc;
-#pragma unroll
-                    for (int j = 0; j + 1 < K - 1; ++j) win[j][v] = win[j + 1][v];
-                    win[K - 2][v] = cur;
-                }
-                store_vec<T, VEC>(yr, f);
+                for (int v = 0; v < VEC; ++v) cur[v] = to_f<T>(raw[u].v[v]);
+                conv_row<K, VEC>(w, bias, win, cur, p.activation, f);
+                if (u < left) store_vec<T, VEC>(yr, f);
                 yr += p.y_stride;
             }
         }
@@ -163,10 +189,14 @@ void launch_k(const SsmConvParams& p, const SsmSeqs& q, int sm_count, cudaStream
     constexpr int V = 4;
     const int vec = p.vector ? V : 1;
     const int blocks_y = (p.channels + kThreads * vec - 1) / (kThreads * vec);
-    // A tile re-reads its 3 first rows' predecessors and the taps: 64 rows where that leaves
-    // 8 CTAs per SM, else 32 (4 per SM), else 16.
-    const int64_t rows_y = q.T * blocks_y;
-    const int tile = rows_y >= int64_t{64} * 8 * sm_count ? 64 : rows_y >= int64_t{32} * 4 * sm_count ? 32 : 16;
+    // A tile fetches the K - 1 rows before it again (from L2) and the taps, and its CTA starts
+    // with those waits.  FP32 waits for HBM either way and takes 16 rows: 16384 x 10240 205 us
+    // (32 rows 209, 64 211), 256 rows 13 us (16, 19).  16-bit rows wait for their arithmetic
+    // too and take the largest tile that leaves 4 CTAs per SM: 10240 channels, BF16, tiles of
+    // 16 / 32 / 64 rows: 256 rows 13 / 13 / 18 us, 1024 20 / 18 / 20, 2048 28 / 26 / 25,
+    // 16384 139 / 128 / 124.
+    const int64_t rows_y = q.T * blocks_y, fill = int64_t{4} * sm_count;
+    const int tile = sizeof(T) == 4 || rows_y < 32 * fill ? 16 : rows_y < 64 * fill ? 32 : 64;
     const dim3 grid(static_cast<unsigned>((q.T + tile - 1) / tile), blocks_y);
     if (vec == V)
         ssm_conv_kernel<T, K, V><<<grid, kThreads, 0, s>>>(p, q, tile);

@@ -197,27 +197,6 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                  "r"(x), "r"(y)
                  : "memory");
 }
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float rcp(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)));
-    return upk(r);
-}
-// silu of both: z / (1 + 2^(-z log2 e)); an infinite divisor gives 0
-__device__ __forceinline__ float2 silu2(float2 z) {
-    const float2 m = fmul2(z, make_float2(-kLog2e, -kLog2e));
-    const float2 d = fadd2(make_float2(ex2(m.x), ex2(m.y)), make_float2(1.f, 1.f));
-    return fmul2(z, make_float2(rcp(d.x), rcp(d.y)));
-}
 
 // ---- pairs of the 16-bit types ----
 template <bool BF16>
@@ -1042,16 +1021,21 @@ std::atomic<int*> g_status_word[64];  // its address on the devices it was asked
 }  // namespace
 
 // Segments: with H heads, SMs / H segments of all tokens together fill the device; a
-// segment is at least that share of the call's chunks, an eighth of them (so that a
-// segment sums at most 7 others) and 4 chunks (the first launch then costs more than it
-// saves: about 12 us against 6 us for each chunk that a segment is shorter).
-int64_t ssm_scan_segment(int64_t T, int n_heads, int sm_count) {
-    const int64_t chunks = (T + L - 1) / L;
+// segment is that share of the call's chunks, but at least a 16th of them (a segment sums
+// the contributions of those before it).  One sequence, BF16, 128 x 128, us at segments of
+// the share and at the next ones: 48 heads, 768 tokens (2 chunks) 38 (3 chunks 44, uncut 48),
+// 2048 (6) 68 (3 chunks 80, 8 81, uncut 101); 16 heads, 1024 (1) 32 (2 chunks 37, 4 48,
+// uncut 55); 8 heads, 4096 (2) 44 (4 chunks 54, uncut 181).  Two chunks stay uncut (24
+// against 27).  Several sequences are mostly whole segments, for which the first launch is
+// in vain, so theirs are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of
+// 4 chunks 76, uncut 70; 4 of 128: of 2 chunks 37, uncut 32).
+int64_t ssm_scan_segment(int64_t T, int n_seq, int n_heads, int sm_count) {
+    const int64_t chunks = (T + L - 1) / L, least = n_seq > 1 ? 4 : chunks < 3 ? chunks : 1;
     int64_t parts = sm_count / n_heads;
-    if (parts > 8) parts = 8;
+    if (parts > 16) parts = 16;
     if (parts < 1) parts = 1;
     const int64_t share = (chunks + parts - 1) / parts;
-    return (share < 4 ? 4 : share) * L;
+    return (share < least ? least : share) * L;
 }
 
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq) {
@@ -1060,7 +1044,7 @@ bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_
 }
 
 size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count) {
-    const int64_t seg = ssm_scan_segment(T, n_heads, sm_count);
+    const int64_t seg = ssm_scan_segment(T, n_seq, n_heads, sm_count);
     if (seg >= T) return 0;
     const size_t units = static_cast<size_t>(T / seg) + n_seq;
     return units * n_heads * (static_cast<size_t>(head_dim) * state_dim + 4) * sizeof(float);
@@ -1074,7 +1058,7 @@ cudaError_t launch_ssm_scan_tc(const SsmScanParams& p, void* workspace, int sm_c
         !make_map16(&t.tm_c, bf16, p.C, static_cast<int64_t>(p.n_groups) * p.state_dim, p.T, p.c_stride) ||
         (p.z && !make_map16(&t.tm_z, bf16, p.z, static_cast<int64_t>(p.n_heads) * p.head_dim, p.T, p.z_stride)))
         return cudaErrorInvalidValue;
-    const int64_t seg = ssm_scan_segment(p.T, p.n_heads, sm_count);
+    const int64_t seg = ssm_scan_segment(p.T, p.n_seq, p.n_heads, sm_count);
     const int64_t units = p.T / seg + p.n_seq;
     t.a = p.a; t.z = p.z; t.y = p.y;
     t.a_stride = p.a_stride; t.z_stride = p.z_stride; t.y_stride = p.y_stride;
