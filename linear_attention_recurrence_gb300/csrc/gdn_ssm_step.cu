@@ -9,11 +9,11 @@
 // group's heads in tiles of 32; every CTA convolves the group's B and C channels and its
 // own x channels into shared memory.  The x history belongs to one CTA each; the B and C
 // history is read by all of the cluster, and its first CTA writes it after a cluster
-// barrier behind those reads.  A tile's rows are shared by WPT warps (1 when there are
-// requests enough to fill the device, 4 for few: each warp then loads 32 rows in one
-// round, so a lone request waits for memory once); lanes hold 4 rows x 8 float4 columns
-// per load instruction, and the sums over rows meet in two shuffles (and, with 4 warps,
-// in shared memory in a fixed order).
+// barrier behind those reads.  A tile's rows are shared by WPT warps (4, 2 or 1, see the
+// launch), which load them in rounds of 16 rows; lanes hold 4 rows x 8 float4 columns per
+// load instruction, and the sums over rows meet in two shuffles (and, with more than one
+// warp, in shared memory in a fixed order).  48 heads of 128 x 128: 250 requests in FP32
+// 281 us (5.9 TB/s), 64 in BF16 76 us (5.4 TB/s), one 13 us (the waits of one request's chain).
 #include <cooperative_groups.h>
 
 #include "gdn_ssm.cuh"
@@ -220,13 +220,17 @@ template <class T>
 cudaError_t launch_t(const SsmStepParams& p, int sm_count, cudaStream_t s) {
     const int tiles = p.n_heads / p.n_groups * (p.head_dim / COLS);
     const int64_t all = static_cast<int64_t>(p.batch) * p.n_groups * tiles;
-    // Few tiles: 4 warps to each, 2 tiles to a CTA; else a warp each, 8 to a CTA.  A cluster
-    // has at most 8 CTAs, each taking its share of the group's tiles in turn.
-    if (all <= static_cast<int64_t>(sm_count) * 16) {
-        const int ranks = tiles >= 16 ? 8 : (tiles + 1) / 2;
-        return launch_w<T, 4>(p, ranks, s);
-    }
-    const int ranks = tiles >= 64 ? 8 : (tiles + 7) / 8;
+    // Warps to a tile.  With few tiles a lone request's loads should be in flight at once: 4,
+    // or what 8 CTAs hold of a group in one pass (48 heads of 128 x 128, 12 tiles a group, 1
+    // request: 1 / 2 / 4 warps 17.5 / 14.5 / 13.4 us; 32 tiles 16.5 / 13.4 / 13.4; 64 tiles
+    // 15.5 / 16.6 / 17.6).  With many, as few as occupy a CTA's 8 warps (12 tiles, 64 requests:
+    // 81 / 81 / 91 us; 4 tiles, 256: 64 / 56 / 64; 2 tiles, 256: 36 / 30 / 30).  They meet
+    // between 8 requests of 12 tiles in 16 groups (22 / 20 / 22) and 16 (28 / 32 / 32).
+    const bool few = all <= static_cast<int64_t>(sm_count) * 12;
+    const int wpt = few ? (tiles <= 16 ? 4 : tiles <= 32 ? 2 : 1) : (tiles >= 8 ? 1 : tiles >= 3 ? 2 : 4);
+    const int per_cta = kWarps / wpt, ranks = tiles >= 8 * per_cta ? 8 : (tiles + per_cta - 1) / per_cta;
+    if (wpt == 4) return launch_w<T, 4>(p, ranks, s);
+    if (wpt == 2) return launch_w<T, 2>(p, ranks, s);
     return launch_w<T, 1>(p, ranks, s);
 }
 

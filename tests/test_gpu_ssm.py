@@ -178,6 +178,12 @@ SCAN = [
     ((200,), 2, 1, 256, 64, F16, True, True, 3, False),
     ((640,), 3, 1, 128, 128, BF16, True, True, 0, False),
     ((1500,), 3, 1, 128, 128, F16, False, True, 0, False),
+    # one sequence over segments of one, two and more chunks
+    ((170,), 4, 2, 128, 128, BF16, True, True, 0, False),
+    ((300,), 5, 1, 64, 64, F16, True, True, 0, True),
+    ((1000,), 8, 8, 64, 128, BF16, True, True, 0, False),
+    ((2300,), 2, 1, 128, 64, F16, True, False, 0, False),
+    ((900,), 40, 2, 64, 64, BF16, False, True, 0, True),
 ]
 
 
@@ -291,6 +297,13 @@ STEP = [
     (9, 20, 1, 128, 128, 4, BF16, True, True, True),
     (130, 6, 2, 128, 128, 4, F32, True, False, True),
     (3, 2, 1, 256, 32, 4, F16, True, True, True),
+    # a group of 32 and of 64 tiles; many requests with groups of 1 to 4 tiles
+    (3, 16, 1, 64, 128, 4, BF16, True, True, True),
+    (2, 32, 1, 64, 64, 4, F32, True, True, False),
+    (460, 4, 4, 32, 32, 4, BF16, True, True, True),
+    (250, 8, 8, 64, 64, 2, F16, True, True, True),
+    (110, 18, 6, 32, 128, 4, F32, False, True, True),
+    (130, 16, 8, 64, 16, 3, BF16, True, False, True),
 ]
 
 
