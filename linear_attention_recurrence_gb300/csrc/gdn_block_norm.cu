@@ -7,9 +7,10 @@
 // takes a token at a time and keeps its row in registers in FP32 across the two sums,
 // which meet in a shuffle butterfly and one exchange between warps, in a fixed order.  y
 // is formed from r' before r' is rounded to the stream's type.  Two forms, same bits:
-// one CTA per token reading its row itself (few tokens, or rows off 16-byte boundaries),
-// and CTAs that stay, the weights in registers, while bulk copies bring their next rows
-// into shared memory (many tokens: the two sums of a row leave memory idle otherwise).
+// one CTA per token reading its row itself (short rows, rows off 16-byte boundaries, rows
+// longer than the other form holds), and CTAs that stay, the weights in registers, while
+// bulk copies bring their next rows into shared memory (the two sums of a row leave memory
+// idle otherwise).  8192 x 6144 (BF16, FP32 stream, a gate per token) takes 118 us, 6.0 TB/s.
 #include "gdn_ssm.cuh"
 #include "gdn_ssm.h"
 
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const BlockNormPara
                 load_vec<T, VEC>(gate + c, gt);
                 if (p.gate_sigmoid) {
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) gt[v] = __fdividef(1.0f, 1.0f + __expf(-gt[v]));
+                    for (int v = 0; v < VEC; ++v) gt[v] = ssm_sigmoid(gt[v]);
                 }
             }
 #pragma unroll
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) block_norm_rows_kernel(const B
                     load_vec<T, VEC>(gate + c, gt);
                     if (p.gate_sigmoid) {
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) gt[v] = __fdividef(1.0f, 1.0f + __expf(-gt[v]));
+                        for (int v = 0; v < VEC; ++v) gt[v] = ssm_sigmoid(gt[v]);
                     }
                 }
                 load_vec<R, VEC>(r + c, x[i]);
@@ -220,10 +221,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) block_norm_rows_kernel(const B
     }
 }
 
-// Whether the rows form takes a call: enough tokens for every CTA to see several, rows of
-// whole 16-byte pieces, and at most 3 accesses of 8 elements a thread (the weights stay in
-// registers).  At 8192 x 6144 (BF16, FP32 stream, a gate per token) it takes 118 us against
-// 174 us for one CTA per token; at 512 x 6144 both take the same.
 template <class T, class R, int NV>
 cudaError_t launch_rows(const BlockNormParams& p, int sm_count, cudaStream_t s) {
     const uint32_t bytes = static_cast<uint32_t>(p.dim) * (sizeof(T) * (p.gate && p.gate_stride ? 2 : 1) + sizeof(R));
@@ -256,24 +253,31 @@ void launch_n(const BlockNormParams& p, cudaStream_t s) {
 }
 
 template <class T, class R, int VEC>
-void launch_v(const BlockNormParams& p, cudaStream_t s) {
-    // 4 accesses of a thread at most: 256 threads while they reach, then 1024
-    if (p.dim <= VEC * 256 * 4) launch_n<T, R, VEC, 256>(p, s);
+void launch_v(const BlockNormParams& p, int sm_count, cudaStream_t s) {
+    // 4 accesses of a thread at most: 256 threads while they reach, then 1024; 1024 too where a
+    // lone row would take 256 threads 3 or 4 accesses (8192 elements, BF16, FP32 stream, 256 /
+    // 1024 threads: 1 token 14.5 / 10.4 us, 152 14.5 / 12.5, 304 16.6 / 19.6, 2432 87 / 95;
+    // 4096 elements: 1 token 4.0 / 4.0).
+    if (p.dim <= VEC * 256 * (p.T <= sm_count ? 2 : 4)) launch_n<T, R, VEC, 256>(p, s);
     else launch_n<T, R, VEC, 1024>(p, s);
 }
 
 template <class T, class R>
 cudaError_t launch_r(const BlockNormParams& p, int sm_count, cudaStream_t s) {
     const int nv = (p.dim + 8 * kRowThreads - 1) / (8 * kRowThreads);
-    if (p.rows16 && p.T >= 4 * sm_count && nv <= 3) {
+    // Rows of whole 16-byte pieces, at most 3 accesses of 8 elements a thread (the weights stay
+    // in registers) and 1024 elements.  One CTA per token / this form, us, BF16, FP32 stream
+    // and a gate per token: 512 elements: 1 token 2.3 / 2.7, 8192 32 / 32; 1024: 2.5 / 2.7,
+    // 40 / 34; 2048: 2.8 / 2.8, 58 / 46; 6144: 5.0 / 4.7, 171 / 118.
+    if (p.rows16 && p.dim >= 1024 && nv <= 3) {
         if (nv == 1) return launch_rows<T, R, 1>(p, sm_count, s);
         if (nv == 2) return launch_rows<T, R, 2>(p, sm_count, s);
         return launch_rows<T, R, 3>(p, sm_count, s);
     }
-    if (p.vec >= 8) launch_v<T, R, 8>(p, s);
-    else if (p.vec >= 4) launch_v<T, R, 4>(p, s);
-    else if (p.vec >= 2) launch_v<T, R, 2>(p, s);
-    else launch_v<T, R, 1>(p, s);
+    if (p.vec >= 8) launch_v<T, R, 8>(p, sm_count, s);
+    else if (p.vec >= 4) launch_v<T, R, 4>(p, sm_count, s);
+    else if (p.vec >= 2) launch_v<T, R, 2>(p, sm_count, s);
+    else launch_v<T, R, 1>(p, sm_count, s);
     return cudaGetLastError();
 }
 

@@ -34,6 +34,13 @@ CASES = [
     (2, 16383, BF16, F32, True, "row", True, 0, False),
     (3, 9999, F32, F32, False, "token", True, 0, True),
     (3, 8190, F16, F16, True, "none", False, 0, True),
+    # rows through shared memory: one row, and several in turn of every CTA
+    (1, 1024, F32, F32, True, "token", True, 0, False),
+    (700, 2056, BF16, F32, True, "token", True, 8, True),
+    (950, 1536, F32, F32, True, "row", False, 0, False),
+    (640, 6144, F16, F16, False, "token", True, 0, True),
+    (7, 6136, BF16, BF16, False, "none", False, 0, False),
+    (200, 8192, BF16, F32, True, "token", True, 0, True),
 ]
 
 
