@@ -71,7 +71,7 @@ constexpr uint32_t TM_COLS = 512;
 constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
-constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: (gamma, dt)[128] at 0, w[128] at
+constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: gamma[128] at 0, dt at 128, w at
 constexpr uint32_t SM_GATE_STAGE = 1664;                // 256, 2^k of w and 2^j of dt at 384
 constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
 constexpr uint32_t SM_MISC = SM_IO + 4 * kOutGroups * 512;
@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 pre[i] += up;
             }
             float* gt = reinterpret_cast<float*>(sm + SM_GATE + s * SM_GATE_STAGE);
-            float4* gd = reinterpret_cast<float4*>(gt);
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = dt[i] * ex2(suf[i]);
@@ -637,10 +636,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     gt[385] = ds;
                 }
             }
-            gd[2 * lane] = make_float4(pre[0], dt[0], pre[1], dt[1]);
-            gd[2 * lane + 1] = make_float4(pre[2], dt[2], pre[3], dt[3]);
-            reinterpret_cast<float4*>(gt + 256)[lane] =
-                make_float4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<float4*>(gt)[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+            reinterpret_cast<float4*>(gt + 128)[lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+            reinterpret_cast<float4*>(gt + 256)[lane] = make_float4(w[0], w[1], w[2], w[3]);
             seg_sum += pre[3];  // lane 31: the chunk's sum
             warp_arrive(sy, B_GATE + s);
         }
@@ -662,8 +660,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int c = 0; c < nch; ++c) {
                 const int s = c % kStages;
                 if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
-                const float2* gd = reinterpret_cast<const float2*>(sm + SM_GATE + s * SM_GATE_STAGE);
-                const float gt = gd[t].x;
+                const float* gd = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
+                const float gt = gd[t];
                 bool ok = true;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++gi) {
@@ -678,13 +676,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         float v[16];
                         tmem_ld16(tm + lanes + TM_G + j0, v);
                         const int above = t - 64 * half - j0;  // columns past it are above the diagonal
-                        const float4* e4 = reinterpret_cast<const float4*>(gd + 64 * half + j0);
+                        const float4* g4 = reinterpret_cast<const float4*>(gd + 64 * half + j0);
                         uint32_t o[8];
+                        float4 g, dt;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float4 e = e4[i];
-                            const float2 d = fadd2(make_float2(gt, gt), make_float2(-e.x, -e.z));
-                            float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(e.y, e.w));
+                            if (i % 2 == 0) {
+                                g = g4[i / 2];
+                                dt = g4[32 + i / 2];
+                            }
+                            const float2 d = ffma2(i % 2 ? make_float2(g.z, g.w) : make_float2(g.x, g.y),
+                                                   make_float2(-1.f, -1.f), make_float2(gt, gt));
+                            float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), i % 2 ? make_float2(dt.z, dt.w) : make_float2(dt.x, dt.y));
                             a = fmul2(a, make_float2(v[2 * i], v[2 * i + 1]));
                             // selected, not multiplied: what is above may be anything
                             o[i] = pack2<BF16>(2 * i > above ? 0.f : a.x, 2 * i + 1 > above ? 0.f : a.y);
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) return false;
                 tc_fence_after_sync();
                 if (live) {
-                    const float keep = ex2(gt[2 * (L - 1)]) * (scale * (1.0f / next_scale));
+                    const float keep = ex2(gt[L - 1]) * (scale * (1.0f / next_scale));
 #pragma unroll 1
                     for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                         float v[32];
@@ -761,7 +764,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             tmem_st_u16(tm + lanes + TM_HB + n0 / 2, o);
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= keep;
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 d = fmul2(make_float2(v[i], v[i + 1]), make_float2(keep, keep));
+                            v[i] = d.x;
+                            v[i + 1] = d.y;
+                        }
                         tmem_st32(tm + lanes + TM_H + n0, v);
                     }
                     tmem_wait_st();
@@ -792,7 +799,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             for (int q = 0; q < PARTS; ++q) {
                                 part[g2][q][k] = pack2<BF16>(f.x, f.y);
                                 const float2 back = unpack2<BF16>(part[g2][q][k]);
-                                f = fadd2(f, make_float2(-back.x, -back.y));
+                                f = ffma2(back, make_float2(-1.f, -1.f), f);
                             }
                         }
                     }
@@ -927,8 +934,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             float2 y1[4], y2[4];
                             if (gated && i + kOutGroups < 8) next_z();
                             ldsm4t(x + t0 * 128, xr);
-                            const float4 gd = *reinterpret_cast<const float4*>(gt + 2 * t0 + 4 * (lane & 3));  // of 2 tokens
-                            const float2 e2 = make_float2(ex2(gd.x), ex2(gd.z));
+                            const float2 gd = *reinterpret_cast<const float2*>(gt + t0 + 2 * (lane & 3));
+                            const float2 e2 = make_float2(ex2(gd.x), ex2(gd.y));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
