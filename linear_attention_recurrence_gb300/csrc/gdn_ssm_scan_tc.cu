@@ -62,7 +62,7 @@ constexpr int kCopyWarp = 20, kMmaWarp = 21, kGateWarp = 22, kStateMmaWarp = 23;
 constexpr uint32_t TM_H = 0;     // H^T, FP32 [head_dim lanes][state_dim]
 constexpr uint32_t TM_HB = 128;  // H^T in 16 bits, 2 per column
 constexpr uint32_t TM_G = 192;   // G, 64 columns (tokens i) at a time [128 lanes t]
-constexpr uint32_t TM_Y1 = 256;  // x^T M^T, 64 columns (tokens t) at a time
+constexpr uint32_t TM_Y1 = 256;  // x^T M^T, two buffers of 32 columns (tokens t)
 constexpr uint32_t TM_Y2 = 320;  // H^T C^T, 128 columns
 constexpr uint32_t TM_XW = 448;  // parts of w o x: ring of blocks of 16 tokens, 8 columns a part
 constexpr uint32_t TM_COLS = 512;
@@ -82,8 +82,9 @@ enum {
     B_FULL, B_XFULL = B_FULL + kStages,                       // B and C, and x, of a stage landed
     B_GATE = B_XFULL + kStages,
     B_BCFREE = B_GATE + kStages, B_EMPTY = B_BCFREE + kStages,  // B and C, and x and the gates, are read
-    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S, B_Y1, B_Y1FREE,
-    B_Y2FREE,         // [2], by half
+    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S,
+    B_Y1, B_Y1FREE = B_Y1 + 2,      // [2], by buffer
+    B_Y2FREE = B_Y1FREE + 2,        // [2], by half
     B_XW = B_Y2FREE + 2,  // [8]
     B_XWFREE = B_XW + 8,
     B_TAIL = B_XWFREE + 8,
@@ -236,7 +237,7 @@ __device__ constexpr int arrivals(int b, bool out) {
     if (b == B_H || b == B_TAIL) return out ? 4 : 16;
     if (b == B_INIT) return 4 * kOutGroups;
     if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
-    if (b == B_Y1FREE || b == B_Y2FREE || b == B_Y2FREE + 1) return 4 * kOutGroups;
+    if (b >= B_Y1FREE && b < B_XW) return 4 * kOutGroups;
     if (b == B_FIN) return out ? 2 : 1;
     if (b >= B_XW && b < B_XWFREE) return out ? 4 : 16;
     return 1;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     } else if (OUT && warp == kMmaWarp) {
         if (elect_one()) {
             constexpr uint32_t ID_G = idesc_f16(BF16, 128, 64, false, false);   // C, B: K-major
-            constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 64, true, false);   // x^T: M-major
+            constexpr uint32_t ID_Y1 = idesc_f16(BF16, 128, 32, true, false);   // x^T: M-major
             constexpr uint32_t ID_Y2 = idesc_f16(BF16, 128, 64, false, false);
             const uint32_t sm0 = smem_addr(sm);
             uint32_t gi = 0, yi = 0;
@@ -492,16 +493,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 ++gi;
                 return true;
             };
-            auto issue_y1 = [&](int c, int half) {
-                if (!wait_phase(sy, half ? B_M1 : B_M0, c)) return false;
-                if (yi > 0 && !wait_phase(sy, B_Y1FREE, yi - 1)) return false;
+            auto issue_y1 = [&](int c, int q) {  // tokens t of quarter q, from tokens i up to its end
+                if ((q & 1) == 0 && !wait_phase(sy, q ? B_M1 : B_M0, c)) return false;
+                if (yi > 1 && !wait_phase(sy, B_Y1FREE + (q & 1), (yi >> 1) - 1)) return false;
                 tc_fence_after_sync();
-                const uint32_t x = sm0 + (c % kStages) * SM_STAGE + SM_X, m = sm0 + SM_M;
+                const uint32_t x = sm0 + (c % kStages) * SM_STAGE + SM_X, m = sm0 + SM_M + q * 4096;
 #pragma unroll 1
-                for (int k = 0; k < 4 + 4 * half; ++k)
-                    mma_ss(tm + TM_Y1, desc_mn(x + k * 2048),
-                           desc_k(k < 4 ? m + half * 8192 + k * 32 : m + kBox + (k - 4) * 32), ID_Y1, k > 0);
-                umma_commit(&bar[B_Y1]);
+                for (int k = 0; k < 2 * q + 2; ++k)
+                    mma_ss(tm + TM_Y1 + 32 * (q & 1), desc_mn(x + k * 2048),
+                           desc_k(k < 4 ? m + k * 32 : m + kBox - 8192 + (k - 4) * 32), ID_Y1, k > 0);
+                umma_commit(&bar[B_Y1 + (q & 1)]);
                 ++yi;
                 return true;
             };
@@ -514,9 +515,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     mma_ts(tm + TM_Y2 + 64 * half, tm + TM_HB + 8 * k, desc_k(st + (k >> 2) * kBox + (k & 3) * 32), ID_Y2, k > 0);
                 return true;
             };
-            // Order: H^T C^T, the second half of G, the first half of Y1, H^T C^T, the next chunk's first
-            // half of G, the second half of Y1: what a half of the output needs as soon as the
-            // buffers of the half before are read.  (A loop over the halves: the code of all roles
+            // Order: H^T C^T, the second half of G, two quarters of Y1, H^T C^T, the next chunk's first
+            // half of G, two quarters of Y1: what a quarter of the output needs while the one before
+            // is read.  (A loop over the halves: the code of all roles
             // has to fit the instruction caches.)
             bool ok = wait_phase(sy, B_FULL, 0) && issue_g(0, 0);
 #pragma unroll 1
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     if (half) ok = wait_phase(sy, B_FULL + next % kStages, next / kStages);
                     ok = ok && issue_g(next, half ^ 1);
                 }
-                ok = ok && issue_y1(c, half);
+                ok = ok && issue_y1(c, 2 * half) && issue_y1(c, 2 * half + 1);
                 if (half && ok) {
                     umma_commit(&bar[B_MFREE]);
                     umma_commit(&bar[B_EMPTY + c % kStages]);
@@ -648,14 +649,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             // ---- M: lane = token t ----
             const int t = tid;
             const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-            unsigned char* m0 = sm + SM_M + t * 128;                   // columns 0-63
-            unsigned char* m1 = sm + SM_M + kBox + (t - 64) * 128;     // columns 64-127 (t >= 64)
-            // the blocks of 32 columns above the diagonal blocks stay zero
-            if ((warp & 1) == 0) {
-                unsigned char* m = warp == 0 ? m0 : m1;
-#pragma unroll
-                for (int k = 4; k < 8; ++k) *reinterpret_cast<uint4*>(m + ((k ^ (t & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-            }
+            unsigned char* m0 = sm + SM_M + t * 128;                   // columns 0-63 (no product reads past
+            unsigned char* m1 = sm + SM_M + kBox + (t - 64) * 128;     // the diagonal block), 64-127 (t >= 64)
             uint32_t gi = 0;
             for (int c = 0; c < nch; ++c) {
                 const int s = c % kStages;
@@ -854,7 +849,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
             tc_fence_before_sync();
             warp_arrive(sy, B_INIT);
-            constexpr int BLOCKS = (8 + kOutGroups - 1) / kOutGroups;  // of a half chunk, at most
             const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
             const bool live = wq * 32 < P;
             const float D = p.D ? __ldg(p.D + h) : 0.f;
@@ -870,35 +864,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             const int64_t col = static_cast<int64_t>(h) * P + wq * 32 + 8 * (lane & 3);
             const T* zp = gated ? static_cast<const T*>(p.z) + un.begin * p.z_stride + col : nullptr;
             T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + col;
-            // z of this warp's 4 blocks of a half chunk, a half ahead of their use (from L2, where the copy
-            // warp has them fetched with the chunk's other operands): one batch, because a wait for the
-            // oldest of several loads is a wait for all of them
-            uint4 zn[BLOCKS], zc[BLOCKS];
-            auto load_z = [&](int t) {
+            // This warp's blocks of 8 tokens are og, og + kOutGroups, ..  A block's gates are formed in
+            // the step before its own, and its z is loaded in the one before that (from L2, where
+            // the copy warp has it fetched with the chunk's other operands).
+            uint4 zq = {};
+            auto load_z = [&](int b) {
                 if (!gated || !live) return;
-#pragma unroll
-                for (int i = 0; i < BLOCKS; ++i) {
-                    const int row = t + 8 * kOutGroups * i + pt < un.len ? t + 8 * kOutGroups * i + pt : un.len - 1;
-                    zn[i] = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
-                }
+                const int row = 8 * b + pt < un.len ? 8 * b + pt : un.len - 1;
+                zq = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
             };
-            load_z(8 * og);
             uint32_t zr[4] = {};
             float2 gz[4];
             auto next_z = [&]() {  // the next block's z as a fragment
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zc[0].x), "r"(zc[0].y), "r"(zc[0].z),
-                             "r"(zc[0].w)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(io_piece), "r"(zq.x), "r"(zq.y), "r"(zq.z), "r"(zq.w)
                              : "memory");
                 __syncwarp();
                 ldsm4t(io_frag, zr);
-#pragma unroll
-                for (int k = 0; k < BLOCKS - 1; ++k) zc[k] = zc[k + 1];
             };
             auto gates = [&]() {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) gz[k] = silu2(unpack2<BF16>(zr[k]));
             };
-            uint32_t yi = 0;
+            int b = og;  // the next block
+            if (gated && live) {
+                load_z(b);
+                next_z();
+                load_z(b + kOutGroups);
+                gates();
+                __syncwarp();
+            }
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % kStages;
@@ -908,31 +902,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : gt[385];
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    // Blocks i = og, og + kOutGroups, .. in a rolled loop (the code of all roles has to fit the instruction
-                    // caches).  The gates of a block are formed in the step before its own, those of the
-                    // first one while its products are on their way; a step's loads come first, so that
-                    // the arithmetic of both overlaps their latency.  (z and y take turns in the buffer.)
-                    if (gated && live) {
-                        // (the loads for the next half stay out of the loop: a register of its own for each,
-                        // or the loop would move them, and wait)
-#pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) zc[k] = zn[k];
-                        load_z(c * L + 64 * half + 64 + 8 * og);
-                        next_z();
-                        gates();
-                        __syncwarp();
-                    }
-                    ok = wait_warp(sy, B_Y1, yi++);
+                for (int q = 0; q < 4; ++q) {
+                    ok = wait_warp(sy, B_Y1 + (q & 1), 2 * c + (q >> 1));
                     if (!ok) break;
                     tc_fence_after_sync();
+                    // (a rolled loop: the code of all roles has to fit the instruction caches; a step's
+                    // loads come first, so that its arithmetic overlaps their latency; z and y take
+                    // turns in the buffer)
 #pragma unroll 1
-                    for (int i = og; i < 8; i += kOutGroups) {
-                        const int t0 = 64 * half + 8 * i;
+                    for (; b < 16 * c + 4 * q + 4; b += kOutGroups) {
+                        const int t0 = 8 * b - c * L;
                         if (live && t0 < nv) {
                             uint32_t xr[4], yr[4];
                             float2 y1[4], y2[4];
-                            if (gated && i + kOutGroups < 8) next_z();
+                            if (gated) {
+                                next_z();
+                                load_z(b + 2 * kOutGroups);
+                            }
                             ldsm4t(x + t0 * 128, xr);
                             const float2 gd = *reinterpret_cast<const float2*>(gt + t0 + 2 * (lane & 3));
                             const float2 e2 = make_float2(ex2(gd.x), ex2(gd.y));
@@ -946,7 +932,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 if (gated) o = fmul2(o, gz[k]);
                                 yr[k] = pack2<BF16>(o.x, o.y);
                             }
-                            if (gated) gates();  // (after the last block: of a z that is not used)
+                            if (gated) gates();
                             __syncwarp();
                             stsm4t(io_frag, yr);
                             __syncwarp();
@@ -961,8 +947,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         }
                     }
                     tc_fence_before_sync();  // the products are read
-                    warp_arrive(sy, B_Y1FREE);
-                    warp_arrive(sy, B_Y2FREE + half);
+                    warp_arrive(sy, B_Y1FREE + (q & 1));
+                    if (q & 1) warp_arrive(sy, B_Y2FREE + (q >> 1));
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_EMPTY + s);
