@@ -484,11 +484,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if (gi > 0 && !wait_phase(sy, B_GFREE, gi - 1)) return false;
                 tc_fence_after_sync();
                 const uint32_t st = sm0 + (c % kStages) * SM_STAGE;
+                uint64_t dc = desc_k(st + SM_C), db = desc_k(st + SM_B + half * 8192);
 #pragma unroll 1
-                for (int k = 0; k < N / 16; ++k) {
-                    const uint32_t at = (k >> 2) * kBox + (k & 3) * 32;
-                    mma_ss(tm + TM_G, desc_k(st + SM_C + at), desc_k(st + SM_B + half * 8192 + at), ID_G, k > 0);
-                }
+                for (int k = 0; k < N / 64; ++k, dc += kBox >> 4, db += kBox >> 4)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_ss(tm + TM_G, dc + 2 * j, db + 2 * j, ID_G, j > 0 || k > 0);
                 umma_commit(&bar[B_G]);
                 ++gi;
                 return true;
@@ -497,11 +497,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if ((q & 1) == 0 && !wait_phase(sy, q ? B_M1 : B_M0, c)) return false;
                 if (yi > 1 && !wait_phase(sy, B_Y1FREE + (q & 1), (yi >> 1) - 1)) return false;
                 tc_fence_after_sync();
-                const uint32_t x = sm0 + (c % kStages) * SM_STAGE + SM_X, m = sm0 + SM_M + q * 4096;
+                uint64_t dx = desc_mn(sm0 + (c % kStages) * SM_STAGE + SM_X), dm = desc_k(sm0 + SM_M + q * 4096);
+                const uint32_t d = tm + TM_Y1 + 32 * (q & 1);
 #pragma unroll 1
-                for (int k = 0; k < 2 * q + 2; ++k)
-                    mma_ss(tm + TM_Y1 + 32 * (q & 1), desc_mn(x + k * 2048),
-                           desc_k(k < 4 ? m + k * 32 : m + kBox - 8192 + (k - 4) * 32), ID_Y1, k > 0);
+                for (int k = 0; k <= q; ++k, dx += 256) {  // 32 tokens i; the second 64 in the other part of M
+                    mma_ss(d, dx, dm, ID_Y1, k > 0);
+                    mma_ss(d, dx + 128, dm + 2, ID_Y1, true);
+                    dm += k == 1 ? ((kBox - 8192) >> 4) - 4 : 4;
+                }
                 umma_commit(&bar[B_Y1 + (q & 1)]);
                 ++yi;
                 return true;
@@ -509,10 +512,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             auto issue_y2 = [&](int c, int half) {
                 if (c > 0 && !wait_phase(sy, B_Y2FREE + half, c - 1)) return false;
                 tc_fence_after_sync();
-                const uint32_t st = sm0 + (c % kStages) * SM_STAGE + SM_C + half * 8192;
+                uint64_t dc = desc_k(sm0 + (c % kStages) * SM_STAGE + SM_C + half * 8192);
 #pragma unroll 1
-                for (int k = 0; k < N / 16; ++k)
-                    mma_ts(tm + TM_Y2 + 64 * half, tm + TM_HB + 8 * k, desc_k(st + (k >> 2) * kBox + (k & 3) * 32), ID_Y2, k > 0);
+                for (int k = 0; k < N / 64; ++k, dc += kBox >> 4)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_ts(tm + TM_Y2 + 64 * half, tm + TM_HB + 32 * k + 8 * j, dc + 2 * j, ID_Y2, j > 0 || k > 0);
                 return true;
             };
             // Order: H^T C^T, the second half of G, two quarters of Y1, H^T C^T, the next chunk's first
