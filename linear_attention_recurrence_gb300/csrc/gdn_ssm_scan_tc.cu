@@ -55,7 +55,7 @@ namespace {
 constexpr int L = 128;        // tokens per chunk
 constexpr int kThreadsTc = 768;
 constexpr int kOutGroups = 3;  // groups of 4 output warps
-constexpr int kStages = 2;
+constexpr int kStages = 2, kMaxStages = 3;
 constexpr int kCopyWarp = 20, kMmaWarp = 21, kGateWarp = 22, kStateMmaWarp = 23;
 
 // tensor-memory columns
@@ -79,10 +79,10 @@ constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
 enum {
-    B_FULL, B_XFULL = B_FULL + kStages,                       // B and C, and x, of a stage landed
-    B_GATE = B_XFULL + kStages,
-    B_BCFREE = B_GATE + kStages, B_EMPTY = B_BCFREE + kStages,  // B and C, and x and the gates, are read
-    B_G = B_EMPTY + kStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S,
+    B_FULL, B_XFULL = B_FULL + kMaxStages,                       // B and C, and x, of a stage landed
+    B_GATE = B_XFULL + kMaxStages,
+    B_BCFREE = B_GATE + kMaxStages, B_EMPTY = B_BCFREE + kMaxStages,  // B and C, and x and the gates, are read
+    B_G = B_EMPTY + kMaxStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S,
     B_Y1, B_Y1FREE = B_Y1 + 2,      // [2], by buffer
     B_Y2FREE = B_Y1FREE + 2,        // [2], by half
     B_XW = B_Y2FREE + 2,  // [8]
@@ -233,7 +233,7 @@ __device__ __forceinline__ float range_scale(float v) {
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
     if (b >= B_BCFREE && b < B_EMPTY) return out ? 2 : 1;
-    if (b >= B_EMPTY && b < B_EMPTY + kStages) return out ? 9 + 4 * kOutGroups : 16;
+    if (b >= B_EMPTY && b < B_EMPTY + kMaxStages) return out ? 9 + 4 * kOutGroups : 16;
     if (b == B_H || b == B_TAIL) return out ? 4 : 16;
     if (b == B_INIT) return 4 * kOutGroups;
     if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
@@ -369,18 +369,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
     constexpr int PARTS = BF16 ? 3 : 2;
     constexpr bool OUT = PASS == 0;
-    // PASS 1 has tensor memory for 8 blocks' parts, and all 16 working warps to form them
-    constexpr int SLOTS = OUT ? 64 / (8 * PARTS) : 8;
+    // PASS 1 goes through a segment from its last chunk, w with the decay to the segment's end: the
+    // sum needs no decay between chunks (for FP16 a change of its power of two).
+    constexpr bool kStepped = OUT || !BF16;
+    // PASS 1 has tensor memory for two chunks' parts, and 16 warps to form them
+    constexpr int SLOTS = OUT ? 64 / (8 * PARTS) : 16;
     constexpr uint32_t TM_PARTS = OUT ? TM_XW : TM_HB;
     constexpr int X_FIRST = OUT ? 1 : 0, X_GROUPS = OUT ? 1 : 4;
     constexpr int GROUP = OUT ? 1 : 4;  // blocks whose parts share a barrier
     constexpr int NB = N / 64, PB = P / 64;
+    // the stages: PASS 1 has no C, and room for three (its gates lie where M is else)
+    constexpr int STAGES = OUT ? kStages : 3;
+    constexpr uint32_t STAGE_BYTES = OUT ? SM_STAGE : 4 * kBox, B_AT = OUT ? SM_B : 0, X_AT = OUT ? SM_X : 2 * kBox;
+    constexpr uint32_t GATE_AT = OUT ? SM_GATE : SM_M;
+    static_assert(STAGES <= kMaxStages && 3 * 4 * kBox <= SM_M, "stages");
     unsigned char* sm = aligned_dynamic_smem<unsigned char, 1024>();
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM_MISC + NBAR * 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
-    float* decay_sum = reinterpret_cast<float*>(sm + SM_MISC + NBAR * 8 + 16);  // (PASS 1) by gate warp
-    int* warp_sum = reinterpret_cast<int*>(sm + SM_GATE);  // before the gates are written
+    int* warp_sum = reinterpret_cast<int*>(sm + GATE_AT);  // before the gates are written
     const Sync sy{bar, abort_flag, p.status};
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -433,9 +440,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         }
         if (PASS == 1 && un.k == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) kept[i * P] = v[i];
+            for (int i = 0; i < 32; ++i) {
+                kept[i * P] = v[i];
+                v[i] = 0.f;
+            }
         }
-        tmem_st32(tm + (static_cast<uint32_t>(wq * 32) << 16) + TM_H + n0, v);
+        if (kStepped) tmem_st32(tm + (static_cast<uint32_t>(wq * 32) << 16) + TM_H + n0, v);  // (else the first MMA sets it)
     };
 
     if (warp == kCopyWarp) {
@@ -451,27 +461,33 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             const int row0 = static_cast<int>(un.begin);
             int bc = 0, xc = 0;
             for (int c = 0; c < nch; ++c) {
-                const int s = c % kStages, row = row0 + c * L;
-                unsigned char* st = sm + s * SM_STAGE;
-                if (c + kStages < nch) {
-                    rows(&p.tm_b, g * N, NB, row + kStages * L, nullptr, 0);
-                    if (OUT) rows(&p.tm_c, g * N, NB, row + kStages * L, nullptr, 0);
-                    rows(&p.tm_x, h * P, PB, row + kStages * L, nullptr, 0);
+                const int s = c % STAGES, row = row0 + (OUT ? c : nch - 1 - c) * L, ahead = OUT ? row + STAGES * L : row - STAGES * L;
+                unsigned char* st = sm + s * STAGE_BYTES;
+                if (c + STAGES < nch) {
+                    rows(&p.tm_b, g * N, NB, ahead, nullptr, 0);
+                    if (OUT) rows(&p.tm_c, g * N, NB, ahead, nullptr, 0);
+                    rows(&p.tm_x, h * P, PB, ahead, nullptr, 0);
                 }
                 if (OUT && p.z) rows(&p.tm_z, h * P, PB, row, nullptr, 0);
-                if (c >= kStages && !wait_phase(sy, B_BCFREE + s, c / kStages - 1)) break;
-                mbar_arrive_expect_tx(&bar[B_FULL + s], (OUT ? 2 : 1) * NB * kBox);
-                rows(&p.tm_b, g * N, NB, row, st + SM_B, B_FULL + s);
-                if (OUT) rows(&p.tm_c, g * N, NB, row, st + SM_C, B_FULL + s);
-                ++bc;
-                if (c >= kStages && !wait_phase(sy, B_EMPTY + s, c / kStages - 1)) break;
+                auto bc_rows = [&]() {
+                    if (c >= STAGES && !wait_phase(sy, B_BCFREE + s, c / STAGES - 1)) return false;
+                    mbar_arrive_expect_tx(&bar[B_FULL + s], (OUT ? 2 : 1) * NB * kBox);
+                    rows(&p.tm_b, g * N, NB, row, st + B_AT, B_FULL + s);
+                    if (OUT) rows(&p.tm_c, g * N, NB, row, st + SM_C, B_FULL + s);
+                    ++bc;
+                    return true;
+                };
+                // (in the order in which they are freed)
+                if (OUT && !bc_rows()) break;
+                if (c >= STAGES && !wait_phase(sy, B_EMPTY + s, c / STAGES - 1)) break;
                 mbar_arrive_expect_tx(&bar[B_XFULL + s], PB * kBox);
-                rows(&p.tm_x, h * P, PB, row, st + SM_X, B_XFULL + s);
+                rows(&p.tm_x, h * P, PB, row, st + X_AT, B_XFULL + s);
                 ++xc;
+                if (!OUT && !bc_rows()) break;
             }
             // the copies in flight land before the CTA ends, also after a wait that gave up
-            for (int i = bc > kStages ? bc - kStages : 0; i < bc; ++i) land(&bar[B_FULL + i % kStages], i / kStages);
-            for (int i = xc > kStages ? xc - kStages : 0; i < xc; ++i) land(&bar[B_XFULL + i % kStages], i / kStages);
+            for (int i = bc > STAGES ? bc - STAGES : 0; i < bc; ++i) land(&bar[B_FULL + i % STAGES], i / STAGES);
+            for (int i = xc > STAGES ? xc - STAGES : 0; i < xc; ++i) land(&bar[B_XFULL + i % STAGES], i / STAGES);
         }
     } else if (OUT && warp == kMmaWarp) {
         if (elect_one()) {
@@ -483,8 +499,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             auto issue_g = [&](int c, int half) {  // G's columns of tokens 64 half .. +63
                 if (gi > 0 && !wait_phase(sy, B_GFREE, gi - 1)) return false;
                 tc_fence_after_sync();
-                const uint32_t st = sm0 + (c % kStages) * SM_STAGE;
-                uint64_t dc = desc_k(st + SM_C), db = desc_k(st + SM_B + half * 8192);
+                const uint32_t st = sm0 + (c % STAGES) * STAGE_BYTES;
+                uint64_t dc = desc_k(st + SM_C), db = desc_k(st + B_AT + half * 8192);
 #pragma unroll 1
                 for (int k = 0; k < N / 64; ++k, dc += kBox >> 4, db += kBox >> 4)
 #pragma unroll
@@ -497,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if ((q & 1) == 0 && !wait_phase(sy, q ? B_M1 : B_M0, c)) return false;
                 if (yi > 1 && !wait_phase(sy, B_Y1FREE + (q & 1), (yi >> 1) - 1)) return false;
                 tc_fence_after_sync();
-                uint64_t dx = desc_mn(sm0 + (c % kStages) * SM_STAGE + SM_X), dm = desc_k(sm0 + SM_M + q * 4096);
+                uint64_t dx = desc_mn(sm0 + (c % STAGES) * STAGE_BYTES + X_AT), dm = desc_k(sm0 + SM_M + q * 4096);
                 const uint32_t d = tm + TM_Y1 + 32 * (q & 1);
 #pragma unroll 1
                 for (int k = 0; k <= q; ++k, dx += 256) {  // 32 tokens i; the second 64 in the other part of M
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             auto issue_y2 = [&](int c, int half) {
                 if (c > 0 && !wait_phase(sy, B_Y2FREE + half, c - 1)) return false;
                 tc_fence_after_sync();
-                uint64_t dc = desc_k(sm0 + (c % kStages) * SM_STAGE + SM_C + half * 8192);
+                uint64_t dc = desc_k(sm0 + (c % STAGES) * STAGE_BYTES + SM_C + half * 8192);
 #pragma unroll 1
                 for (int k = 0; k < N / 64; ++k, dc += kBox >> 4)
 #pragma unroll
@@ -529,21 +545,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int n = 0; ok && n < 2 * nch; ++n) {
                 const int c = n >> 1, half = n & 1, next = c + half;
                 // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
-                if (half == 0) ok = wait_phase(sy, B_XFULL + c % kStages, c / kStages) && wait_phase(sy, B_H, c);
+                if (half == 0) ok = wait_phase(sy, B_XFULL + c % STAGES, c / STAGES) && wait_phase(sy, B_H, c);
                 ok = ok && issue_y2(c, half);
                 if (!ok) break;
                 if (half) {
                     umma_commit(&bar[B_HBFREE]);
-                    umma_commit(&bar[B_BCFREE + c % kStages]);
+                    umma_commit(&bar[B_BCFREE + c % STAGES]);
                 }
                 if (next < nch) {
-                    if (half) ok = wait_phase(sy, B_FULL + next % kStages, next / kStages);
+                    if (half) ok = wait_phase(sy, B_FULL + next % STAGES, next / STAGES);
                     ok = ok && issue_g(next, half ^ 1);
                 }
                 ok = ok && issue_y1(c, 2 * half) && issue_y1(c, 2 * half + 1);
                 if (half && ok) {
                     umma_commit(&bar[B_MFREE]);
-                    umma_commit(&bar[B_EMPTY + c % kStages]);
+                    umma_commit(&bar[B_EMPTY + c % STAGES]);
                 }
             }
             finish_mma(&bar[B_FIN]);
@@ -554,8 +570,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             const uint32_t sm0 = smem_addr(sm);
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
-                const int s = c % kStages;
-                if (!wait_phase(sy, B_FULL + s, c / kStages) || !wait_phase(sy, B_H, c)) break;
+                const int s = c % STAGES;
+                if (!wait_phase(sy, B_FULL + s, c / STAGES) || (kStepped && !wait_phase(sy, B_H, c))) break;
 #pragma unroll 1
                 for (int j = 0; j < L / 16; j += GROUP) {  // GROUP blocks to a barrier
                     const uint32_t group = (c * (L / 16) + j) / GROUP, slot = group % (SLOTS / GROUP);
@@ -564,15 +580,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int i = 0; i < GROUP; ++i) {
-                        const uint64_t b = desc_mn(sm0 + s * SM_STAGE + SM_B + (j + i) * 2048);
+                        const uint64_t b = desc_mn(sm0 + s * STAGE_BYTES + B_AT + (j + i) * 2048);
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q)
-                            mma_ts(tm + TM_H, tm + TM_PARTS + ((slot * GROUP + i) * PARTS + q) * 8, b, ID_S, true);
+                            mma_ts(tm + TM_H, tm + TM_PARTS + ((slot * GROUP + i) * PARTS + q) * 8, b, ID_S,
+                                   kStepped || group > 0 || i > 0 || q > 0);
                     }
                     umma_commit(&bar[B_XWFREE + slot]);
                 }
                 if (!ok) break;
-                umma_commit(&bar[B_S]);
+                if (kStepped || c == nch - 1) umma_commit(&bar[B_S]);
                 umma_commit(&bar[B_BCFREE + s]);
             }
             finish_mma(&bar[B_FIN]);
@@ -580,23 +597,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     } else if (warp == kGateWarp || (!OUT && warp == kMmaWarp)) {
         const float A = ssm_rate(__ldg(p.A_log + h)), bias = __ldg(p.dt_bias + h);
         const T* a = static_cast<const T*>(p.a) + un.begin * p.a_stride + h;
-        // PASS 1 has two gate warps, a chunk each in turn
+        // PASS 1 has two gate warps, a chunk each in turn; they hand on the sum of the decays behind
         constexpr int GATES = OUT ? 1 : 2;
-        float seg_sum = 0.f;
         for (int c = warp != kGateWarp ? 1 : 0; c < nch; c += GATES) {
-            const int s = c % kStages;
+            const int s = c % STAGES, chunk = OUT ? c : nch - 1 - c;
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = c * L + 4 * lane + i;
+                const int t = chunk * L + 4 * lane + i;
                 v[i] = t < un.len ? to_f<T>(a[t * p.a_stride]) : 0.f;
             }
-            if (c >= kStages && !wait_warp(sy, B_EMPTY + s, c / kStages - 1)) break;
+            if (c >= STAGES && !wait_warp(sy, B_EMPTY + s, c / STAGES - 1)) break;
             float dt[4], g2[4], pre[4], suf[4];
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool live = c * L + 4 * lane + i < un.len;
+                const bool live = chunk * L + 4 * lane + i < un.len;
                 dt[i] = live ? (OUT ? softplus_call(v[i] + bias) : ssm_softplus(v[i] + bias)) : 0.f;
                 g2[i] = fmaxf(A * dt[i] * kLog2e, kMinLog2Decay);
                 sum += g2[i];
@@ -613,14 +629,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             down = __shfl_down_sync(0xffffffffu, down, 1);
             if (lane == 0) up = 0.f;
             if (lane == 31) down = 0.f;
-            float after = down;
+            float behind = 0.f;  // (PASS 1) the sum over the segment's chunks behind this one
+            if (!OUT && c > 0) {
+                if (!wait_warp(sy, B_GATE + (c - 1) % STAGES, (c - 1) / STAGES)) break;
+                behind = reinterpret_cast<const float*>(sm + GATE_AT + (c - 1) % STAGES * SM_GATE_STAGE)[386];
+            }
+            float after = down + behind;
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
                 suf[i] = after;
                 after += g2[i];
                 pre[i] += up;
             }
-            float* gt = reinterpret_cast<float*>(sm + SM_GATE + s * SM_GATE_STAGE);
+            float* gt = reinterpret_cast<float*>(sm + GATE_AT + s * SM_GATE_STAGE);
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = dt[i] * ex2(suf[i]);
@@ -642,13 +663,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     gt[385] = ds;
                 }
             }
-            reinterpret_cast<float4*>(gt)[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
-            reinterpret_cast<float4*>(gt + 128)[lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+            if constexpr (OUT) {
+                reinterpret_cast<float4*>(gt)[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                reinterpret_cast<float4*>(gt + 128)[lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+            } else if (lane == 0) {
+                gt[386] = after;  // with this chunk's
+            }
             reinterpret_cast<float4*>(gt + 256)[lane] = make_float4(w[0], w[1], w[2], w[3]);
-            seg_sum += pre[3];  // lane 31: the chunk's sum
             warp_arrive(sy, B_GATE + s);
         }
-        if (PASS == 1 && lane == 31) decay_sum[warp == kGateWarp] = seg_sum;
     } else if (OUT && warp < 4) {
         if constexpr (OUT) {
             // ---- M: lane = token t ----
@@ -658,9 +681,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             unsigned char* m1 = sm + SM_M + kBox + (t - 64) * 128;     // the diagonal block), 64-127 (t >= 64)
             uint32_t gi = 0;
             for (int c = 0; c < nch; ++c) {
-                const int s = c % kStages;
-                if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
-                const float* gd = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
+                const int s = c % STAGES;
+                if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
+                const float* gd = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
                 const float gt = gd[t];
                 bool ok = true;
 #pragma unroll 1
@@ -723,22 +746,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         bool ok = true;
         float scale = 1.f;  // tensor memory holds H / scale
         for (int c = 0; ok && c < nch; ++c) {
-            const int s = c % kStages;
-            unsigned char* st = sm + s * SM_STAGE;
-            const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
-            if (!wait_warp(sy, B_GATE + s, c / kStages)) break;
-            if (!wait_warp(sy, B_XFULL + s, c / kStages)) break;
-            const int nv = un.len - c * L;
+            const int s = c % STAGES;
+            unsigned char* st = sm + s * STAGE_BYTES;
+            const float* gt = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
+            if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
+            if (!wait_warp(sy, B_XFULL + s, c / STAGES)) break;
+            const int nv = un.len - (OUT ? c : nch - 1 - c) * L;
             if (nv < L) {
-                if (!wait_warp(sy, B_FULL + s, c / kStages)) break;
+                if (!wait_warp(sy, B_FULL + s, c / STAGES)) break;
                 // rows behind the segment's end (another sequence's, which may hold anything) become
                 // zeros in x and B, the operands whose rows are summed over
                 for (int i = tid - 128 * X_FIRST; i < (L - nv) * 8; i += 128 * X_GROUPS) {
                     const uint32_t off = (nv + i / 8) * 128 + (i % 8) * 16;
 #pragma unroll
-                    for (int k = 0; k < PB; ++k) *reinterpret_cast<uint4*>(st + SM_X + k * kBox + off) = make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < PB; ++k) *reinterpret_cast<uint4*>(st + X_AT + k * kBox + off) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) *reinterpret_cast<uint4*>(st + SM_B + k * kBox + off) = make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < NB; ++k) *reinterpret_cast<uint4*>(st + B_AT + k * kBox + off) = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
                 warp_arrive(sy, B_TAIL);
@@ -751,7 +774,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) return false;
                 tc_fence_after_sync();
                 if (live) {
-                    const float keep = ex2(gt[L - 1]) * (scale * (1.0f / next_scale));
+                    const float keep = (OUT ? ex2(gt[L - 1]) : 1.f) * (scale * (1.0f / next_scale));
 #pragma unroll 1
                     for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                         float v[32];
@@ -785,7 +808,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 // the parts are formed before the wait for their slot
                 uint32_t part[2][PARTS][4];
                 if (live) {
-                    const uint32_t x = smem_addr(st) + SM_X + j * 2048;
+                    const uint32_t x = smem_addr(st) + X_AT + j * 2048;
                     const float2 w0 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 2 * (lane & 3));
                     const float2 w1 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 8 + 2 * (lane & 3));
 #pragma unroll
@@ -804,8 +827,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         }
                     }
                 }
-                const uint32_t qi = c * (L / 16) + j, xs = qi % SLOTS, xb = xs / GROUP;
-                if (qi >= SLOTS && !wait_warp(sy, B_XWFREE + xb, qi / SLOTS - 1)) {
+                const uint32_t blk = c * (L / 16) + j, xs = blk % SLOTS, xb = xs / GROUP;
+                if (blk >= SLOTS && !wait_warp(sy, B_XWFREE + xb, blk / SLOTS - 1)) {
                     ok = false;
                     break;
                 }
@@ -821,7 +844,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 tc_fence_before_sync();
                 warp_arrive(sy, B_XW + xb);
             }
-            if (!ok || (!OUT && !state_step())) {
+            if (!ok || (!OUT && kStepped && !state_step())) {
                 ok = false;
                 break;
             }
@@ -829,16 +852,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         }
         // the state behind the segment
         const bool keep_it = PASS == 1 || (slot >= 0 && un.k == un.n_seg - 1);
-        if (ok && keep_it && wait_warp(sy, B_S, nch - 1)) {
+        if (ok && keep_it && wait_warp(sy, B_S, kStepped ? nch - 1 : 0)) {
             tc_fence_after_sync();
             float* dst = PASS == 1 ? p.ws + (u * p.n_heads + h) * N * P + pcol : pool;
+            // (PASS 1) a first segment's includes the state before it, with the segment's decay
+            const float* before = PASS == 1 && un.k == 0 ? dst + (un.n_seg - 1) * static_cast<int64_t>(p.n_heads) * N * P : nullptr;
+            const float decay = PASS == 1 ? exp2f(reinterpret_cast<const float*>(sm + GATE_AT + (nch - 1) % STAGES * SM_GATE_STAGE)[386]) : 0.f;
+            if (PASS == 1 && tid == 0) p.ws_decay[u * p.n_heads + h] = decay;
             if (live) {
 #pragma unroll 1
                 for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                     float v[32];
                     tmem_ld32(tm + lanes + TM_H + n0, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(n0 + i) * P] = v[i] * scale;
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] *= scale;
+                        if (before) v[i] = fmaf(decay, before[static_cast<int64_t>(n0 + i) * P], v[i]);
+                        dst[static_cast<int64_t>(n0 + i) * P] = v[i];
+                    }
                 }
             }
         }
@@ -900,10 +931,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             }
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
-                const int s = c % kStages;
-                const uint32_t x = smem_addr(sm) + s * SM_STAGE + SM_X + x_frag;
-                const float* gt = reinterpret_cast<const float*>(sm + SM_GATE + s * SM_GATE_STAGE);
-                if (!wait_warp(sy, B_GATE + s, c / kStages) || !wait_warp(sy, B_XFULL + s, c / kStages)) break;
+                const int s = c % STAGES;
+                const uint32_t x = smem_addr(sm) + s * STAGE_BYTES + X_AT + x_frag;
+                const float* gt = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
+                if (!wait_warp(sy, B_GATE + s, c / STAGES) || !wait_warp(sy, B_XFULL + s, c / STAGES)) break;
                 const int nv = un.len - c * L;
                 const float m_scale = BF16 ? 1.f : gt[385];
 #pragma unroll 1
@@ -963,7 +994,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     tc_fence_before_sync();
     __syncthreads();
     __syncwarp();
-    if (PASS == 1 && tid == 0) p.ws_decay[u * p.n_heads + h] = exp2f(decay_sum[0] + decay_sum[1]);
     if (warp == kMmaWarp) tmem_dealloc(tm, TM_COLS);
 }
 
