@@ -898,16 +898,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             const int pt = lane >> 2;
             const uint32_t io_piece = io + piece(pt, lane & 3), io_frag = io + piece(r8, lane >> 3);
             const int64_t col = static_cast<int64_t>(h) * P + wq * 32 + 8 * (lane & 3);
-            const T* zp = gated ? static_cast<const T*>(p.z) + un.begin * p.z_stride + col : nullptr;
-            T* yp = static_cast<T*>(p.y) + un.begin * p.y_stride + col;
+            const T* zp = gated ? static_cast<const T*>(p.z) + (un.begin + 8 * og + pt) * p.z_stride + col : nullptr;
+            T* yp = static_cast<T*>(p.y) + (un.begin + 8 * og + pt) * p.y_stride + col;
+            const int64_t z_step = 8 * kOutGroups * p.z_stride, y_step = 8 * kOutGroups * p.y_stride;
+            int z_left = un.len - 8 * og - pt;  // rows from the next load's on
             // This warp's blocks of 8 tokens are og, og + kOutGroups, ..  A block's gates are formed in
             // the step before its own, and its z is loaded in the one before that (from L2, where
             // the copy warp has it fetched with the chunk's other operands).
             uint4 zq = {};
-            auto load_z = [&](int b) {
-                if (!gated || !live) return;
-                const int row = 8 * b + pt < un.len ? 8 * b + pt : un.len - 1;
-                zq = __ldcs(reinterpret_cast<const uint4*>(zp + static_cast<int64_t>(row) * p.z_stride));
+            auto load_z = [&]() {
+                if (z_left > 0) zq = __ldcs(reinterpret_cast<const uint4*>(zp));
+                z_left -= 8 * kOutGroups;
+                zp += z_step;
             };
             uint32_t zr[4] = {};
             float2 gz[4];
@@ -923,9 +925,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             };
             int b = og;  // the next block
             if (gated && live) {
-                load_z(b);
+                load_z();
                 next_z();
-                load_z(b + kOutGroups);
+                load_z();
                 gates();
                 __syncwarp();
             }
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             float2 y1[4], y2[4];
                             if (gated) {
                                 next_z();
-                                load_z(b + 2 * kOutGroups);
+                                load_z();
                             }
                             ldsm4t(x + t0 * 128, xr);
                             const float2 gd = *reinterpret_cast<const float2*>(gt + t0 + 2 * (lane & 3));
@@ -977,8 +979,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                          : "r"(io_piece)
                                          : "memory");
-                            const int t = t0 + pt;
-                            if (t < nv) __stcs(reinterpret_cast<uint4*>(yp + static_cast<int64_t>(c * L + t) * p.y_stride), v);
+                            if (t0 + pt < nv) __stcs(reinterpret_cast<uint4*>(yp), v);
+                            yp += y_step;
                             __syncwarp();  // y is read: the buffer is free
                         }
                     }
