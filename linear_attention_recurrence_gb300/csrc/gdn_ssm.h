@@ -51,8 +51,8 @@ cudaError_t launch_ssm_scan_tokens(const SsmScanParams& p, cudaStream_t s);
 // Chunks of 128 tokens on the tensor cores (gdn_ssm_scan_tc.cu): 16-bit types, head_dim
 // and state_dim 64 or 128, rows of x, B and C on 16-byte boundaries.
 // Tokens per sequence from which it is taken: 48 heads of 128 x 128, BF16, tensor / token
-// form, us: 1 sequence of 16 tokens 15 / 10, 32 15 / 15, 64 16 / 21, 128 17 / 33; 4 of 32
-// 26 / 28; 32 of 16 140 / 103, of 32 142 / 165, of 128 162 / 562.
+// form, us: 1 sequence of 16 tokens 14 / 11, 32 15 / 14, 64 15 / 21, 128 15 / 34; 4 of 32
+// 24 / 28; 32 of 16 116 / 101, of 32 138 / 162, of 128 152 / 549.
 constexpr int kSsmTcMinTokens = 32;
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq);
 size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count);

@@ -22,7 +22,8 @@
 // Where sequences x heads do not fill the device, sequences are cut into segments: a
 // first launch forms, for every segment but the last, its own contribution to the state
 // behind it (the update's product alone) and its decay; the second starts each segment
-// from the sum of those before it.
+// from the sum of those before it.  The first walks a segment from its last chunk, with w
+// down to the segment's end, so that its sum is never decayed.
 //
 // Warp roles (768 threads): warps 0-3 form M (lane = token); 4-7 the parts of w o x and the
 // state's decay and rounding (lane = column of x); 8-19 the output; 20 issues the copies, 21
@@ -33,14 +34,17 @@
 // tensor-memory accesses), so that x, z and y cross shared and global memory 16 bytes at a
 // time although a lane's row is a column of x.
 //
-// What bounds it: the instructions of the roles around the products, 6500 per scheduler and
-// chunk at about one in two cycles (the tensor pipe is busy a fifth of the time); memory
-// next.  48 heads of 128 x 128, BF16, z: 32768 tokens of one sequence 629 us (the first
-// launch 141 us, 1.6 us a chunk; the second 487 us, 5.7 us a chunk; 1.48 GB: 219 us at the
-// copy rate).  Steps on the way, 32768 tokens: z by 2-byte loads in the output 1052 us;
-// fragments 883; eight output warps and z a half chunk ahead 792; the MMA chains apart and
-// elected issuing lanes 691; code that fits the instruction caches (81 -> 55 KB: rolled
-// loops, waits out of line) 670; x freed apart from B and C 652; twelve output warps 629.
+// What bounds it: the instructions of the roles around the products, and their latency, of
+// the output's above all (5100 per scheduler and chunk, at a little over one in two cycles; the tensor pipe
+// is busy a quarter of the time); memory next.  48 heads of 128 x 128, BF16, z: 32768 tokens
+// of one sequence 495 us (the first launch 115 us, 1.3 us a chunk; the second 375 us, 4.4 us
+// a chunk; 1.48 GB: 3.0 TB/s).  Steps on the way, 32768 tokens: z by 2-byte loads in the
+// output 1052 us; fragments 883; eight output warps and z a half chunk ahead 792; the MMA
+// chains apart and elected issuing lanes 691; code that fits the instruction caches (81 -> 55
+// KB: rolled loops, waits out of line) 670; x freed apart from B and C 652; twelve output
+// warps 629; packed gates 619; the output in quarters of a chunk with two product buffers
+// 550; descriptors stepped between MMAs 527; the first launch from the end 500; z and y
+// addresses stepped 495.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -79,7 +83,7 @@ constexpr uint32_t SM_TOTAL = SM_MISC + 512;
 static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
 
 enum {
-    B_FULL, B_XFULL = B_FULL + kMaxStages,                       // B and C, and x, of a stage landed
+    B_FULL, B_XFULL = B_FULL + kMaxStages,  // B and C, and x, of a stage landed
     B_GATE = B_XFULL + kMaxStages,
     B_BCFREE = B_GATE + kMaxStages, B_EMPTY = B_BCFREE + kMaxStages,  // B and C, and x and the gates, are read
     B_G = B_EMPTY + kMaxStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S,
@@ -1066,19 +1070,22 @@ std::atomic<int*> g_status_word[64];  // its address on the devices it was asked
 // Segments: with H heads, SMs / H segments of all tokens together fill the device; a
 // segment is that share of the call's chunks, but at least a 16th of them (a segment sums
 // the contributions of those before it).  One sequence, BF16, 128 x 128, us at segments of
-// the share and at the next ones: 48 heads, 768 tokens (2 chunks) 38 (3 chunks 44, uncut 48),
-// 2048 (6) 68 (3 chunks 80, 8 81, uncut 101); 16 heads, 1024 (1) 32 (2 chunks 37, 4 48,
-// uncut 55); 8 heads, 4096 (2) 44 (4 chunks 54, uncut 181).  Two chunks stay uncut (24
-// against 27).  Several sequences are mostly whole segments, for which the first launch is
-// in vain, so theirs are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of
-// 4 chunks 76, uncut 70; 4 of 128: of 2 chunks 37, uncut 32).
+// the share and at others: 48 heads, 1024 tokens (3 chunks) 40 (2 chunks 50, 4 44, uncut 48),
+// 2048 (6) 59 (3 chunks 67, uncut 81); 16 heads, 1024 (1) 32 (2 chunks 34, 4 42, uncut 46);
+// 8 heads, 4096 (2) 41 (4 chunks 46, uncut 145).  The first launch costs what 3 chunks do:
+// sequences stay whole where segments save fewer (48 heads, 512 tokens: of 2 chunks 34,
+// uncut 32; 16 heads, 384: of 1 chunk 28, uncut 26; 512: of 1 chunk 28, uncut 30).
+// Several sequences are mostly whole segments, for which that launch is in vain, so theirs
+// are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of 4 chunks 67, uncut
+// 61; 8 of 128: of 2 chunks 52, uncut 44).
 int64_t ssm_scan_segment(int64_t T, int n_seq, int n_heads, int sm_count) {
-    const int64_t chunks = (T + L - 1) / L, least = n_seq > 1 ? 4 : chunks < 3 ? chunks : 1;
+    const int64_t chunks = (T + L - 1) / L, least = n_seq > 1 ? 4 : 1;
     int64_t parts = sm_count / n_heads;
     if (parts > 16) parts = 16;
     if (parts < 1) parts = 1;
-    const int64_t share = (chunks + parts - 1) / parts;
-    return (share < least ? least : share) * L;
+    int64_t share = (chunks + parts - 1) / parts;
+    if (share < least) share = least;
+    return (chunks - share < 3 ? chunks : share) * L;
 }
 
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq) {

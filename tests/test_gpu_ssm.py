@@ -481,3 +481,82 @@ def test_another_stream():
         torch.cuda.synchronize()
         for (y, st), (wy, ws) in zip(got, want):
             assert torch.equal(y, wy) and torch.equal(st, ws)
+
+
+@pytest.mark.parametrize("dtype,T", [(BF16, 1000), (F16, 1300)])
+def test_segmented_scans_in_a_row(dtype, T):
+    """Scans over segments one right behind the other, each reusing the workspace of the one before and
+    going on from its state, eager and as replays of one graph: always the bits of calls far apart."""
+    gen = torch.Generator().manual_seed(T)
+    H, G, P, N = 8, 2, 128, 128
+    sets = [layer(gen, T, H, G, P, N, dtype) for _ in range(3)]
+    start = rnd(gen, 1, H, N, P)
+    apart, st = [], start.clone()
+    for s in sets:
+        apart.append(gdn.gdn_ssm_scan(*s, st).clone())
+        torch.cuda.synchronize()
+    end = st.clone()
+
+    def run(st):
+        return [gdn.gdn_ssm_scan(*s, st) for s in sets]
+
+    for _ in range(5):
+        st = start.clone()
+        got = run(st)
+        torch.cuda.synchronize()
+        assert torch.equal(st, end) and all(torch.equal(u, v) for u, v in zip(got, apart))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(st)
+    for _ in range(5):
+        st.copy_(start)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(st, end) and all(torch.equal(u, v) for u, v in zip(got, apart))
+    assert gdn.gdn_device_status() == gdn.GDN_OK
+
+
+def test_more_sequences_than_threads():
+    gen = torch.Generator().manual_seed(31)
+    lens = [(20, 50, 31)[i % 3] for i in range(800)]
+    cu, T = packed(lens)
+    H, G, P, N = 2, 1, 64, 64
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, G, P, N, BF16)
+    states = rnd(gen, len(lens), H, N, P, scale=0.3)
+    out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    y, st, mag, smag = ref.scan(x, a, B, C, A_log, dt_bias, states, None, None, cu, None, None, out)
+    gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states, cu_seqlens=cu, out=out)
+    torch.cuda.synchronize()
+    check(out, y, mag, scan_bound(BF16, P, N, 50), "y")
+    check(states, st, smag, scan_bound(F32, P, N, 50), "states")
+
+
+@pytest.mark.parametrize("dtype,T", [(F32, 60), (BF16, 700)])
+def test_nan_in_a_gate_reaches_its_head_from_there_on(dtype, T):
+    gen = torch.Generator().manual_seed(32)
+    H, G, P, N, at = 4, 2, 128, 128, T // 2
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, G, P, N, dtype)
+    states = rnd(gen, 1, H, N, P)
+    want_st = states.clone()
+    want = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, want_st)
+    a[at, 1] = float("nan")
+    y = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states)
+    torch.cuda.synchronize()
+    other = [0, 2, 3]
+    assert torch.equal(y[:, other], want[:, other]) and torch.equal(states[:, other], want_st[:, other])
+    assert torch.equal(y[:at, 1], want[:at, 1]) and bool(y[at:, 1].isnan().all()) and bool(states[:, 1].isnan().all())
+
+
+def test_one_row_for_every_token():
+    """Inputs expanded along the tokens (stride 0) give what their copies give in the same form."""
+    gen = torch.Generator().manual_seed(33)
+    H, G, P, N, T = 2, 1, 64, 64, 150
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, G, P, N, F32)
+    B1, a1 = B[:1].expand(T, G, N), a[:1].expand(T, H)
+    got = gdn.gdn_ssm_scan(x, a1, B1, C, A_log, dt_bias, z=x[:1].expand(T, H, P))
+    want = gdn.gdn_ssm_scan(x, a1.contiguous(), B1.contiguous(), C, A_log, dt_bias, z=x[:1].expand(T, H, P).contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    rows = rnd(gen, 1, 40).expand(T, 40)
+    w = rnd(gen, 40, 4)
+    assert torch.equal(gdn.gdn_ssm_conv(rows, w), gdn.gdn_ssm_conv(rows.contiguous(), w))
