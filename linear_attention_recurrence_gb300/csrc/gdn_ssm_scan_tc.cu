@@ -35,16 +35,16 @@
 // time although a lane's row is a column of x.
 //
 // What bounds it: the instructions of the roles around the products, and their latency, of
-// the output's above all (5100 per scheduler and chunk, at a little over one in two cycles; the tensor pipe
-// is busy a quarter of the time); memory next.  48 heads of 128 x 128, BF16, z: 32768 tokens
-// of one sequence 495 us (the first launch 115 us, 1.3 us a chunk; the second 375 us, 4.4 us
-// a chunk; 1.48 GB: 3.0 TB/s).  Steps on the way, 32768 tokens: z by 2-byte loads in the
-// output 1052 us; fragments 883; eight output warps and z a half chunk ahead 792; the MMA
-// chains apart and elected issuing lanes 691; code that fits the instruction caches (81 -> 55
-// KB: rolled loops, waits out of line) 670; x freed apart from B and C 652; twelve output
-// warps 629; packed gates 619; the output in quarters of a chunk with two product buffers
-// 550; descriptors stepped between MMAs 527; the first launch from the end 500; z and y
-// addresses stepped 495.
+// the output's above all (5100 per scheduler and chunk, at a little over one in two cycles;
+// the tensor pipe is busy a quarter of the time); memory next.  48 heads of 128 x 128, BF16,
+// z: 32768 tokens of one sequence 491 us (the first launch 115 us, 1.3 us a chunk; the second
+// 372 us, 4.3 us a chunk; 1.48 GB: 3.0 TB/s).  Steps on the way, 32768 tokens: z by 2-byte
+// loads in the output 1052 us; fragments 883; eight output warps and z a half chunk ahead
+// 792; the MMA chains apart and elected issuing lanes 691; code that fits the instruction
+// caches (81 -> 55 KB: rolled loops, waits out of line) 670; x freed apart from B and C 652;
+// twelve output warps 629; packed gates 619; the output in quarters of a chunk with two
+// product buffers 550; descriptors stepped between MMAs 527; the first launch from the end
+// 500; z and y addresses stepped 495; a quarter of Y1 ahead of G 491.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                         mma_ts(tm + TM_Y2 + 64 * half, tm + TM_HB + 32 * k + 8 * j, dc + 2 * j, ID_Y2, j > 0 || k > 0);
                 return true;
             };
-            // Order: H^T C^T, the second half of G, two quarters of Y1, H^T C^T, the next chunk's first
-            // half of G, two quarters of Y1: what a quarter of the output needs while the one before
+            // Order: H^T C^T, a quarter of Y1, the second half of G, a quarter of Y1, and again with the
+            // next chunk's first half of G: what a quarter of the output needs while the one before
             // is read.  (A loop over the halves: the code of all roles
             // has to fit the instruction caches.)
             bool ok = wait_phase(sy, B_FULL, 0) && issue_g(0, 0);
@@ -558,11 +558,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     umma_commit(&bar[B_HBFREE]);
                     umma_commit(&bar[B_BCFREE + c % STAGES]);
                 }
-                if (next < nch) {
+                ok = issue_y1(c, 2 * half);
+                if (ok && next < nch) {
                     if (half) ok = wait_phase(sy, B_FULL + next % STAGES, next / STAGES);
                     ok = ok && issue_g(next, half ^ 1);
                 }
-                ok = ok && issue_y1(c, 2 * half) && issue_y1(c, 2 * half + 1);
+                ok = ok && issue_y1(c, 2 * half + 1);
                 if (half && ok) {
                     umma_commit(&bar[B_MFREE]);
                     umma_commit(&bar[B_EMPTY + c % STAGES]);
