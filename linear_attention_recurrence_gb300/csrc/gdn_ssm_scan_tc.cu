@@ -367,6 +367,61 @@ __device__ bool find_unit(const SsmSeqs& q, int seg, int64_t units, int64_t u, U
     return found.s >= 0;
 }
 
+// The same for unit v of the segments that are not their sequence's last; *u: its number among all.
+__device__ bool find_inner_unit(const SsmSeqs& q, int seg, int64_t units, int64_t v, int64_t* u, Unit* out, void* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreadsTc / 32;
+    int64_t* warp_sum = static_cast<int64_t*>(scratch);
+    int* warp_seqs = reinterpret_cast<int*>(warp_sum + kWarps);
+    __shared__ Unit found;
+    __shared__ int64_t found_u;
+    if (tid == 0) found.s = -1;
+    int64_t base = 0, seqs = 0;  // segments, and sequences that have some
+    for (int s0 = 0; s0 < q.n_seq; s0 += kThreadsTc) {
+        int64_t b = 0, e = 0;
+        if (s0 + tid < q.n_seq) seq_rows(q, s0 + tid, b, e);
+        const int n = static_cast<int>((e - b + seg - 1) / seg);
+        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+        int64_t inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t w = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += w;
+        }
+        if (lane == 31) {
+            warp_sum[warp] = inc;
+            warp_seqs[warp] = __popc(some);
+        }
+        __syncthreads();
+        int64_t first = base + inc - n, inner = -seqs - __popc(some & ((1u << lane) - 1));
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) {
+                first += warp_sum[w];
+                inner -= warp_seqs[w];
+            }
+            base += warp_sum[w];
+            seqs += warp_seqs[w];
+        }
+        inner += first;  // those before that are not last ones
+        if (v >= inner && v < inner + n - 1 && first + n <= units) {
+            const int k = static_cast<int>(v - inner);
+            found.s = s0 + tid;
+            found.k = k;
+            found.n_seg = n;
+            found.begin = b + static_cast<int64_t>(k) * seg;
+            found.len = seg;
+            found_u = first + k;
+        }
+        __syncthreads();
+        if (base - seqs > v) break;  // uniform
+    }
+    __syncthreads();
+    *out = found;
+    *u = found_u;
+    return found.s >= 0;
+}
+
 // PASS 0: outputs (and final states); PASS 1: the segments' contributions.
 template <bool BF16, int P, int N, int PASS>
 __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid_constant__ TcParams p) {
@@ -396,11 +451,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     const int h = blockIdx.x % p.n_heads;
-    const int64_t u = blockIdx.x / p.n_heads;
+    int64_t u = blockIdx.x / p.n_heads;
     Unit un;
-    if (!find_unit(p.q, p.seg, p.units, u, &un, warp_sum)) return;
+    if constexpr (OUT) {
+        if (!find_unit(p.q, p.seg, p.units, u, &un, warp_sum)) return;
+    } else {  // (nothing reads a last segment's contribution)
+        if (!find_inner_unit(p.q, p.seg, p.units, u, &u, &un, warp_sum)) return;
+    }
     if constexpr (PASS == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (PASS == 1 && un.k == un.n_seg - 1) return;  // nothing reads a last segment's contribution
     const int g = h % p.n_groups;
     const int nch = (un.len + L - 1) / L;
 
@@ -1033,11 +1091,12 @@ template <bool BF16, int P, int N>
 cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
     constexpr int bytes = SM_TOTAL + 1024;
     const unsigned grid = static_cast<unsigned>(units * p.n_heads);
+    const unsigned inner = static_cast<unsigned>((units - p.q.n_seq) * p.n_heads);  // (T / seg: no fewer than are not last ones)
     cudaError_t e;
     if (p.ws) {
         e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 1>), bytes);
         if (e != cudaSuccess) return e;
-        ssm_scan_tc_kernel<BF16, P, N, 1><<<grid, kThreadsTc, bytes, s>>>(p);
+        ssm_scan_tc_kernel<BF16, P, N, 1><<<inner, kThreadsTc, bytes, s>>>(p);
         internal_count_launch();
     }
     e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 0>), bytes);
