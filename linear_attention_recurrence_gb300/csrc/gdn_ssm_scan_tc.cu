@@ -1102,7 +1102,7 @@ cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
     e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 0>), bytes);
     if (e != cudaSuccess) return e;
     // Behind a first launch the second starts on the SMs as they fall free, and waits where it
-    // first needs what that one leaves (2048 tokens, 48 heads: 65 -> 61 us).
+    // first needs what that one leaves (2048 tokens, 48 heads: 61 us, 65 without).
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreadsTc);
@@ -1137,7 +1137,7 @@ std::atomic<int*> g_status_word[64];  // its address on the devices it was asked
 // uncut 32; 16 heads, 384: of 1 chunk 28, uncut 26; 512: of 1 chunk 28, uncut 30).
 // Several sequences are mostly whole segments, for which that launch is in vain, so theirs
 // are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of 4 chunks 67, uncut
-// 61; 8 of 128: of 2 chunks 52, uncut 44).
+// 61; 8 of 128: of 2 chunks 50, uncut 42).
 int64_t ssm_scan_segment(int64_t T, int n_seq, int n_heads, int sm_count) {
     const int64_t chunks = (T + L - 1) / L, least = n_seq > 1 ? 4 : 1;
     int64_t parts = sm_count / n_heads;
