@@ -76,7 +76,7 @@ constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: gamma[128] at 0, dt at 128, w at
-constexpr uint32_t SM_GATE_STAGE = 1664;                // 256, 2^k of w and 2^j of dt at 384
+constexpr uint32_t SM_GATE_STAGE = 1664;                // 256, 2^k of w and 2^j of dt at 384, PASS 1's sum behind at 386
 constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
 constexpr uint32_t SM_MISC = SM_IO + 4 * kOutGroups * 512;
 constexpr uint32_t SM_TOTAL = SM_MISC + 512;
@@ -922,7 +922,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             float* dst = PASS == 1 ? p.ws + (u * p.n_heads + h) * N * P + pcol : pool;
             // (PASS 1) a first segment's includes the state before it, with the segment's decay
             const float* before = PASS == 1 && un.k == 0 ? dst + (un.n_seg - 1) * static_cast<int64_t>(p.n_heads) * N * P : nullptr;
-            const float decay = PASS == 1 ? exp2f(reinterpret_cast<const float*>(sm + GATE_AT + (nch - 1) % STAGES * SM_GATE_STAGE)[386]) : 0.f;
+            const float* last_gates = reinterpret_cast<const float*>(sm + GATE_AT + (nch - 1) % STAGES * SM_GATE_STAGE);
+            const float decay = PASS == 1 ? exp2f(last_gates[386]) : 0.f;
             if (PASS == 1 && tid == 0) p.ws_decay[u * p.n_heads + h] = decay;
             if (live) {
 #pragma unroll 1
@@ -1091,7 +1092,8 @@ template <bool BF16, int P, int N>
 cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
     constexpr int bytes = SM_TOTAL + 1024;
     const unsigned grid = static_cast<unsigned>(units * p.n_heads);
-    const unsigned inner = static_cast<unsigned>((units - p.q.n_seq) * p.n_heads);  // (T / seg: no fewer than are not last ones)
+    // (T / seg: no fewer than the segments of disjoint sequences that are not last ones)
+    const unsigned inner = static_cast<unsigned>((units - p.q.n_seq) * p.n_heads);
     cudaError_t e;
     if (p.ws) {
         e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 1>), bytes);
