@@ -156,8 +156,13 @@ __global__ void __launch_bounds__(kThreads, 5) ssm_conv_kernel(const SsmConvPara
                 }
             }
         } else {
+            // (the tile's edge is K - 1 rows into the sequence at least, unless bounds step back
+            // and r is where an overlapping sequence ended: rows before the sequence are not read)
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) load_vec<T, VEC>(x + (r - (K - 1) + j) * p.x_stride, win[j]);
+            for (int j = 0; j < K - 1; ++j) {
+                const int64_t at = r - (K - 1) + j;
+                load_vec<T, VEC>(x + (at > b ? at : b) * p.x_stride, win[j]);
+            }
         }
         const int64_t stop = e < hi ? e : hi;
         const T* xr = x + r * p.x_stride;
