@@ -272,9 +272,9 @@ int gdn_recurrence_chunked_noalloc(const float* q, const float* k, const float* 
  * rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of the T rows (cu_seqlens [n_seq + 1],
  * on the device, not decreasing; NULL: one sequence of all T rows).  Rows before
  * cu_seqlens[0] and from cu_seqlens[n_seq] on belong to no sequence: their outputs
- * are left as they were.  Bounds outside [0, T] or out of order make their sequence
- * empty; where bounds step back so that sequences overlap, the outputs and slots of
- * those sequences are undefined (nothing else is touched).
+ * are left as they were.  A sequence with a bound outside [0, T] is empty.  Where
+ * bounds decrease, the call's outputs and the slots that it names are undefined, of
+ * its sound sequences too; nothing outside its arrays is read or written.
  *
  * Slots: sequence s keeps its state (and its convolution history) in slot slots[s]
  * of a pool of n_slots (slots NULL: slot s).  It starts from the slot's content

@@ -105,8 +105,11 @@ __device__ __forceinline__ float ssm_rate(float A_log) { return fmaxf(-expf(A_lo
 constexpr float kMinLog2Decay = -256.0f;
 
 // The packed sequences of a call: sequence s has rows [begin, end) of the packed rows.
-// Bounds outside [0, T] or out of order give an empty sequence, so no row outside the
-// arrays is touched whatever cu_seqlens holds.
+// A bound outside [0, T], or an end below its begin, gives an empty sequence, so every row
+// that a sequence has is one of the arrays'.  Bounds that decrease between sequences can make
+// them overlap or put them out of order, which no kernel looks for: what they leave is
+// undefined, so each holds what it derives from other sequences' bounds (a window's rows, a
+// unit's number) to its own arrays.
 struct SsmSeqs {
     const int32_t* cu;         // [n_seq + 1], or nullptr: one sequence of T rows
     const int32_t* slots;      // [n_seq], or nullptr: sequence s has slot s

@@ -447,7 +447,7 @@ def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_st
     x: [T][channels], FP32, BF16 or FP16, the rows any distance apart; w:
     [channels][width] and bias: [channels] (FP32), width 2 to 4; hist:
     [slots][width - 1][channels] of x's type, or None (sequences start from zeros).
-    cu_seqlens: [n + 1] int32 on the device (None: one sequence); slots: [n] int32
+    cu_seqlens: [n + 1] int32 on the device, not decreasing (None: one sequence); slots: [n] int32
     (None: sequence i has slot i; -1: no slot); has_state: [n] bool (None: all
     continue from their slots).  ``out`` ([T][channels]) is allocated if None; rows
     of no sequence are left as they were.
