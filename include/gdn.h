@@ -333,7 +333,8 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
  * There the decayed scores and the state (for its product with C) are rounded once to
  * `dtype`, while the state itself keeps FP32's precision.  For GDN_F16 this asks that
  * C . B and the state stay in FP16's range (below 65504; beyond it y is not finite),
- * and it keeps the state to 2^-24 of a chunk's largest step.  A NaN or infinity in x
+ * and a chunk's part of a state is off by up to 2^-24 max(w, 2^-60) sum |B|, w its steps
+ * times the decay behind them (the parts' smallest step).  A NaN or infinity in x
  * reaches, besides its own and later tokens, the outputs of the up to 127 tokens of
  * the same sequence before it that share its chunk.
  */

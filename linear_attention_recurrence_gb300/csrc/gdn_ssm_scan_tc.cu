@@ -16,7 +16,7 @@
 // the chunk's end, so neither loses precision when the decay over the chunk is large.
 // FP16's range is short: there dt and w enter M and the update divided by a power of two
 // of each chunk (its largest dt, its largest w), which the output and the state's decay
-// multiply back, so neither small steps nor large ones leave the range.
+// multiply back, so no step from 2^-60 to 2^24 leaves the range.
 //
 // Work is one CTA per (head, segment of a sequence); it walks the segment's chunks.
 // Where sequences x heads do not fill the device, sequences are cut into segments: a
@@ -224,11 +224,11 @@ __device__ __forceinline__ float unpack1(uint16_t v) {
     return __half2float(__ushort_as_half(v));
 }
 
-// The power of two just above v, from 2^-14 (the state times its inverse stays far from
-// overflow) to 2^24.
+// The power of two just above v, from 2^-60 (tensor memory holds the state times its inverse,
+// in FP32: a state up to 2^67 stays finite there) to 2^24.
 __device__ __forceinline__ float range_scale(float v) {
     int e = static_cast<int>((__float_as_uint(v) >> 23) & 255) - 126;
-    e = e < -14 ? -14 : e > 24 ? 24 : e;
+    e = e < -60 ? -60 : e > 24 ? 24 : e;
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
