@@ -12,8 +12,10 @@
 // of the rows' own type: H is rounded to it for the product with C (as M is: together
 // one rounding of disjoint terms of y), but the update takes w o x in parts of that type
 // (three of 8 bits for BF16, two of 11 for FP16), so the state keeps FP32's precision.
-// M is formed by exponentials of differences (never above 0), w from sums that start at
-// the chunk's end, so neither loses precision when the decay over the chunk is large.
+// An exponent of M is the sum of the log-decays behind token i up to t, from sums that start
+// anew every 4 tokens (the difference of two sums from the chunk's start, up to 2^15, would be
+// off by 2^-9); w comes from sums that start at the chunk's end.  So neither loses precision
+// when the decay over the chunk is large.
 // FP16's range is short: there dt and w enter M and the update divided by a power of two
 // of each chunk (its largest dt, its largest w), which the output and the state's decay
 // multiply back, so no step from 2^-60 to 2^24 leaves the range.
@@ -75,12 +77,22 @@ constexpr uint32_t TM_COLS = 512;
 constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
-constexpr uint32_t SM_GATE = SM_M + 24576;              // per stage, floats: gamma[128] at 0, dt at 128, w at
-constexpr uint32_t SM_GATE_STAGE = 1664;                // 256, 2^k of w and 2^j of dt at 384, PASS 1's sum behind at 386
+constexpr uint32_t SM_GATE = SM_M + 24576;
+constexpr uint32_t SM_GATE_STAGE = 2320;
 constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
 constexpr uint32_t SM_MISC = SM_IO + 4 * kOutGroups * 512;
-constexpr uint32_t SM_TOTAL = SM_MISC + 512;
-static_assert(SM_TOTAL + 1024 <= 227 * 1024, "shared memory of the tensor form");
+constexpr uint32_t SM_TOTAL = SM_MISC + 464;
+static_assert(SM_TOTAL <= 227 * 1024, "shared memory of the tensor form");
+// A stage's gates, floats; log-decays are to the base 2.
+constexpr uint32_t GT_COL = 0;      // M's column i: the sum of i's group of 4 tokens up to i, less log2 dt_i
+constexpr uint32_t GT_ROW = 128;    // M's row t: the sum of t's group up to t
+constexpr uint32_t GT_W = 256;      // w
+constexpr uint32_t GT_E = 384;      // e^gamma_t
+constexpr uint32_t GT_GROUP = 512;  // the sum of each of the 32 groups
+constexpr uint32_t GT_FAR = 544;    // the sum from token 64 to each later group's start
+constexpr uint32_t GT_WSCALE = 560, GT_DTSCALE = 561;  // 2^k of w and 2^j of dt (FP16)
+constexpr uint32_t GT_SUM = 562;    // the sum of the chunk (PASS 1: and of those behind it)
+static_assert((GT_SUM + 1) * 4 <= SM_GATE_STAGE, "gates");
 
 enum {
     B_FULL, B_XFULL = B_FULL + kMaxStages,  // B and C, and x, of a stage landed
@@ -96,7 +108,7 @@ enum {
     NBAR
 };
 static_assert(kOutGroups >= 3, "the output warps bring the state's rows 32 .. 127");
-static_assert(SM_MISC + NBAR * 8 + 24 <= SM_TOTAL, "barrier space");
+static_assert(SM_MISC + NBAR * 8 + 16 <= SM_TOTAL, "barrier space");
 
 __device__ int g_ssm_status;  // bits of kDevErr*
 
@@ -325,9 +337,16 @@ struct Unit {
     int64_t begin;        // first row
     int len;              // rows
 };
-__device__ bool find_unit(const SsmSeqs& q, int seg, int64_t units, int64_t u, Unit* out, int* warp_sum) {
+struct UnitScratch {  // shared memory of the search
+    int64_t warp_sum[kThreadsTc / 32];
+    int warp_seqs[kThreadsTc / 32];
+    Unit found;
+    int64_t found_u;
+};
+__device__ bool find_unit(const SsmSeqs& q, int seg, int64_t units, int64_t u, Unit* out, UnitScratch& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ Unit found;
+    int* warp_sum = sh.warp_seqs;
+    Unit& found = sh.found;
     if (tid == 0) found.s = -1;
     int64_t base = 0;
     for (int s0 = 0; s0 < q.n_seq; s0 += kThreadsTc) {
@@ -368,13 +387,14 @@ __device__ bool find_unit(const SsmSeqs& q, int seg, int64_t units, int64_t u, U
 }
 
 // The same for unit v of the segments that are not their sequence's last; *u: its number among all.
-__device__ bool find_inner_unit(const SsmSeqs& q, int seg, int64_t units, int64_t v, int64_t* u, Unit* out, void* scratch) {
+__device__ bool find_inner_unit(const SsmSeqs& q, int seg, int64_t units, int64_t v, int64_t* u, Unit* out,
+                                UnitScratch& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreadsTc / 32;
-    int64_t* warp_sum = static_cast<int64_t*>(scratch);
-    int* warp_seqs = reinterpret_cast<int*>(warp_sum + kWarps);
-    __shared__ Unit found;
-    __shared__ int64_t found_u;
+    int64_t* warp_sum = sh.warp_sum;
+    int* warp_seqs = sh.warp_seqs;
+    Unit& found = sh.found;
+    int64_t& found_u = sh.found_u;
     if (tid == 0) found.s = -1;
     int64_t base = 0, seqs = 0;  // segments, and sequences that have some
     for (int s0 = 0; s0 < q.n_seq; s0 += kThreadsTc) {
@@ -442,11 +462,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     constexpr uint32_t STAGE_BYTES = OUT ? SM_STAGE : 4 * kBox, B_AT = OUT ? SM_B : 0, X_AT = OUT ? SM_X : 2 * kBox;
     constexpr uint32_t GATE_AT = OUT ? SM_GATE : SM_M;
     static_assert(STAGES <= kMaxStages && 3 * 4 * kBox <= SM_M, "stages");
-    unsigned char* sm = aligned_dynamic_smem<unsigned char, 1024>();
+    // (all of the SM's shared memory is used, so there is none to round the address up in: the
+    // kernel has no other, and its start is a multiple of 1024 as declared, or it gives up)
+    extern __shared__ __align__(1024) unsigned char ssm_tc_smem[];
+    unsigned char* sm = ssm_tc_smem;
+    if (smem_addr(sm) % 1024 != 0) {
+        if (threadIdx.x == 0) report_error(p.status, kDevErrLayout);
+        return;
+    }
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM_MISC + NBAR * 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM_MISC + NBAR * 8 + 8);
-    int* warp_sum = reinterpret_cast<int*>(sm + GATE_AT);  // before the gates are written
+    UnitScratch& scratch = *reinterpret_cast<UnitScratch*>(sm + GATE_AT);  // before the gates are written
     const Sync sy{bar, abort_flag, p.status};
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -454,9 +481,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
     int64_t u = blockIdx.x / p.n_heads;
     Unit un;
     if constexpr (OUT) {
-        if (!find_unit(p.q, p.seg, p.units, u, &un, warp_sum)) return;
+        if (!find_unit(p.q, p.seg, p.units, u, &un, scratch)) return;
     } else {  // (nothing reads a last segment's contribution)
-        if (!find_inner_unit(p.q, p.seg, p.units, u, &u, &un, warp_sum)) return;
+        if (!find_inner_unit(p.q, p.seg, p.units, u, &u, &un, scratch)) return;
     }
     if constexpr (PASS == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int g = h % p.n_groups;
@@ -683,28 +710,31 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 sum += g2[i];
                 pre[i] = sum;
             }
-            float up = sum, down = sum;  // inclusive sums over the lanes, from either end
+            float up = sum, down = sum;  // inclusive sums over the lanes, from the half's start and the end
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, up, off), y = __shfl_down_sync(0xffffffffu, down, off);
-                if (lane >= off) up += x;
+                const float y = __shfl_down_sync(0xffffffffu, down, off);
                 if (lane + off < 32) down += y;
+                if (OUT && off < 16) {
+                    const float x = __shfl_up_sync(0xffffffffu, up, off);
+                    if ((lane & 15) >= off) up += x;
+                }
             }
+            const float first_half = __shfl_sync(0xffffffffu, up, 15);
             up = __shfl_up_sync(0xffffffffu, up, 1);
             down = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) up = 0.f;
+            if ((lane & 15) == 0) up = 0.f;
             if (lane == 31) down = 0.f;
             float behind = 0.f;  // (PASS 1) the sum over the segment's chunks behind this one
             if (!OUT && c > 0) {
                 if (!wait_warp(sy, B_GATE + (c - 1) % STAGES, (c - 1) / STAGES)) break;
-                behind = reinterpret_cast<const float*>(sm + GATE_AT + (c - 1) % STAGES * SM_GATE_STAGE)[386];
+                behind = reinterpret_cast<const float*>(sm + GATE_AT + (c - 1) % STAGES * SM_GATE_STAGE)[GT_SUM];
             }
             float after = down + behind;
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
                 suf[i] = after;
                 after += g2[i];
-                pre[i] += up;
             }
             float* gt = reinterpret_cast<float*>(sm + GATE_AT + s * SM_GATE_STAGE);
             float w[4];
@@ -724,17 +754,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     dt[i] *= 1.0f / ds;
                 }
                 if (lane == 0) {
-                    gt[384] = ws;
-                    gt[385] = ds;
+                    gt[GT_WSCALE] = ws;
+                    gt[GT_DTSCALE] = ds;
                 }
             }
             if constexpr (OUT) {
-                reinterpret_cast<float4*>(gt)[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
-                reinterpret_cast<float4*>(gt + 128)[lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+                float col[4], e[4];
+                const float before = lane < 16 ? up : first_half + up;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    col[i] = pre[i] - lg2(dt[i]);  // (no step: infinity, a factor of 0)
+                    e[i] = ex2(before + pre[i]);
+                }
+                reinterpret_cast<float4*>(gt + GT_COL)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+                reinterpret_cast<float4*>(gt + GT_ROW)[lane] = make_float4(pre[0], pre[1], pre[2], pre[3]);
+                reinterpret_cast<float4*>(gt + GT_E)[lane] = make_float4(e[0], e[1], e[2], e[3]);
+                gt[GT_GROUP + lane] = sum;
+                if (lane >= 16) gt[GT_FAR + lane - 16] = up;
             } else if (lane == 0) {
-                gt[386] = after;  // with this chunk's
+                gt[GT_SUM] = after;  // with this chunk's
             }
-            reinterpret_cast<float4*>(gt + 256)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<float4*>(gt + GT_W)[lane] = make_float4(w[0], w[1], w[2], w[3]);
             warp_arrive(sy, B_GATE + s);
         }
     } else if (OUT && warp < 4) {
@@ -749,7 +789,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const int s = c % STAGES;
                 if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
                 const float* gd = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
-                const float gt = gd[t];
+                const float row = gd[GT_ROW + t];
                 bool ok = true;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++gi) {
@@ -758,27 +798,31 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     tc_fence_after_sync();
                     unsigned char* m = half ? m1 : m0;
                     // 16 columns at a time, up to the block of 32 on the diagonal
-                    const int stop = half == 0 && warp >= 2 ? 64 : 32 * (warp + 1) - 64 * half;
+                    const bool far = half == 0 && warp >= 2;
+                    const int stop = far ? 64 : 32 * (warp + 1) - 64 * half;
+                    // the sum from a group's start to t, group after group from t's own down
+                    float base = far ? row + gd[GT_FAR + t / 4 - 16] : row;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < stop; j0 += 16) {
+                    for (int j0 = stop - 16; j0 >= 0; j0 -= 16) {
                         float v[16];
                         tmem_ld16(tm + lanes + TM_G + j0, v);
                         const int above = t - 64 * half - j0;  // columns past it are above the diagonal
-                        const float4* g4 = reinterpret_cast<const float4*>(gd + 64 * half + j0);
+                        const float4* c4 = reinterpret_cast<const float4*>(gd + GT_COL + 64 * half + j0);
+                        const float4 sums = *reinterpret_cast<const float4*>(gd + GT_GROUP + 16 * half + j0 / 4);
                         uint32_t o[8];
-                        float4 g, dt;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (i % 2 == 0) {
-                                g = g4[i / 2];
-                                dt = g4[32 + i / 2];
+                        for (int k = 3; k >= 0; --k) {
+                            const float4 c = c4[k];
+                            if (k < above >> 2) base += k == 3 ? sums.w : k == 2 ? sums.z : k == 1 ? sums.y : sums.x;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int j = 4 * k + 2 * i;
+                                const float2 d = ffma2(i ? make_float2(c.z, c.w) : make_float2(c.x, c.y),
+                                                       make_float2(-1.f, -1.f), make_float2(base, base));
+                                const float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(v[j], v[j + 1]));
+                                // selected, not multiplied: what is above may be anything
+                                o[j / 2] = pack2<BF16>(j > above ? 0.f : a.x, j + 1 > above ? 0.f : a.y);
                             }
-                            const float2 d = ffma2(i % 2 ? make_float2(g.z, g.w) : make_float2(g.x, g.y),
-                                                   make_float2(-1.f, -1.f), make_float2(gt, gt));
-                            float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), i % 2 ? make_float2(dt.z, dt.w) : make_float2(dt.x, dt.y));
-                            a = fmul2(a, make_float2(v[2 * i], v[2 * i + 1]));
-                            // selected, not multiplied: what is above may be anything
-                            o[i] = pack2<BF16>(2 * i > above ? 0.f : a.x, 2 * i + 1 > above ? 0.f : a.y);
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -832,14 +876,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 warp_arrive(sy, B_TAIL);
                 if (!wait_warp(sy, B_TAIL, 0)) break;
             }
-            const float next_scale = BF16 ? 1.f : gt[384];
+            const float next_scale = BF16 ? 1.f : gt[GT_WSCALE];
             // the state's decay, and its rounding for the product with C
             auto state_step = [&]() {
                 if (OUT && c == 0 && !wait_warp(sy, B_INIT, 0)) return false;
                 if (c > 0 && (!wait_warp(sy, B_S, c - 1) || (OUT && !wait_warp(sy, B_HBFREE, c - 1)))) return false;
                 tc_fence_after_sync();
                 if (live) {
-                    const float keep = (OUT ? ex2(gt[L - 1]) : 1.f) * (scale * (1.0f / next_scale));
+                    const float keep = (OUT ? gt[GT_E + L - 1] : 1.f) * (scale * (1.0f / next_scale));
 #pragma unroll 1
                     for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                         float v[32];
@@ -874,8 +918,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 uint32_t part[2][PARTS][4];
                 if (live) {
                     const uint32_t x = smem_addr(st) + X_AT + j * 2048;
-                    const float2 w0 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 2 * (lane & 3));
-                    const float2 w1 = *reinterpret_cast<const float2*>(gt + 256 + 16 * j + 8 + 2 * (lane & 3));
+                    const float2 w0 = *reinterpret_cast<const float2*>(gt + GT_W + 16 * j + 2 * (lane & 3));
+                    const float2 w1 = *reinterpret_cast<const float2*>(gt + GT_W + 16 * j + 8 + 2 * (lane & 3));
 #pragma unroll
                     for (int g2 = 0; g2 < 2; ++g2) {
                         uint32_t xr[4];
@@ -923,7 +967,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             // (PASS 1) a first segment's includes the state before it, with the segment's decay
             const float* before = PASS == 1 && un.k == 0 ? dst + (un.n_seg - 1) * static_cast<int64_t>(p.n_heads) * N * P : nullptr;
             const float* last_gates = reinterpret_cast<const float*>(sm + GATE_AT + (nch - 1) % STAGES * SM_GATE_STAGE);
-            const float decay = PASS == 1 ? exp2f(last_gates[386]) : 0.f;
+            const float decay = PASS == 1 ? exp2f(last_gates[GT_SUM]) : 0.f;
             if (PASS == 1 && tid == 0) p.ws_decay[u * p.n_heads + h] = decay;
             if (live) {
 #pragma unroll 1
@@ -1004,7 +1048,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const float* gt = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
                 if (!wait_warp(sy, B_GATE + s, c / STAGES) || !wait_warp(sy, B_XFULL + s, c / STAGES)) break;
                 const int nv = un.len - c * L;
-                const float m_scale = BF16 ? 1.f : gt[385];
+                const float m_scale = BF16 ? 1.f : gt[GT_DTSCALE];
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     ok = wait_warp(sy, B_Y1 + (q & 1), 2 * c + (q >> 1));
@@ -1024,8 +1068,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 load_z();
                             }
                             ldsm4t(x + t0 * 128, xr);
-                            const float2 gd = *reinterpret_cast<const float2*>(gt + t0 + 2 * (lane & 3));
-                            const float2 e2 = make_float2(ex2(gd.x), ex2(gd.y));
+                            const float2 e2 = *reinterpret_cast<const float2*>(gt + GT_E + t0 + 2 * (lane & 3));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -1090,7 +1133,7 @@ bool make_map16(CUtensorMap* m, bool bf16, const void* base, int64_t width, int6
 
 template <bool BF16, int P, int N>
 cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
-    constexpr int bytes = SM_TOTAL + 1024;
+    constexpr int bytes = SM_TOTAL;
     const unsigned grid = static_cast<unsigned>(units * p.n_heads);
     // (T / seg: no fewer than the segments of disjoint sequences that are not last ones)
     const unsigned inner = static_cast<unsigned>((units - p.q.n_seq) * p.n_heads);
