@@ -331,10 +331,12 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
  * and GDN_F16 with head_dim and state_dim 64 or 128, at least 32 tokens per sequence
  * on average, and x, B, C, z and y in rows of 16-byte pieces on 16-byte boundaries.
  * There the decayed scores and the state (for its product with C) are rounded once to
- * `dtype`, while the state itself keeps FP32's precision.  For GDN_F16 this asks that
- * C . B and the state stay in FP16's range (below 65504; beyond it y is not finite),
- * and a chunk's part of a state is off by up to 2^-24 max(w, 2^-60) sum |B|, w its steps
- * times the decay behind them (the parts' smallest step).  A NaN or infinity in x
+ * `dtype`, while the state itself keeps FP32's precision.  FP16's short range is held
+ * off by powers of two, so what is left of it are its smallest steps: a chunk's part of
+ * a state is off by up to 2^-24 max(w, 2^-60) sum |B|, w its steps times the decay
+ * behind them; a score by 2^-24 max(dt, 2^-60), the chunk's largest dt, or 2^-37 of the
+ * largest score of 32 neighbouring tokens if that is more; the state in its product with
+ * C by 2^-40 of the largest of 32 neighbouring columns.  A NaN or infinity in x
  * reaches, besides its own and later tokens, the outputs of the up to 127 tokens of
  * the same sequence before it that share its chunk.
  */

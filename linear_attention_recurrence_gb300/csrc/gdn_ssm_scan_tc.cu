@@ -18,7 +18,9 @@
 // when the decay over the chunk is large.
 // FP16's range is short: there dt and w enter M and the update divided by a power of two
 // of each chunk (its largest dt, its largest w), which the output and the state's decay
-// multiply back, so no step from 2^-60 to 2^24 leaves the range.
+// multiply back, so no step from 2^-60 to 2^24 leaves the range.  Nor do states and scores:
+// H is rounded relative to a power of two of each 32 columns of x (their largest element), and
+// where the scores of 32 tokens t pass the range, those are formed again relative to one of theirs.
 //
 // Work is one CTA per (head, segment of a sequence); it walks the segment's chunks.
 // Where sequences x heads do not fill the device, sequences are cut into segments: a
@@ -78,7 +80,7 @@ constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;
-constexpr uint32_t SM_GATE_STAGE = 2320;
+constexpr uint32_t SM_GATE_STAGE = 2304;
 constexpr uint32_t SM_IO = SM_GATE + kStages * SM_GATE_STAGE;  // an output warp's 512 bytes: 8 tokens x 32 columns
 constexpr uint32_t SM_MISC = SM_IO + 4 * kOutGroups * 512;
 constexpr uint32_t SM_TOTAL = SM_MISC + 464;
@@ -92,13 +94,18 @@ constexpr uint32_t GT_GROUP = 512;  // the sum of each of the 32 groups
 constexpr uint32_t GT_FAR = 544;    // the sum from token 64 to each later group's start
 constexpr uint32_t GT_WSCALE = 560, GT_DTSCALE = 561;  // 2^k of w and 2^j of dt (FP16)
 constexpr uint32_t GT_SUM = 562;    // the sum of the chunk (PASS 1: and of those behind it)
-static_assert((GT_SUM + 1) * 4 <= SM_GATE_STAGE, "gates");
+// FP16, powers of two: what H^T was divided by, of each 32 columns of x, and M (dt's included),
+// of each 32 tokens t
+constexpr uint32_t GT_HSCALE = 564, GT_MSCALE = 568;
+static_assert((GT_MSCALE + 4) * 4 <= SM_GATE_STAGE, "gates");
 
 enum {
     B_FULL, B_XFULL = B_FULL + kMaxStages,  // B and C, and x, of a stage landed
     B_GATE = B_XFULL + kMaxStages,
     B_BCFREE = B_GATE + kMaxStages, B_EMPTY = B_BCFREE + kMaxStages,  // B and C, and x and the gates, are read
-    B_G = B_EMPTY + kMaxStages, B_GFREE, B_M0, B_M1, B_MFREE, B_H, B_HBFREE, B_S,
+    B_H = B_EMPTY + kMaxStages,  // by stage: the state is rounded and decayed,
+    B_M = B_H + kMaxStages,      // and each half of M formed (with the powers of two of both)
+    B_G = B_M + 2 * kStages, B_GFREE, B_MFREE, B_HBFREE, B_S,
     B_Y1, B_Y1FREE = B_Y1 + 2,      // [2], by buffer
     B_Y2FREE = B_Y1FREE + 2,        // [2], by half
     B_XW = B_Y2FREE + 2,  // [8]
@@ -236,6 +243,13 @@ __device__ __forceinline__ float unpack1(uint16_t v) {
     return __half2float(__ushort_as_half(v));
 }
 
+// The larger magnitudes of two pairs of FP16, with some sign (a NaN counts as none).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // The power of two just above v, from 2^-60 (tensor memory holds the state times its inverse,
 // in FP32: a state up to 2^67 stays finite there) to 2^24.
 __device__ __forceinline__ float range_scale(float v) {
@@ -244,15 +258,17 @@ __device__ __forceinline__ float range_scale(float v) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // Arrivals that complete a phase of barrier b: one where a copy, a commit or the gate warp
 // arrives, 4 where a role's warps do; a stage is free when the MMAs and every role that
 // reads it are done.
 __device__ constexpr int arrivals(int b, bool out) {
     if (b >= B_BCFREE && b < B_EMPTY) return out ? 2 : 1;
     if (b >= B_EMPTY && b < B_EMPTY + kMaxStages) return out ? 9 + 4 * kOutGroups : 16;
-    if (b == B_H || b == B_TAIL) return out ? 4 : 16;
+    if ((b >= B_H && b < B_M) || b == B_TAIL) return out ? 4 : 16;
     if (b == B_INIT) return 4 * kOutGroups;
-    if (b == B_GFREE || b == B_M0 || b == B_M1) return 4;
+    if ((b >= B_M && b < B_G) || b == B_GFREE) return 4;
     if (b >= B_Y1FREE && b < B_XW) return 4 * kOutGroups;
     if (b == B_FIN) return out ? 2 : 1;
     if (b >= B_XW && b < B_XWFREE) return out ? 4 : 16;
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 return true;
             };
             auto issue_y1 = [&](int c, int q) {  // tokens t of quarter q, from tokens i up to its end
-                if ((q & 1) == 0 && !wait_phase(sy, q ? B_M1 : B_M0, c)) return false;
+                if ((q & 1) == 0 && !wait_phase(sy, B_M + 2 * (c % STAGES) + (q >> 1), c / STAGES)) return false;
                 if (yi > 1 && !wait_phase(sy, B_Y1FREE + (q & 1), (yi >> 1) - 1)) return false;
                 tc_fence_after_sync();
                 uint64_t dx = desc_mn(sm0 + (c % STAGES) * STAGE_BYTES + X_AT), dm = desc_k(sm0 + SM_M + q * 4096);
@@ -636,7 +652,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int n = 0; ok && n < 2 * nch; ++n) {
                 const int c = n >> 1, half = n & 1, next = c + half;
                 // (the state's rounding, B_H, comes after the zeroing of a last chunk's rows)
-                if (half == 0) ok = wait_phase(sy, B_XFULL + c % STAGES, c / STAGES) && wait_phase(sy, B_H, c);
+                if (half == 0) ok = wait_phase(sy, B_XFULL + c % STAGES, c / STAGES) && wait_phase(sy, B_H + c % STAGES, c / STAGES);
                 ok = ok && issue_y2(c, half);
                 if (!ok) break;
                 if (half) {
@@ -663,7 +679,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             bool ok = true;
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % STAGES;
-                if (!wait_phase(sy, B_FULL + s, c / STAGES) || (kStepped && !wait_phase(sy, B_H, c))) break;
+                if (!wait_phase(sy, B_FULL + s, c / STAGES) || (kStepped && !wait_phase(sy, B_H + s, c / STAGES))) break;
 #pragma unroll 1
                 for (int j = 0; j < L / 16; j += GROUP) {  // GROUP blocks to a barrier
                     const uint32_t group = (c * (L / 16) + j) / GROUP, slot = group % (SLOTS / GROUP);
@@ -788,8 +804,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             for (int c = 0; c < nch; ++c) {
                 const int s = c % STAGES;
                 if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
-                const float* gd = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
+                float* gd = reinterpret_cast<float*>(sm + GATE_AT + s * SM_GATE_STAGE);
                 const float row = gd[GT_ROW + t];
+                int shift = 0;          // (FP16) the scores of the warp's rows are formed times 2^shift
+                bool hopeless = false;  // (FP16) this row has an infinite score
                 bool ok = true;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half, ++gi) {
@@ -800,39 +818,71 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                     // 16 columns at a time, up to the block of 32 on the diagonal
                     const bool far = half == 0 && warp >= 2;
                     const int stop = far ? 64 : 32 * (warp + 1) - 64 * half;
-                    // the sum from a group's start to t, group after group from t's own down
-                    float base = far ? row + gd[GT_FAR + t / 4 - 16] : row;
+                    const int first_shift = shift;
+                    bool again = false;
+                    do {
+                        uint32_t largest = 0;  // (FP16) the row's largest magnitudes, a pair
+                        // the sum from a group's start to t, group after group from t's own down
+                        float base = far ? row + gd[GT_FAR + t / 4 - 16] : row;
+                        if constexpr (!BF16) base += static_cast<float>(shift);
 #pragma unroll 1
-                    for (int j0 = stop - 16; j0 >= 0; j0 -= 16) {
-                        float v[16];
-                        tmem_ld16(tm + lanes + TM_G + j0, v);
-                        const int above = t - 64 * half - j0;  // columns past it are above the diagonal
-                        const float4* c4 = reinterpret_cast<const float4*>(gd + GT_COL + 64 * half + j0);
-                        const float4 sums = *reinterpret_cast<const float4*>(gd + GT_GROUP + 16 * half + j0 / 4);
-                        uint32_t o[8];
+                        for (int j0 = stop - 16; j0 >= 0; j0 -= 16) {
+                            float v[16];
+                            tmem_ld16(tm + lanes + TM_G + j0, v);
+                            const int above = t - 64 * half - j0;  // columns past it are above the diagonal
+                            const float4* c4 = reinterpret_cast<const float4*>(gd + GT_COL + 64 * half + j0);
+                            const float4 sums = *reinterpret_cast<const float4*>(gd + GT_GROUP + 16 * half + j0 / 4);
+                            uint32_t o[8];
 #pragma unroll
-                        for (int k = 3; k >= 0; --k) {
-                            const float4 c = c4[k];
-                            if (k < above >> 2) base += k == 3 ? sums.w : k == 2 ? sums.z : k == 1 ? sums.y : sums.x;
+                            for (int k = 3; k >= 0; --k) {
+                                const float4 c = c4[k];
+                                if (k < above >> 2) base += k == 3 ? sums.w : k == 2 ? sums.z : k == 1 ? sums.y : sums.x;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int j = 4 * k + 2 * i;
-                                const float2 d = ffma2(i ? make_float2(c.z, c.w) : make_float2(c.x, c.y),
-                                                       make_float2(-1.f, -1.f), make_float2(base, base));
-                                const float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(v[j], v[j + 1]));
-                                // selected, not multiplied: what is above may be anything
-                                o[j / 2] = pack2<BF16>(j > above ? 0.f : a.x, j + 1 > above ? 0.f : a.y);
+                                for (int i = 0; i < 2; ++i) {
+                                    const int j = 4 * k + 2 * i;
+                                    const float2 d = ffma2(i ? make_float2(c.z, c.w) : make_float2(c.x, c.y),
+                                                           make_float2(-1.f, -1.f), make_float2(base, base));
+                                    const float2 a = fmul2(make_float2(ex2(d.x), ex2(d.y)), make_float2(v[j], v[j + 1]));
+                                    // selected, not multiplied: what is above may be anything
+                                    o[j / 2] = pack2<BF16>(j > above ? 0.f : a.x, j + 1 > above ? 0.f : a.y);
+                                    if constexpr (!BF16) largest = max_abs2(largest, o[j / 2]);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                *reinterpret_cast<uint4*>(m + (((j0 / 8 + i) ^ (t & 7)) << 4)) =
+                                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                        if constexpr (!BF16) {
+                            // Scores above the range (C . B is) came out infinite: the warp's are formed again, a
+                            // 16th as large, until none is (C . B < 2^40: 7 times at most); a row with an
+                            // infinite C . B does not count in that.
+                            const bool over = !hopeless && ((largest & 0x7fff) == 0x7c00 || (largest >> 16 & 0x7fff) == 0x7c00);
+                            again = __any_sync(0xffffffffu, over) != 0;
+                            if (again && shift > first_shift - 28) {
+                                shift -= 4;
+                            } else if (again) {
+                                shift = first_shift;
+                                hopeless |= over;
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint4*>(m + (((j0 / 8 + i) ^ (t & 7)) << 4)) =
-                                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } while (again);
+                    if constexpr (!BF16) {
+                        if (half && shift != first_shift) {  // the first half's columns follow
+                            const float f = pow2(shift - first_shift);
+#pragma unroll 1
+                            for (int i = 0; i < 32; ++i) {
+                                uint32_t* at = reinterpret_cast<uint32_t*>(m0) + i;
+                                const float2 v = unpack2<BF16>(*at);
+                                *at = pack2<BF16>(v.x * f, v.y * f);
+                            }
+                        }
+                        if (warp / 2 == half && lane == 0) gd[GT_MSCALE + warp] = gd[GT_DTSCALE] * pow2(-shift);
                     }
                     tc_fence_before_sync();
                     warp_arrive(sy, B_GFREE);
                     fence_async_smem();
-                    warp_arrive(sy, half ? B_M1 : B_M0);
+                    warp_arrive(sy, B_M + 2 * s + half);
                 }
                 if (!ok) break;
                 warp_arrive(sy, B_EMPTY + s);
@@ -857,7 +907,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
         for (int c = 0; ok && c < nch; ++c) {
             const int s = c % STAGES;
             unsigned char* st = sm + s * STAGE_BYTES;
-            const float* gt = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
+            float* gt = reinterpret_cast<float*>(sm + GATE_AT + s * SM_GATE_STAGE);
             if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
             if (!wait_warp(sy, B_XFULL + s, c / STAGES)) break;
             const int nv = un.len - (OUT ? c : nch - 1 - c) * L;
@@ -884,6 +934,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 tc_fence_after_sync();
                 if (live) {
                     const float keep = (OUT ? gt[GT_E + L - 1] : 1.f) * (scale * (1.0f / next_scale));
+                    float round_by = 1.f;  // (FP16) a power of two that brings the warp's largest below 2^15
+                    if constexpr (OUT && !BF16) {
+                        float most = 0.f;
+#pragma unroll 1
+                        for (int n0 = 0; n0 < N; n0 += 32) {
+                            float v[32];
+                            tmem_ld32(tm + lanes + TM_H + n0, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) most = fmaxf(most, fabsf(v[i]));
+                        }
+                        if (!(most < INFINITY)) most = 0.f;  // (of a column with an infinite element the rest does not count)
+#pragma unroll
+                        for (int off = 1; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                        // the power's exponent, and the scale's: both powers and their quotient in FP32's range
+                        const int es = static_cast<int>(__float_as_uint(scale) >> 23) - 127;
+                        int e = static_cast<int>(__float_as_uint(most) >> 23) - 126;
+                        e = max(e, max(-110, -110 - es));
+                        e = min(e, 142 - es);
+                        round_by = pow2(15 - e);
+                        if (lane == 0) gt[GT_HSCALE + wq] = pow2(es + e - 15);
+                    }
 #pragma unroll 1
                     for (int n0 = 32 * xg; n0 < N; n0 += 32 * X_GROUPS) {
                         float v[32];
@@ -892,7 +963,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                             uint32_t o[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                o[i] = BF16 ? pack2<BF16>(v[2 * i], v[2 * i + 1]) : pack2<BF16>(v[2 * i] * scale, v[2 * i + 1] * scale);
+                                o[i] = BF16 ? pack2<BF16>(v[2 * i], v[2 * i + 1])
+                                            : pack2<BF16>(v[2 * i] * round_by, v[2 * i + 1] * round_by);
                             tmem_st_u16(tm + lanes + TM_HB + n0 / 2, o);
                         }
 #pragma unroll
@@ -907,7 +979,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 }
                 scale = next_scale;
                 tc_fence_before_sync();
-                warp_arrive(sy, B_H);
+                warp_arrive(sy, B_H + s);
                 return true;
             };
             // with few slots the state goes first, with many the parts (they then wait for no update)
@@ -1046,14 +1118,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                 const int s = c % STAGES;
                 const uint32_t x = smem_addr(sm) + s * STAGE_BYTES + X_AT + x_frag;
                 const float* gt = reinterpret_cast<const float*>(sm + GATE_AT + s * SM_GATE_STAGE);
-                if (!wait_warp(sy, B_GATE + s, c / STAGES) || !wait_warp(sy, B_XFULL + s, c / STAGES)) break;
+                // (behind it are the state's warps' own waits for the gates and for x)
+                if (!wait_warp(sy, B_H + s, c / STAGES)) break;
                 const int nv = un.len - c * L;
-                const float m_scale = BF16 ? 1.f : gt[GT_DTSCALE];
+                const float h_scale = BF16 ? 1.f : gt[GT_HSCALE + wq];
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                    ok = wait_warp(sy, B_Y1 + (q & 1), 2 * c + (q >> 1));
+                    ok = wait_warp(sy, B_Y1 + (q & 1), 2 * c + (q >> 1)) &&
+                         (BF16 || (q & 1) || wait_warp(sy, B_M + 2 * s + (q >> 1), c / STAGES));
                     if (!ok) break;
                     tc_fence_after_sync();
+                    const float m_scale = BF16 ? 1.f : gt[GT_MSCALE + q];
                     // (a rolled loop: the code of all roles has to fit the instruction caches; a step's
                     // loads come first, so that its arithmetic overlaps their latency; z and y take
                     // turns in the buffer)
@@ -1068,7 +1143,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
                                 load_z();
                             }
                             ldsm4t(x + t0 * 128, xr);
-                            const float2 e2 = *reinterpret_cast<const float2*>(gt + GT_E + t0 + 2 * (lane & 3));
+                            float2 e2 = *reinterpret_cast<const float2*>(gt + GT_E + t0 + 2 * (lane & 3));
+                            if constexpr (!BF16) e2 = fmul2(e2, make_float2(h_scale, h_scale));
                             tmem_ld_frag(tm + lanes + TM_Y1 + (t0 & 63), tm + lanes + TM_Y2 + t0, y1, y2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
