@@ -710,11 +710,12 @@ int gdn_device_status(void* cuda_stream) {
     if (e != cudaSuccess) return cuda_fail(e, "status read (non-allocating entry point)");
     int ssm_word = 0;
     e = gdn::ssm_take_status(dev, &ssm_word);
-    if (e != cudaSuccess) return cuda_fail(e, "status read (selective scan)");
+    if (e != cudaSuccess) return cuda_fail(e, "status read (selective scan and block norm)");
     if (word == 0 && na_word == 0 && ssm_word == 0) return GDN_OK;
     std::string msg = "a kernel gave up a bounded wait (status word " + std::to_string(word | na_word | ssm_word) + ")";
     if (na_word != 0) msg += " in gdn_recurrence_chunked_noalloc";
-    if (ssm_word != 0) msg += " in gdn_ssm_scan";
+    if (ssm_word & gdn::kDevErrBlockNorm) msg += " in gdn_block_norm";
+    if (ssm_word & ~gdn::kDevErrBlockNorm) msg += " in gdn_ssm_scan";
     if (ssm_word & gdn::kDevErrLayout) msg += " (its shared memory does not start where it has to)";
     if (word & gdn::kDevErrNormTimeout) msg += " (the fused sequential norm's exchange between CTAs)";
     if (word & gdn::kDevErrRingTimeout) msg += " (a chunk prep's wait for a free slot of the tile ring)";

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) block_norm_rows_kernel(const B
         bool ok = false;
         for (uint32_t n = 0; n < kWaitPolls && !ok; ++n) ok = mbar_try_wait(&full[s], phase);
         if (!ok) {  // (threads that leave count as arrived at the barriers below)
-            report_timeout(p.status);
+            report_error(p.status, kDevErrBlockNorm);
             if (tid == 0)  // the copies in flight land before the CTA's shared memory is another's
                 for (int i = 0; i < stages && t + i * static_cast<int64_t>(gridDim.x) < p.T; ++i) {
                     const bool wrapped = s + i >= stages;

@@ -15,6 +15,7 @@ constexpr int kDevErrFlagTimeout = 2;  // a wait for another CTA's flag gave up 
 constexpr int kDevErrNormTimeout = 4;  // a wait for another CTA's sums of squares gave up (fused sequential norm)
 constexpr int kDevErrRingTimeout = 8;  // a chunk prep's wait for a free slot of the tile ring gave up
 constexpr int kDevErrLayout = 16;      // shared memory did not start where the kernel needs it
+constexpr int kDevErrBlockNorm = 32;   // the block norm's wait for a row's copies gave up
 
 // A wait gives up after this many unsuccessful mbarrier.try_wait polls (each
 // poll may itself suspend the thread for a hardware-chosen interval).  Legit
