@@ -328,17 +328,18 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
  *
  * Two forms.  Token after token, the state in registers: any call; a sequence split
  * over calls gives the same bits.  Chunks of 128 tokens on the tensor cores: GDN_BF16
- * and GDN_F16 with head_dim and state_dim 64 or 128, at least 32 tokens per sequence
- * on average, and x, B, C, z and y in rows of 16-byte pieces on 16-byte boundaries.
+ * and GDN_F16 with head_dim and state_dim 64 or 128, T >= 32 n_seq, and x, B, C, z and
+ * y in rows of 16-byte pieces on 16-byte boundaries; so a sequence's form, and with it its
+ * rounding, can depend on the others of the call.
  * There the decayed scores and the state (for its product with C) are rounded once to
  * `dtype`, while the state itself keeps FP32's precision.  FP16's short range is held
  * off by powers of two, so what is left of it are its smallest steps: a chunk's part of
  * a state is off by up to 2^-24 max(w, 2^-60) sum |B|, w its steps times the decay
  * behind them; a score by 2^-24 max(dt, 2^-60), the chunk's largest dt, or 2^-37 of the
  * largest score of 32 neighbouring tokens if that is more; the state in its product with
- * C by 2^-40 of the largest of 32 neighbouring columns.  A NaN or infinity in x
- * reaches, besides its own and later tokens, the outputs of the up to 127 tokens of
- * the same sequence before it that share its chunk.
+ * C by 2^-39 of the largest of 32 neighbouring columns.  A NaN or infinity in x
+ * reaches, besides its own and later tokens of its column, the outputs of the up to 31
+ * tokens before it that are of the same 32 tokens of its chunk.
  */
 int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const void* B, int64_t b_stride,
                  const void* C, int64_t c_stride, const void* z, int64_t z_stride, const float* A_log,
@@ -377,7 +378,9 @@ int gdn_ssm_step(const void* xbc, int64_t xbc_stride, const void* a, int64_t a_s
  *   b, gate, y [T][dim] of `dtype` (gate_stride 0: one row for every token); residual,
  *   residual_out [T][dim] of `residual_dtype`, GDN_F32 or `dtype`; w_post, w_pre [dim]
  *   FP32.  residual_out may be residual itself.
- * Computed in FP32; y comes from residual_out before its rounding.  dim <= 16384.
+ * Computed in FP32; y comes from residual_out before its rounding.  dim <= 16384.  The
+ * order of a row's sums goes by the rows' alignment, dim and T: the same token can get
+ * other last bits in a call of another T.
  */
 int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_t residual_stride, const void* gate,
                    int64_t gate_stride, int gate_sigmoid, const float* w_post, const float* w_pre, float scale,

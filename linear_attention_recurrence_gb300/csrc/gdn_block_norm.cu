@@ -6,7 +6,9 @@
 // Bound by HBM: b, r and a per-token gate are read once, r' and y written once.  A CTA
 // takes a token at a time and keeps its row in registers in FP32 across the two sums,
 // which meet in a shuffle butterfly and one exchange between warps, in a fixed order.  y
-// is formed from r' before r' is rounded to the stream's type.  Two forms, same bits:
+// is formed from r' before r' is rounded to the stream's type.  The sums' order goes by the
+// widest access that the rows allow and by the number of threads, which for rows of 513
+// to 1024 accesses goes by T <= SMs: another T can give a token other last bits.  Two forms:
 // one CTA per token reading its row itself (short rows, rows off 16-byte boundaries, rows
 // longer than the other form holds), and CTAs that stay, the weights in registers, while
 // bulk copies bring their next rows into shared memory (the two sums of a row leave memory
@@ -274,7 +276,7 @@ cudaError_t launch_r(const BlockNormParams& p, int sm_count, cudaStream_t s) {
     // in registers) and 1024 elements.  One CTA per token / this form, us, BF16, FP32 stream
     // and a gate per token: 512 elements: 1 token 2.3 / 2.7, 8192 32 / 32; 1024: 2.5 / 2.7,
     // 40 / 34; 2048: 2.8 / 2.8, 58 / 46; 6144: 5.0 / 4.7, 171 / 118.
-    if (p.rows16 && p.dim >= 1024 && nv <= 3) {
+    if (p.vec == 8 && p.dim >= 1024 && nv <= 3) {
         if (nv == 1) return launch_rows<T, R, 1>(p, sm_count, s);
         if (nv == 2) return launch_rows<T, R, 2>(p, sm_count, s);
         return launch_rows<T, R, 3>(p, sm_count, s);

@@ -87,7 +87,6 @@ struct BlockNormParams {
     int dim, gate_sigmoid, dtype, stream_dtype;
     int vec;      // elements that every row's start is a multiple of (8, 4, 2 or 1)
     int* status;
-    bool rows16;  // rows start on 16-byte boundaries and are whole 16-byte pieces (and 8 elements)
 };
 cudaError_t launch_block_norm(const BlockNormParams& p, int sm_count, cudaStream_t s);
 

@@ -292,7 +292,7 @@ int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_
         vec /= 2;
     BlockNormParams p{b, residual, gate, residual_out, y, b_stride, residual_stride, gate_stride,
                             residual_out_stride, y_stride, w_post, w_pre, scale, eps, T, dim, gate_sigmoid, dtype,
-                            residual_dtype, vec, nullptr, vec == 8};
+                            residual_dtype, vec, nullptr};
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
     if (cudaError_t err = ssm_status_word(&p.status); err != cudaSuccess) return cuda_bad(err, "block norm set-up");

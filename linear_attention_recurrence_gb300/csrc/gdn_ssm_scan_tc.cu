@@ -237,11 +237,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     if constexpr (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
-template <bool BF16>
-__device__ __forceinline__ float unpack1(uint16_t v) {
-    if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    return __half2float(__ushort_as_half(v));
-}
 
 // The larger magnitudes of two pairs of FP16, with some sign (a NaN counts as none).
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
@@ -910,8 +905,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) ssm_scan_tc_kernel(const __grid
             float* gt = reinterpret_cast<float*>(sm + GATE_AT + s * SM_GATE_STAGE);
             if (!wait_warp(sy, B_GATE + s, c / STAGES)) break;
             if (!wait_warp(sy, B_XFULL + s, c / STAGES)) break;
-            const int nv = un.len - (OUT ? c : nch - 1 - c) * L;
-            if (nv < L) {
+            // (PASS 1 has whole chunks alone: a sequence's last segment is not its)
+            const int nv = OUT ? un.len - c * L : L;
+            if (OUT && nv < L) {
                 if (!wait_warp(sy, B_FULL + s, c / STAGES)) break;
                 // rows behind the segment's end (another sequence's, which may hold anything) become
                 // zeros in x and B, the operands whose rows are summed over
