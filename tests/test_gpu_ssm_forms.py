@@ -1,0 +1,80 @@
+"""The scan's token form with 16-bit rows, held to its own bound.
+
+Which form runs goes by sizes: the tensor form takes BF16 and FP16 with head_dim and state_dim
+64 or 128, T >= 32 n_seq, and rows of 16-byte pieces.  The calls here are
+outside of that, so nothing but y is rounded to the type: the bound is the token form's,
+(4 tokens + 2 state_dim + 32) 2^-24 + 2^-21 of the magnitude, for y and the states."""
+import pytest
+import torch
+
+import ssm_reference as ref
+from linear_attention_recurrence_gb300 import gdn
+from test_gpu_ssm import BF16, F16, F32, check, layer, packed, rnd, scan_bound
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from linear_attention_recurrence_gb300 import build
+
+    build.build()
+
+
+CASES = [
+    # lens, H, G, P, N, wide (columns before x), strong
+    ((70, 70), 2, 2, 96, 32, 0, False),      # sizes
+    ((200,), 2, 1, 256, 64, 3, True),
+    ((150,), 3, 1, 32, 16, 0, False),
+    ((90, 1, 60), 4, 2, 128, 32, 5, True),
+    ((1,), 3, 1, 128, 128, 0, False),        # tokens per sequence
+    ((28,), 4, 2, 64, 64, 0, True),
+    ((40, 1, 3, 50), 2, 1, 128, 128, 0, False),
+    ((300,), 2, 1, 128, 128, 4, False),      # rows off 16-byte boundaries
+    ((127, 129), 4, 2, 64, 128, 1, True),
+    ((640,), 3, 3, 64, 64, 2, False),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens,H,G,P,N,wide,strong", CASES)
+def test_token_form_keeps_its_bound(lens, H, G, P, N, wide, strong, dtype):
+    gen = torch.Generator().manual_seed(sum(lens) + P + N + 1)
+    n = len(lens)
+    cu, end = packed(lens, lead=1)
+    T = end + 2
+    assert P not in (64, 128) or N not in (64, 128) or T < 32 * n or wide % 8
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, G, P, N, dtype, wide, strong)
+    z, D = rnd(gen, T, H, P, dtype=dtype), rnd(gen, H)
+    states, out = rnd(gen, n + 2, H, N, P, scale=0.3), rnd(gen, T, H, P, dtype=dtype)
+    slots = torch.randperm(n + 2, generator=gen)[:n].to(torch.int32)
+    has = torch.tensor([i % 3 != 1 for i in range(n)])
+    y, st, mag, smag = ref.scan(x, a, B, C, A_log, dt_bias, states, D, z, cu, slots, has, out)
+    gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states, D=D, z=z, cu_seqlens=cu, slots=slots.cuda(),
+                     has_state=has.cuda(), out=out)
+    torch.cuda.synchronize()
+    check(out, y, mag, scan_bound(F32, P, N, max(lens)), "y")
+    check(states, st, smag, scan_bound(F32, P, N, max(lens)), "states")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,H", [(300, 40), (900, 4)])
+def test_nan_in_x_stays_in_its_column_and_32_tokens(dtype, T, H):
+    """The tensor form: a NaN in x reaches its column's later outputs and those of the same 32 tokens
+    of its chunk, the column's state, and nothing else."""
+    gen = torch.Generator().manual_seed(61)
+    P, N, at, h, col = 128, 64, 170, 1, 9
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, 2, P, N, dtype)
+    states = rnd(gen, 1, H, N, P)
+    want_st = states.clone()
+    want = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, want_st)
+    x[at, h, col] = float("nan")
+    y = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states)
+    torch.cuda.synchronize()
+    first = at // 32 * 32
+    assert torch.equal(y[:first], want[:first])
+    assert bool(y[at:, h, col].isnan().all()) and bool(states[0, h, :, col].isnan().all())
+    keep = torch.ones(H, P, dtype=torch.bool).cuda()
+    keep[h, col] = False
+    assert torch.equal(y[:, keep], want[:, keep])
+    assert torch.equal(states[0].transpose(1, 2)[keep], want_st[0].transpose(1, 2)[keep])
