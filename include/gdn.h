@@ -330,7 +330,7 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
  * over calls gives the same bits.  Chunks of 128 tokens on the tensor cores: GDN_BF16
  * and GDN_F16 with head_dim and state_dim 64 or 128, T >= 32 n_seq, and x, B, C, z and
  * y in rows of 16-byte pieces on 16-byte boundaries; so a sequence's form, and with it its
- * rounding, can depend on the others of the call.
+ * rounding, can depend on the others of the call (GDN_OPT_SSM_SCAN_FORM keeps to the first).
  * There the decayed scores and the state (for its product with C) are rounded once to
  * `dtype`, while the state itself keeps FP32's precision.  FP16's short range is held
  * off by powers of two, so what is left of it are its smallest steps: a chunk's part of
@@ -423,6 +423,12 @@ typedef enum gdn_option {
      * default: 4 n_kh; else this many), capped by the SMs the scan leaves and at
      * least n_kh.  Same bits either way. */
     GDN_OPT_CHUNK_PREP_CTAS = 5,
+    /* gdn_ssm_scan: 0 (default) takes the tensor form where its sizes and alignment
+     * allow, 1 the token form for every call: nothing but y is rounded to the
+     * activations' type, the result does not go by the other sequences of the call,
+     * and a sequence split over calls gives the same bits (on GB300 at several times
+     * the tensor form's time).  gdn_ssm_scan_workspace_bytes() goes by it too. */
+    GDN_OPT_SSM_SCAN_FORM = 6,
     /* Failure-path test hook: the prep task (chunk * n_kh + key head, in every
      * super-block) whose hand-off flag the one-launch chunked kernel never
      * publishes, so the scan CTAs waiting for it give up their bounded wait and

@@ -41,7 +41,7 @@ DeviceState g_dev[kMaxDevices];
 // when it starts.  Nothing is read from the environment.
 constexpr int kOptSlots = 8;
 // constant-initialised defaults, in slot order (see opt_slot)
-std::atomic<int> g_opt[kOptSlots] = {GDN_PRODUCTS_TMEM, 1, 0, 16, -1, 0, 0, 0};  // slot 6: prep CTAs (0: auto)
+std::atomic<int> g_opt[kOptSlots] = {GDN_PRODUCTS_TMEM, 1, 0, 16, -1, 0, 0, 0};  // slots 6: prep CTAs (0: auto), 7: the scan's form
 int opt_slot(int option) {
     switch (option) {
         case GDN_OPT_CHUNK_PRODUCTS: return 0;
@@ -49,6 +49,7 @@ int opt_slot(int option) {
         case GDN_OPT_NORM_IN_LAUNCH: return 2;
         case GDN_OPT_SEQ_ROWS_PER_THREAD: return 3;
         case GDN_OPT_CHUNK_PREP_CTAS: return 6;
+        case GDN_OPT_SSM_SCAN_FORM: return 7;
         case GDN_OPT_TEST_WITHHOLD_PREP_TASK: return 4;
         case GDN_OPT_TEST_FAIL_SCRATCH_ALLOC: return 5;
         default: return -1;
@@ -292,6 +293,7 @@ ScanKind chunk_scan_kind() {
     }
 }
 void internal_count_launch() { g_launches.fetch_add(1); }
+int internal_option(int option) { return opt(option); }
 }  // namespace gdn
 
 namespace {
@@ -778,6 +780,7 @@ int gdn_set_option(int option, int value) {
             break;
         case GDN_OPT_CHUNK_ONE_LAUNCH:
         case GDN_OPT_NORM_IN_LAUNCH:
+        case GDN_OPT_SSM_SCAN_FORM:
         case GDN_OPT_TEST_FAIL_SCRATCH_ALLOC: ok = value == 0 || value == 1; break;
         case GDN_OPT_SEQ_ROWS_PER_THREAD: ok = value == 8 || value == 16; break;
         case GDN_OPT_CHUNK_PREP_CTAS: ok = value >= 0 && value <= 4096; break;

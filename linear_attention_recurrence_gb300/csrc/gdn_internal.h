@@ -252,5 +252,7 @@ cudaError_t set_smem_once(const void* kernel, int bytes);
 int internal_fail(int code, const std::string& msg);
 // Adds one kernel launch to gdn_launch_count().
 void internal_count_launch();
+// The current value of a known option.
+int internal_option(int option);
 
 }  // namespace gdn

@@ -88,6 +88,11 @@ int check_heads(int n_heads, int n_groups, int head_dim, int state_dim) {
     if (n_heads > 65535) return unsupported("n_heads > 65535");
     return GDN_OK;
 }
+
+bool tensor_form(int head_dim, int state_dim, int dtype, int64_t T, int n_seq) {
+    return gdn::internal_option(GDN_OPT_SSM_SCAN_FORM) == 0 &&
+           gdn::ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq);
+}
 }  // namespace
 
 extern "C" {
@@ -134,7 +139,7 @@ int gdn_ssm_conv(const void* x, int64_t x_stride, const float* w, const float* b
 size_t gdn_ssm_scan_workspace_bytes(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int dtype) {
     int sms = 0;
     if (T <= 0 || n_seq <= 0 || n_heads <= 0 || head_dim <= 0 || state_dim <= 0 ||
-        !gdn::ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) || sm_count(&sms) != GDN_OK)
+        !tensor_form(head_dim, state_dim, dtype, T, n_seq) || sm_count(&sms) != GDN_OK)
         return 0;
     return gdn::ssm_scan_tc_workspace(T, n_seq, n_heads, head_dim, state_dim, sms);
 }
@@ -184,7 +189,7 @@ int gdn_ssm_scan(const void* x, int64_t x_stride, const void* a, int64_t a_strid
         return is_aligned(ptr, 16) && stride % 8 == 0 && stride >= width;
     };
     cudaError_t err;
-    if (ssm_scan_tc_sizes(head_dim, state_dim, dtype, T, n_seq) && (T / 512 + n_seq) * n_heads <= INT32_MAX &&
+    if (tensor_form(head_dim, state_dim, dtype, T, n_seq) && (T / 512 + n_seq) * n_heads <= INT32_MAX &&
         tma_rows(x, x_stride, xw) &&
         tma_rows(B, b_stride, bw) && tma_rows(C, c_stride, bw) &&
         (!z || tma_rows(z, z_stride, xw)) && tma_rows(y, y_stride, xw)) {

@@ -35,6 +35,7 @@ GDN_OPT_CHUNK_ONE_LAUNCH = 2
 GDN_OPT_NORM_IN_LAUNCH = 3
 GDN_OPT_SEQ_ROWS_PER_THREAD = 4
 GDN_OPT_CHUNK_PREP_CTAS = 5
+GDN_OPT_SSM_SCAN_FORM = 6
 GDN_OPT_TEST_WITHHOLD_PREP_TASK = 101
 GDN_OPT_TEST_FAIL_SCRATCH_ALLOC = 102
 # activation types (gdn_ssm_*, gdn_block_norm)
@@ -48,7 +49,7 @@ GDN_PRODUCTS_TCGEN05 = 2
 GDN_PRODUCTS_TMEM = 3
 _OPTIONS = {"chunk_products": GDN_OPT_CHUNK_PRODUCTS, "chunk_one_launch": GDN_OPT_CHUNK_ONE_LAUNCH,
             "norm_in_launch": GDN_OPT_NORM_IN_LAUNCH, "seq_rows_per_thread": GDN_OPT_SEQ_ROWS_PER_THREAD,
-            "chunk_prep_ctas": GDN_OPT_CHUNK_PREP_CTAS,
+            "chunk_prep_ctas": GDN_OPT_CHUNK_PREP_CTAS, "ssm_scan_form": GDN_OPT_SSM_SCAN_FORM,
             "test_withhold_prep_task": GDN_OPT_TEST_WITHHOLD_PREP_TASK,
             "test_fail_scratch_alloc": GDN_OPT_TEST_FAIL_SCRATCH_ALLOC}
 _PRODUCTS = {"mma": GDN_PRODUCTS_MMA, "fma": GDN_PRODUCTS_FMA, "tc": GDN_PRODUCTS_TCGEN05,
@@ -484,7 +485,8 @@ def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seq
     [slots][n_heads][state_dim][head_dim] FP32, or None (sequences start from zeros,
     nothing is kept).  Head h reads group h % n_groups.  cu_seqlens, slots, has_state
     as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.  16-bit prompts run on the
-    tensor cores where their sizes and alignment allow (see gdn.h).
+    tensor cores where their sizes and alignment allow (see gdn.h; with the option
+    "ssm_scan_form" at 1 every call takes the form that rounds nothing but ``out``).
     """
     dt, dev = _activations(x, "x", 3)
     if B.dim() != 3:

@@ -78,3 +78,35 @@ def test_nan_in_x_stays_in_its_column_and_32_tokens(dtype, T, H):
     keep[h, col] = False
     assert torch.equal(y[:, keep], want[:, keep])
     assert torch.equal(states[0].transpose(1, 2)[keep], want_st[0].transpose(1, 2)[keep])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_token_form_on_request(dtype):
+    """The option takes every call to the token form: its bound where the tensor form would run, the
+    same bits for a sequence alone, split over calls and beside others, and no workspace."""
+    gen = torch.Generator().manual_seed(62)
+    T, H, P, N = 420, 4, 128, 128
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, 2, P, N, dtype)
+    start = rnd(gen, 1, H, N, P, scale=0.3)
+    y, st, mag, smag = ref.scan(x, a, B, C, A_log, dt_bias, start, None, None, None, None, None, torch.zeros(T, H, P))
+    tensor = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, start.clone())
+    with gdn.options(ssm_scan_form=1):
+        assert gdn.load_library().gdn_ssm_scan_workspace_bytes(T, 1, H, P, N, gdn.GDN_BF16) == 0
+        s1, s2 = start.clone(), start.clone()
+        whole = gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, s1)
+        parts, at = [], 0
+        for n in (100, 3, 200, 117):
+            r = slice(at, at + n)
+            parts.append(gdn.gdn_ssm_scan(x[r], a[r], B[r], C[r], A_log, dt_bias, s2))
+            at += n
+        cu, _ = packed((T, 1))
+        more = [torch.cat([v, v[:1]]) for v in (x, a, B, C)]
+        s3 = torch.cat([start, start])
+        beside = gdn.gdn_ssm_scan(*more, A_log, dt_bias, s3, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    check(whole, y, mag, scan_bound(F32, P, N, T), "y")
+    check(s1, st, smag, scan_bound(F32, P, N, T), "states")
+    assert at == T and torch.equal(whole, torch.cat(parts)) and torch.equal(s1, s2)
+    assert torch.equal(whole, beside[:T]) and torch.equal(s1[0], s3[0])
+    assert not torch.equal(whole, tensor)  # (the default is the other form here)
+    assert torch.equal(gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, start.clone()), tensor)
