@@ -268,6 +268,13 @@ int gdn_recurrence_chunked_noalloc(const float* q, const float* k, const float* 
  * of B and C, the state is S[state_dim][head_dim] per head (B's dim the row), the
  * gates come from a, A_log and dt_bias as in gdn_prestage.
  *
+ * A layer whose neighbouring heads share a group (its head i reads group i / r of r =
+ * n_heads / n_groups heads each) runs with its heads reordered: head h here is its head
+ * i = (h % n_groups) r + h / n_groups.  With one group, or as many as heads, the two
+ * orders are the same.  Reordered once, with the weights: A_log, dt_bias, D, the rows of
+ * the projections that give a, z and x and of the convolution of x, and the columns of
+ * the projection that reads y.
+ *
  * Packed sequences: the rows of n_seq sequences follow one another; sequence s has
  * rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of the T rows (cu_seqlens [n_seq + 1],
  * on the device, not decreasing; NULL: one sequence of all T rows).  Rows before

@@ -396,6 +396,14 @@ def _activations(t, name, dims):
     return dt, t.get_device()
 
 
+def _dims(t, name, dims):
+    """Checks a tensor whose sizes a call goes by, before they are looked at."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+
+
 def _empty(shape, dtype, index, stream):
     """Memory that belongs to the stream a call runs on (None: the current one)."""
     device = torch.device("cuda", index)
@@ -428,11 +436,16 @@ def _launch(fn, index, stream, *args):
 def _seqs(cu_seqlens, slots, has_state, pool, index):
     """(cu, slots, has_state, n_seq, n_slots) of a packed call; pool: its states or history, or None."""
     i32 = torch.int32
-    n = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    if n < 0:
-        raise ValueError("cu_seqlens needs one element at least")
-    if has_state is not None and has_state.dtype is torch.bool:
-        has_state = has_state.view(torch.uint8)
+    n = 1
+    if cu_seqlens is not None:
+        _dims(cu_seqlens, "cu_seqlens", 1)
+        n = cu_seqlens.shape[0] - 1
+        if n < 0:
+            raise ValueError("cu_seqlens needs one element at least")
+    if has_state is not None:
+        _dims(has_state, "has_state", 1)
+        if has_state.dtype is torch.bool:
+            has_state = has_state.view(torch.uint8)
     n_slots = 0 if pool is None else pool.shape[0]
     if pool is not None and slots is None and n_slots < n:
         raise ValueError(f"{n} sequences but {n_slots} slots")
@@ -456,13 +469,12 @@ def gdn_ssm_conv(x, w, bias=None, hist=None, cu_seqlens=None, slots=None, has_st
     dt, dev = _activations(x, "x", 2)
     T, ch = x.shape
     xp, xs = _rows(x, "x", (T, ch), x.dtype, dev)
-    if w.dim() != 2:
-        raise ValueError("w must have 2 dimensions")
+    _dims(w, "w", 2)
     width = w.shape[1]
     wp = _dense(w, "w", (ch, width), torch.float32, dev)
     bp = _dense(bias, "bias", (ch,), torch.float32, dev)
-    if hist is not None and hist.dim() != 3:
-        raise ValueError("hist must have 3 dimensions")
+    if hist is not None:
+        _dims(hist, "hist", 3)
     hp = None if hist is None else _dense(hist, "hist", (hist.shape[0], width - 1, ch), x.dtype, dev)
     cu, sl, has, n, n_slots = _seqs(cu_seqlens, slots, has_state, hist, dev)
     if out is None:
@@ -483,14 +495,16 @@ def gdn_ssm_scan(x, a, B, C, A_log, dt_bias, states=None, D=None, z=None, cu_seq
     x, or None: all of one type (FP32, BF16 or FP16), the rows any distance apart.
     A_log, dt_bias, D (or None): [n_heads] FP32; states:
     [slots][n_heads][state_dim][head_dim] FP32, or None (sequences start from zeros,
-    nothing is kept).  Head h reads group h % n_groups.  cu_seqlens, slots, has_state
+    nothing is kept).  Head h reads group h % n_groups (gdn.h says how the heads of a
+    layer with another order are laid out).  cu_seqlens, slots, has_state
     as in gdn_ssm_conv.  ``out`` (as x) is allocated if None.  16-bit prompts run on the
     tensor cores where their sizes and alignment allow (see gdn.h; with the option
     "ssm_scan_form" at 1 every call takes the form that rounds nothing but ``out``).
     """
     dt, dev = _activations(x, "x", 3)
-    if B.dim() != 3:
-        raise ValueError("B must have 3 dimensions")
+    _dims(B, "B", 3)
+    if states is not None:
+        _dims(states, "states", 4)
     ty, f32 = x.dtype, torch.float32
     T, H, P = shape = x.shape
     G, N = B.shape[1], B.shape[2]
@@ -535,8 +549,9 @@ def gdn_ssm_step(xbc, a, conv_w, A_log, dt_bias, hist, states, conv_bias=None, D
     ([batch][n_heads][head_dim]) is allocated if None.
     """
     dt, dev = _activations(xbc, "xbc", 2)
-    if states.dim() != 4 or conv_w.dim() != 2 or hist.dim() != 3:
-        raise ValueError("states must have 4 dimensions, hist 3 and conv_w 2")
+    _dims(states, "states", 4)
+    _dims(conv_w, "conv_w", 2)
+    _dims(hist, "hist", 3)
     ty, f32 = xbc.dtype, torch.float32
     n, cw = xbc.shape
     n_slots, H, N, P = states.shape
@@ -585,7 +600,8 @@ def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: boo
     gp = None
     gs = 0
     if gate is not None:
-        one = gate.dim() == 2 and gate.shape[0] == 1
+        _dims(gate, "gate", 2)
+        one = gate.shape[0] == 1
         gp, gs = _rows(gate, "gate", (1, d) if one else shape, ty, dev)
         gs = 0 if one else gs
     wpre = _dense(w_pre, "w_pre", (d,), f32, dev)

@@ -110,3 +110,24 @@ def test_token_form_on_request(dtype):
     assert torch.equal(whole, beside[:T]) and torch.equal(s1[0], s3[0])
     assert not torch.equal(whole, tensor)  # (the default is the other form here)
     assert torch.equal(gdn.gdn_ssm_scan(x, a, B, C, A_log, dt_bias, start.clone()), tensor)
+
+
+@pytest.mark.parametrize("dtype,T", [(F32, 40), (BF16, 200)])
+def test_heads_of_a_layer_whose_neighbours_share_a_group(dtype, T):
+    """Heads reordered as gdn.h says give that layer's results: its head i reads group i / r."""
+    gen = torch.Generator().manual_seed(63)
+    H, G, P, N = 6, 2, 64, 64
+    r = H // G
+    x, a, B, C, A_log, dt_bias = layer(gen, T, H, G, P, N, dtype)
+    D, z, states = rnd(gen, H), rnd(gen, T, H, P, dtype=dtype), rnd(gen, 1, H, N, P, scale=0.3)
+    order = torch.tensor([(h % G) * r + h // G for h in range(H)]).cuda()
+    st = states[:, order].contiguous()
+    got = gdn.gdn_ssm_scan(x[:, order], a[:, order], B, C, A_log[order], dt_bias[order], st, D=D[order], z=z[:, order])
+    torch.cuda.synchronize()
+    for i in range(H):  # the layer's own order: a head and its group, alone
+        g, h = i // r, int((order == i).nonzero())
+        one = [v[:, i:i + 1] for v in (x, a)] + [v[:, g:g + 1] for v in (B, C)] + [A_log[i:i + 1], dt_bias[i:i + 1]]
+        y, s, mag, smag = ref.scan(*one, states[:, i:i + 1], D[i:i + 1], z[:, i:i + 1], None, None, None,
+                                   torch.zeros(T, 1, P))
+        check(got[:, h:h + 1], y, mag, scan_bound(dtype, P, N, T), f"y {i}")
+        check(st[:, h:h + 1], s, smag, scan_bound(F32, P, N, T), f"states {i}")
