@@ -50,9 +50,12 @@ cudaError_t launch_ssm_scan_tokens(const SsmScanParams& p, cudaStream_t s);
 
 // Chunks of 128 tokens on the tensor cores (gdn_ssm_scan_tc.cu): 16-bit types, head_dim
 // and state_dim 64 or 128, rows of x, B and C on 16-byte boundaries.
-// Tokens per sequence from which it is taken: 48 heads of 128 x 128, BF16, tensor / token
-// form, us: 1 sequence of 16 tokens 14 / 11, 32 15 / 14, 64 15 / 21, 128 15 / 34; 4 of 32
-// 24 / 28; 32 of 16 116 / 101, of 32 138 / 162, of 128 152 / 549.
+// Tokens per sequence from which it is taken, tensor / token form, BF16, us.  48 heads of
+// 128 x 128: 1 sequence of 16 tokens 14 / 9, 32 15 / 15, 64 15 / 21, 128 15 / 33; 4 of 32
+// 24 / 28; 32 of 16 114 / 100, of 32 120 / 161, of 128 136 / 547 (FP16 within 4 us of it).
+// Heads of 64 meet between 32 and 64 tokens: 64 heads of 64 x 128, 1 sequence of 32 15 / 11, 64
+// 14 / 15; 4 of 32 23 / 21; 32 of 32 134 / 105, of 64 138 / 197; 24 of 64 x 64, 32 of 32 58 / 34,
+// of 64 60 / 56.
 constexpr int kSsmTcMinTokens = 32;
 bool ssm_scan_tc_sizes(int head_dim, int state_dim, int dtype, int64_t T, int n_seq);
 size_t ssm_scan_tc_workspace(int64_t T, int n_seq, int n_heads, int head_dim, int state_dim, int sm_count);

@@ -39,16 +39,19 @@
 // time although a lane's row is a column of x.
 //
 // What bounds it: the instructions of the roles around the products, and their latency, of
-// the output's above all (5100 per scheduler and chunk, at a little over one in two cycles;
+// the output's above all (5200 per scheduler and chunk, at a little under one in two cycles;
 // the tensor pipe is busy a quarter of the time); memory next.  48 heads of 128 x 128, BF16,
-// z: 32768 tokens of one sequence 491 us (the first launch 115 us, 1.3 us a chunk; the second
-// 372 us, 4.3 us a chunk; 1.48 GB: 3.0 TB/s).  Steps on the way, 32768 tokens: z by 2-byte
+// z: 32768 tokens of one sequence 496 us (the first launch 117 us, 1.4 us a chunk; the second
+// 378 us, 4.4 us a chunk; 1.48 GB: 3.0 TB/s).  FP16 takes 535 us: the largest element of the
+// state and the test of the scores, and what multiplies their powers back.  64 heads of
+// 64 x 128, 8192 tokens: 208 us.  Steps on the way, BF16, 32768 tokens: z by 2-byte
 // loads in the output 1052 us; fragments 883; eight output warps and z a half chunk ahead
 // 792; the MMA chains apart and elected issuing lanes 691; code that fits the instruction
 // caches (81 -> 55 KB: rolled loops, waits out of line) 670; x freed apart from B and C 652;
 // twelve output warps 629; packed gates 619; the output in quarters of a chunk with two
 // product buffers 550; descriptors stepped between MMAs 527; the first launch from the end
-// 500; z and y addresses stepped 495; a quarter of Y1 ahead of G 491.
+// 500; z and y addresses stepped 495; a quarter of Y1 ahead of G 491; exponents from groups of 4
+// tokens 500; barriers by stage, one wait of the output for the state, x and the gates 496.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -1220,7 +1223,7 @@ cudaError_t launch_pn(const TcParams& p, int64_t units, cudaStream_t s) {
     e = set_smem_once(reinterpret_cast<const void*>(ssm_scan_tc_kernel<BF16, P, N, 0>), bytes);
     if (e != cudaSuccess) return e;
     // Behind a first launch the second starts on the SMs as they fall free, and waits where it
-    // first needs what that one leaves (2048 tokens, 48 heads: 61 us, 65 without).
+    // first needs what that one leaves (2048 tokens, 48 heads: 60 us, 4 more without).
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreadsTc);
@@ -1248,14 +1251,17 @@ std::atomic<int*> g_status_word[64];  // its address on the devices it was asked
 // Segments: with H heads, SMs / H segments of all tokens together fill the device; a
 // segment is that share of the call's chunks, but at least a 16th of them (a segment sums
 // the contributions of those before it).  One sequence, BF16, 128 x 128, us at segments of
-// the share and at others: 48 heads, 1024 tokens (3 chunks) 40 (2 chunks 50, 4 44, uncut 48),
-// 2048 (6) 59 (3 chunks 67, uncut 81); 16 heads, 1024 (1) 32 (2 chunks 34, 4 42, uncut 46);
-// 8 heads, 4096 (2) 41 (4 chunks 46, uncut 145).  The first launch costs what 3 chunks do:
-// sequences stay whole where segments save fewer (48 heads, 512 tokens: of 2 chunks 34,
-// uncut 32; 16 heads, 384: of 1 chunk 28, uncut 26; 512: of 1 chunk 28, uncut 30).
+// the share and at others: 48 heads, 1024 tokens (3 chunks) 42 (2 chunks 53, 4 46, uncut 48),
+// 2048 (6) 60 (3 chunks 69, uncut 83); 16 heads, 1024 (1) 34 (2 chunks 36, 4 44, uncut 46);
+// 8 heads, 4096 (2) 45 (4 chunks 48, uncut 147).  The first launch costs what 3 chunks do:
+// sequences stay whole where segments save fewer (48 heads, 512 tokens: of 2 chunks 36,
+// uncut 32; 16 heads, 384: of 1 chunk 30, uncut 26; 512: of 1 chunk 30, uncut 30).
 // Several sequences are mostly whole segments, for which that launch is in vain, so theirs
-// are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of 4 chunks 67, uncut
-// 61; 8 of 128: of 2 chunks 50, uncut 42).
+// are 4 chunks at least (48 heads, 4 sequences of 512 tokens: segments of 4 chunks 70, uncut
+// 60; 8 of 128: of 2 chunks 52, uncut 42).  Heads of 64 x 128: 64 heads, 2048 tokens (8) 71
+// (4 chunks 78, uncut 85), 8192 (32) 208 (16 chunks 214, uncut 302); 80 heads, which are not
+// cut (one segment fills more than half of the SMs), 2048 tokens 85 (8 chunks 108), 8192 303
+// (16 chunks 295, 32 354); 128 heads, 8192 305 (32 chunks 368).
 int64_t ssm_scan_segment(int64_t T, int n_seq, int n_heads, int sm_count) {
     const int64_t chunks = (T + L - 1) / L, least = n_seq > 1 ? 4 : 1;
     int64_t parts = sm_count / n_heads;
