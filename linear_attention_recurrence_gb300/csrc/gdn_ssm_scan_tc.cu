@@ -11,7 +11,8 @@
 // tensor memory as the FP32 accumulator of its update.  Every product is a tcgen05.mma
 // of the rows' own type: H is rounded to it for the product with C (as M is: together
 // one rounding of disjoint terms of y), but the update takes w o x in parts of that type
-// (three of 8 bits for BF16, two of 11 for FP16), so the state keeps FP32's precision.
+// (three of 8 bits for BF16, two of 11 for FP16), so the state keeps FP32's precision
+// (in FP16 as far as its smallest step allows: 2^-24 of the chunk's largest w, whatever x is).
 // An exponent of M is the sum of the log-decays behind token i up to t, from sums that start
 // anew every 4 tokens (the difference of two sums from the chunk's start, up to 2^15, would be
 // off by 2^-9); w comes from sums that start at the chunk's end.  So neither loses precision
