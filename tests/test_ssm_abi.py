@@ -101,13 +101,3 @@ def test_binding_refuses_what_is_not_on_the_gpu():
         gdn.gdn_block_norm(x, x, torch.zeros(8))
     with pytest.raises(TypeError):
         gdn.gdn_ssm_scan(None, x, x, x, x, x)
-
-
-def test_scan_form_option(lib):
-    assert gdn.gdn_get_option("ssm_scan_form") == 0
-    with gdn.options(ssm_scan_form=1):
-        assert gdn.gdn_get_option(gdn.GDN_OPT_SSM_SCAN_FORM) == 1
-    assert gdn.gdn_get_option("ssm_scan_form") == 0
-    for value in (-1, 2):
-        assert lib.gdn_set_option(gdn.GDN_OPT_SSM_SCAN_FORM, value) == INV
-    assert gdn.gdn_get_option("ssm_scan_form") == 0
