@@ -395,6 +395,78 @@ int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_
                    int dim, int dtype, int residual_dtype, void* cuda_stream);
 
 /*
+ * The paged 4-bit cache of softmax attention layers: gdn_kv_append puts new tokens' keys and
+ * values into it, rotated by position, gdn_kv_attention attends over it.  The pages have no
+ * counterpart; packed rows, strides, alignment, overlap, streams and graphs are as for the
+ * selective state space operators above.  Query head h reads key/value head h % n_kv_heads
+ * (a layer whose neighbouring heads share one is reordered with its weights, as above).
+ *
+ * Sequences: sequence s has rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 (cu_seqlens NULL: T / n_seq
+ * rows each), the last of the kv_lens[s] tokens in its cache: row i of n has place
+ * kv_lens[s] - n + i.  Both operators take the lengths with the new tokens.  Place j lies in page
+ * block_table[s][j / page_size] (the table's rows table_stride apart) at j % page_size.  A page
+ * below 0 or not below n_pages is no page, a place below 0 or behind the table's row no place:
+ * nothing is appended there and nothing there is seen.  Sequences may share pages that none of
+ * them appends to.  page_size: 16, 32, 64, 128 or 256.  head_dim: 64 or 128.
+ *
+ * Layout: cache [n_pages][n_kv_heads][2][page_size * 9 head_dim / 16] bytes, 16-byte aligned: of a
+ * page and head the keys, then the values, each the codes [page_size][head_dim / 2] (element 2 i
+ * in a byte's low half), then the scales [page_size][head_dim / 16].  A code is an e2m1 number
+ * (sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6), a scale an e4m3 number for 16 neighbouring elements;
+ * an element is code * scale * k_scale[head] (v_scale for values; NULL: 1).
+ */
+
+/*
+ * gdn_kv_append - rotates keys (and queries) by position and appends keys and values to the
+ * cache.  The first rotary_dim elements of a row (a multiple of 32, or 0) turn in pairs (a, b),
+ * elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where interleaved is 1, i < rotary_dim / 2:
+ *     angle = position * inv_freq[i];  a' = a cos - b sin;  b' = b cos + a sin
+ * position: positions[t], or NULL: the row's place.  Of 16 elements y of a key or value
+ *     scale = e4m3(max|y| / (6 k_scale));  code = e2m1(y / (scale k_scale))
+ * rounded to nearest, ties to even, and held at the largest finite number; the quotients are
+ * those of exact arithmetic, so the codes do not depend on how a row was computed.  An infinity
+ * counts as the largest, a NaN makes its scale a NaN.
+ *   q, q_out [T][n_heads][head_dim] (both or neither; q_out may be q), k, v [T][n_kv_heads]
+ *   [head_dim], k_out, v_out (each may be NULL) the same: of `dtype`.  k_out and v_out receive
+ *   the keys and values as the cache holds them.  inv_freq [rotary_dim / 2], k_scale, v_scale
+ *   [n_kv_heads] (or NULL; positive): FP32.
+ * Rows of no sequence are left as they were.  A token's place belongs to one row of a call.
+ */
+int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  const float* inv_freq, int rotary_dim, int interleaved, const int32_t* positions, const float* k_scale,
+                  const float* v_scale, void* cache, int64_t n_pages, int page_size, const int32_t* block_table,
+                  int64_t table_stride, int max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens, int n_seq,
+                  void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* v_out,
+                  int64_t v_out_stride, int64_t T, int n_heads, int n_kv_heads, int head_dim, int dtype,
+                  void* cuda_stream);
+
+/*
+ * gdn_kv_attention - softmax attention of every row over its sequence's cache:
+ *     out[t][h] = sum_j p_j V_j,  p = softmax over the j it sees of scale * q[t][h] . K_j
+ * A row at place i sees the places j < kv_lens with j <= i where causal is 1, and j > i - window
+ * where window is not 0 (which goes with causal).  A row that sees nothing gets zeros.
+ *   q, out [T][n_heads][head_dim]: GDN_BF16 or GDN_F16.  lse [T][n_heads] FP32 or NULL: the
+ *   logarithm of the softmax's sum (-infinity for a row that sees nothing), with which results
+ *   over several caches can be joined.
+ * Scores, maxima and sums are FP32; probabilities are rounded to FP16 for the product with V,
+ * which like K is exact there.  What a row does not see does not reach it, whatever it is: bytes
+ * behind a sequence's end, pages of others.  A NaN scale among a token's values makes the rows
+ * that see it NaN throughout.  The order of a row's sums goes by the other sequences of the call;
+ * the same call gives the same bits.
+ * workspace: gdn_kv_attention_workspace_bytes() bytes, 16-byte aligned, the call's own until it
+ * has finished.
+ */
+int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t n_pages, int page_size,
+                     const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_lens,
+                     const int32_t* cu_seqlens, int n_seq, const float* k_scale, const float* v_scale, float scale,
+                     int causal, int window, void* out, int64_t out_stride, float* lse, int64_t T, int n_heads,
+                     int n_kv_heads, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
+                     void* cuda_stream);
+
+/* Bytes of workspace a gdn_kv_attention call of these sizes needs (0: none). */
+size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int n_heads, int n_kv_heads, int head_dim);
+
+/*
  * Process-wide options.  The library reads no environment variable: the A/B
  * forms of its kernels and its failure-path test hooks are chosen here.  A value
  * applies to every call that starts after gdn_set_option returns; do not change

@@ -1,0 +1,61 @@
+// Host-side interface between the C ABI of the paged 4-bit cache (gdn_kv_api.cu) and its
+// kernel files, with the cache's layout.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gdn.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+constexpr int kKvGroup = 16;  // elements of a row that share a scale
+
+// The sequences of a call and their pages.
+struct KvSeqs {
+    const int32_t* cu;       // [n_seq + 1], or nullptr: n_seq sequences of per_seq rows each
+    const int32_t* kv_lens;  // [n_seq]
+    const int32_t* table;    // [n_seq][max_pages], rows table_stride apart
+    int64_t table_stride;
+    int64_t T;
+    int64_t n_pages;
+    int64_t per_seq;
+    int n_seq, max_pages, page_log2;
+};
+
+// ---- appending (gdn_kv_append.cu) ----
+struct KvAppendParams {
+    const void *q, *k, *v;  // q may be nullptr
+    void *q_out, *k_out, *v_out;  // each may be nullptr (q_out with q)
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;
+    const float* inv_freq;  // [rotary / 2]
+    const int32_t* positions;  // [T] or nullptr: a row's place in its cache
+    const float *k_scale, *v_scale;  // [n_kv] or nullptr
+    uint8_t* cache;
+    KvSeqs s;
+    int n_heads, n_kv, head_dim, rotary, interleaved, dtype;
+    bool vector;  // every row of 16 bytes' pieces
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, int sm_count, cudaStream_t s);
+
+// ---- attention ----
+struct KvAttentionParams {
+    const void* q;
+    void* out;
+    float* lse;  // [T][n_heads] or nullptr
+    int64_t q_stride, out_stride;
+    const float *k_scale, *v_scale;
+    const uint8_t* cache;
+    KvSeqs s;
+    float scale;  // of the scores, times log2 e
+    int n_heads, n_kv, head_dim, causal, window, dtype;
+    bool vector;  // q's and out's rows on 16-byte boundaries
+    void* workspace;
+    int* status;
+};
+// Up to 16 rows (tokens x heads of a group) at a time on the warps' own MMAs (gdn_kv_few.cu).
+size_t kv_few_workspace(int head_dim, int sm_count);
+cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s);
+
+}  // namespace gdn

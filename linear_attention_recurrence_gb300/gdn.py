@@ -65,7 +65,7 @@ EXPORTS = ("gdn_recurrence", "gdn_out_norm", "gdn_last_error", "gdn_device_statu
            "gdn_release_scratch", "gdn_poison_scratch", "gdn_chunked_scratch_bytes", "gdn_launch_count",
            "gdn_recurrence_chunked_noalloc", "gdn_decode", "gdn_prestage", "gdn_recurrence_norm",
            "gdn_set_option", "gdn_get_option", "gdn_ssm_conv", "gdn_ssm_scan", "gdn_ssm_scan_workspace_bytes",
-           "gdn_ssm_step", "gdn_block_norm")
+           "gdn_ssm_step", "gdn_block_norm", "gdn_kv_append", "gdn_kv_attention", "gdn_kv_attention_workspace_bytes")
 
 
 class GDNError(RuntimeError):
@@ -113,6 +113,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_block_norm.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, f32, f32, vp, i64, vp, i64, i64, i32,
                                        i32, i32, vp]
         lib.gdn_block_norm.restype = i32
+        lib.gdn_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i32, vp, vp, vp, vp, i64, i32, vp, i64, i32, vp,
+                                      vp, i32, vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, i32, vp]
+        lib.gdn_kv_append.restype = i32
+        lib.gdn_kv_attention.argtypes = [vp, i64, vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, vp, f32, i32, i32, vp,
+                                         i64, vp, i64, i32, i32, i32, i32, vp, sz, vp]
+        lib.gdn_kv_attention.restype = i32
+        lib.gdn_kv_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        lib.gdn_kv_attention_workspace_bytes.restype = sz
         lib.gdn_last_error.argtypes = []
         lib.gdn_last_error.restype = ctypes.c_char_p
         lib.gdn_device_status.argtypes = [vp]
@@ -621,6 +629,124 @@ def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: boo
     _launch(lib.gdn_block_norm, dev, stream, bp, bs, rp, rs, gp, gs, 1 if gate_sigmoid else 0, wpost, wpre, scale, eps,
             qp, qs, op, os_, T, d, dt, rt)
     return residual_out, out
+
+
+# ---- the paged 4-bit cache ----
+
+
+def gdn_kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device=None):
+    """An empty cache of ``n_pages`` pages for gdn_kv_append and gdn_kv_attention:
+    [n_pages][n_kv_heads][2][page_size * 9 head_dim / 16] bytes (gdn.h has the layout)."""
+    return torch.zeros((n_pages, n_kv_heads, 2, page_size * 9 * head_dim // 16), dtype=torch.uint8,
+                       device=torch.device("cuda") if device is None else device)
+
+
+def _paged(cache, block_table, kv_lens, cu_seqlens, T, n_kv, D, index):
+    """The arguments that say where a call's tokens lie: (cache, n_pages, page_size, table, table_stride,
+    max_pages, kv_lens, cu, n_seq)."""
+    i32 = torch.int32
+    _dims(cache, "cache", 4)
+    _dims(block_table, "block_table", 2)
+    _dims(kv_lens, "kv_lens", 1)
+    n = kv_lens.shape[0]
+    pages, plane = cache.shape[0], cache.shape[3]
+    page = plane * 16 // (9 * D) if D else 0
+    if page * 9 * D // 16 != plane or page <= 0:
+        raise ValueError(f"the cache's pages of {plane} bytes a head do not hold tokens of head_dim {D}")
+    cp = _dense(cache, "cache", (pages, n_kv, 2, plane), torch.uint8, index)
+    tp, ts = _rows(block_table, "block_table", (n, block_table.shape[1]), i32, index)
+    if n <= 1:
+        ts = max(ts, block_table.shape[1])
+    lp = _dense(kv_lens, "kv_lens", (n,), i32, index)
+    if cu_seqlens is None and n and T % n:
+        raise ValueError(f"{T} rows of {n} sequences need cu_seqlens")
+    return cp, pages, page, tp, ts, block_table.shape[1], lp, _dense(cu_seqlens, "cu_seqlens", (n + 1,), i32, index), n
+
+
+def gdn_kv_append(k, v, cache, block_table, kv_lens, q=None, inv_freq=None, interleaved: bool = False, positions=None,
+                  k_scale=None, v_scale=None, cu_seqlens=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """Appends keys and values to the pages of their sequences in 4 bits, the keys (and the
+    queries) rotated by position; updates ``cache`` in place and returns the rotated queries
+    (None without ``q``).
+
+    k, v: [T][n_kv_heads][head_dim], q: [T][n_heads][head_dim] or None: of one type (FP32, BF16 or
+    FP16), the rows any distance apart.  cache: as gdn_kv_cache gives it; block_table:
+    [n][max_pages] int32, a sequence's pages in order; kv_lens: [n] int32, the sequences' lengths
+    with the new tokens, which are their last; cu_seqlens: [n + 1] int32 (None: T / n rows each).
+    inv_freq: [rotary_dim / 2] FP32 (None: no rotation), positions: [T] int32 (None: a token's
+    place in its cache); interleaved: pairs (2 i, 2 i + 1) rather than (i, i + rotary_dim / 2).
+    k_scale, v_scale: [n_kv_heads] FP32 or None.  ``q_out`` is allocated if None (it may be ``q``);
+    ``k_out`` and ``v_out``, where given, receive what the cache holds of k and v.
+    """
+    dt, dev = _activations(k, "k", 3)
+    ty, f32 = k.dtype, torch.float32
+    T, G, D = shape = k.shape
+    kp, ks = _rows(k, "k", shape, ty, dev)
+    vp_, vs = _rows(v, "v", shape, ty, dev)
+    where = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, dev)
+    rotary = 0
+    if inv_freq is not None:
+        _dims(inv_freq, "inv_freq", 1)
+        rotary = 2 * inv_freq.shape[0]
+    fp = _dense(inv_freq, "inv_freq", (rotary // 2,), f32, dev)
+    pp = _dense(positions, "positions", (T,), torch.int32, dev)
+    ksp, vsp = _dense(k_scale, "k_scale", (G,), f32, dev), _dense(v_scale, "v_scale", (G,), f32, dev)
+    H, qp, qs, qop, qos = G, None, 0, None, 0
+    if q is not None:
+        _dims(q, "q", 3)
+        H = q.shape[1]
+        qp, qs = _rows(q, "q", (T, H, D), ty, dev)
+        if q_out is None:
+            q_out = _empty((T, H, D), ty, dev, stream)
+        qop, qos = _rows(q_out, "q_out", (T, H, D), ty, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kop, kos = (None, 0) if k_out is None else _rows(k_out, "k_out", shape, ty, dev)
+    vop, vos = (None, 0) if v_out is None else _rows(v_out, "v_out", shape, ty, dev)
+    if T <= 1:
+        qos, kos, vos = max(qos, H * D), max(kos, G * D), max(vos, G * D)
+    cp, pages, page, tp, ts, width, lp, cu, n = where
+    lib = _lib or load_library()
+    _launch(lib.gdn_kv_append, dev, stream, qp, qs, kp, ks, vp_, vs, fp, rotary, 1 if interleaved else 0, pp, ksp, vsp, cp,
+            pages, page, tp, ts, width, lp, cu, n, qop, qos, kop, kos, vop, vos, T, H, G, D, dt)
+    return q_out
+
+
+def gdn_kv_attention(q, cache, block_table, kv_lens, k_scale=None, v_scale=None, scale=None, causal: bool = True,
+                     window: int = 0, cu_seqlens=None, out=None, lse=None, stream=None):
+    """Softmax attention of new tokens over their sequences' pages (gdn_kv_append's, theirs
+    included); returns ``out``.
+
+    q: [T][n_heads][head_dim], BF16 or FP16, the rows any distance apart; head h reads key/value
+    head h % n_kv_heads.  cache, block_table, kv_lens, cu_seqlens, k_scale, v_scale as in
+    gdn_kv_append.  scale: of the scores (None: head_dim ** -0.5); causal: a token sees its own
+    place and those before it, with a ``window`` only the last so many.  ``out`` (as q) is
+    allocated if None; ``lse`` ([T][n_heads] FP32), where given, receives the logarithm of each
+    row's sum.  Rows of no sequence are left as they were; a row that sees nothing gets zeros.
+    """
+    dt, dev = _activations(q, "q", 3)
+    _dims(cache, "cache", 4)
+    ty, f32 = q.dtype, torch.float32
+    T, H, D = shape = q.shape
+    G = cache.shape[1]
+    qp, qs = _rows(q, "q", shape, ty, dev)
+    cp, pages, page, tp, ts, width, lp, cu, n = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, dev)
+    ksp, vsp = _dense(k_scale, "k_scale", (G,), f32, dev), _dense(v_scale, "v_scale", (G,), f32, dev)
+    if out is None:
+        out = _empty(shape, ty, dev, stream)
+    op, os_ = _rows(out, "out", shape, ty, dev)
+    lsep = _dense(lse, "lse", (T, H), f32, dev)
+    lib = _lib or load_library()
+    if _current_device() == dev:  # (it goes by the device's multiprocessors)
+        need = lib.gdn_kv_attention_workspace_bytes(T, n, H, G, D)
+    else:
+        with torch.cuda.device(dev):
+            need = lib.gdn_kv_attention_workspace_bytes(T, n, H, G, D)
+    ws = _empty((need,), torch.uint8, dev, stream) if need else None
+    _launch(lib.gdn_kv_attention, dev, stream, qp, qs, cp, pages, page, tp, ts, width, lp, cu, n, ksp, vsp,
+            D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, max(os_, H * D) if T <= 1 else os_, lsep,
+            T, H, G, D, dt, None if ws is None else ws.data_ptr(), need)
+    return out
 
 
 def gdn_device_status(stream=None) -> int:
