@@ -2,14 +2,14 @@
 // requests, drafted tokens.
 //
 // A unit is one (sequence, KV head, block of R = 8 or 16 rows), a row being a (token, head of
-// the KV head's group); its work is the tiles of 32 tokens that one of its rows may see.  All
-// units' tiles, in order, are cut into equal pieces, one for each CTA, so that ragged lengths
-// fill the device evenly; a unit that several CTAs share leaves partial results in the
-// workspace, which a second launch joins in order of the tokens.
+// the KV head's group); its work is the tiles of 64 tokens (32 where R is 16) that one of its rows
+// may see.  All units' tiles, in order, are cut into equal pieces, one for each warp, so that
+// ragged lengths fill the device evenly; a unit that several warps share leaves partial results
+// in the workspace, which a second launch joins in order of the tokens.
 //
-// Every warp walks tiles of its own: it copies a tile's codes and scales into its own slots of
-// shared memory (cp.async.bulk, two tiles ahead) and computes, transposed so that the few rows
-// are the narrow side of m16n8k16 products:
+// A warp copies a tile's codes and scales into its own two slots of shared memory
+// (cp.async.bulk) and computes, transposed so that the few rows are the narrow side of m16n8k16
+// products:
 //     S^T = K Q^T   (16 tokens x 8 rows, over head_dim), running maximum and sum of each row,
 //     O^T += V^T P^T   (16 of head_dim x 8 rows, over 16 tokens)
 // The order of head_dim in the first product's sum and of its lanes in the second is free, so
@@ -31,34 +31,35 @@
 namespace gdn {
 namespace {
 
-constexpr int kTile = 32;    // tokens a warp takes at a time
 constexpr int kSlots = 2;    // tiles in shared memory a warp
-constexpr int kMinTiles = 16;  // a CTA's piece, at least
-constexpr float kPShift = 8.f;
+constexpr int kUnitTiles = 1;  // what a unit's start and end count for, in tiles
+// A row's maximum is renewed only once a score passes it by more than 2^kSlack: probabilities,
+// times 2^kPShift, stay below 2^(kPShift + kSlack) (FP16 ends at 2^16).
+constexpr float kPShift = 8.f, kSlack = 7.f;
+
+// Warps are apart from one another: a unit's start (its lengths, pages and queries, one load after
+// the other) and its end overlap with the other warps' work.  CTAs are only what they come in.
+constexpr int kWarps = 4, kCtasPerSm = 3;
+// Where there is enough to do, pieces a warp of the resident ones: CTAs that end early make room.
+constexpr int kWaves = 2;
+constexpr int kPiecesPerSm = kWarps * kCtasPerSm * kWaves;
+// Tiles of a piece: a wave's share at most, down to kMinTiles, and no fewer than the waves leave.
+constexpr int kMinTiles = 2, kSmallPiece = 8;
 
 template <int NT>
-constexpr int kWarps = NT == 1 ? 16 : 12;
-template <int D>
-constexpr int kTileBytes = 2 * kTile * (D / 2 + D / kKvGroup);
+constexpr int kTileOf = NT == 1 ? 64 : 32;
+template <int D, int NT>
+constexpr int kTileBytes = 2 * kTileOf<NT> * (D / 2 + D / kKvGroup);
 
 // A partial result: R rows of head_dim sums, then R maxima (base 2) and R sums.
 template <int R, int D>
 constexpr int kPartialFloats = R * (D + 2);
 
-struct Unit {
-    int s, head, block;
-    int64_t begin;     // first row of the sequence
-    int64_t rows;      // its rows (tokens)
-    int64_t tiles;     // tiles of each of its units
-    int64_t first;     // tile (of the sequence) that they begin with
-    int64_t blocks;    // row blocks
-};
-
 struct Geometry {
     int64_t begin, rows, tiles, first, blocks, cost;
 };
 // What sequence s has to do: `tiles` for each of n_kv * blocks units.
-__device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, int R) {
+__device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, int R, int tile) {
     Geometry g{};
     int64_t e;
     kv_rows(p.s, s, g.begin, e);
@@ -72,72 +73,103 @@ __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, 
         lo = len - g.rows - p.window + 1;
         lo = lo < 0 ? 0 : lo;
     }
-    g.first = lo / kTile;
-    g.tiles = (hi + kTile - 1) / kTile - g.first;
+    g.first = lo / tile;
+    g.tiles = (hi + tile - 1) / tile - g.first;
     if (g.tiles < 1) g.tiles = 1;  // (its rows see nothing: the outputs are zeros)
     const int group = p.n_heads / p.n_kv;
     g.blocks = (g.rows * group + R - 1) / R;
-    g.cost = g.tiles * g.blocks * p.n_kv;
+    g.cost = (g.tiles + kUnitTiles) * g.blocks * p.n_kv;
     return g;
 }
 
-template <int W>
 struct Scratch {
-    int64_t warp_sum[W];
-    int64_t found_base;
-    int found;
+    int64_t warp_sum[kWarps];
+    int64_t base[kWarps];  // of each warp's piece: the tiles before its sequence,
+    int seq[kWarps];       // and the sequence
 };
 
-// The sum of all sequences' tiles; and the sequence that holds tile `at` of them, with the
-// tiles before it.  (at < 0: the sum alone.)
-template <int W>
-__device__ int64_t scan_tiles(const KvAttentionParams& p, int R, int64_t at, Scratch<W>& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t base = 0;
-    for (int s0 = 0; s0 < p.s.n_seq; s0 += W * 32) {
-        const int64_t n = s0 + tid < p.s.n_seq ? geometry(p, s0 + tid, R).cost : 0;
-        int64_t inc = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += v;
-        }
-        if (lane == 31) sh.warp_sum[warp] = inc;
-        __syncthreads();
-        int64_t before = base, total = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const int64_t v = sh.warp_sum[w];
-            if (w < warp) before += v;
-            total += v;
-        }
-        const int64_t first = before + inc - n;
-        if (at >= first && at < first + n) {
-            sh.found = s0 + tid;
-            sh.found_base = first;
-        }
-        base += total;
-        __syncthreads();
-        if (at >= 0 && base > at) break;
-    }
-    return base;
+// Tiles of a piece, of `total` tiles, over the resident warps or kWaves times as many.
+__device__ __forceinline__ int64_t piece_tiles(int64_t total, int64_t pieces) {
+    const int64_t one = (total * kWaves + pieces - 1) / pieces, all = (total + pieces - 1) / pieces;
+    const int64_t small = one < kSmallPiece ? one : kSmallPiece;
+    const int64_t per = all > small ? all : small;
+    return per > kMinTiles ? per : kMinTiles;
 }
 
-// What the joining launch needs to know of a CTA whose first unit began in an earlier one and
+// Sums up all sequences' tiles and finds, for each of the CTA's warps, the sequence that its
+// piece begins in.  Returns the tiles of a piece; 0: nothing is left for this CTA.
+__device__ int64_t find_pieces(const KvAttentionParams& p, int R, int tile, int64_t* all, Scratch& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kThreads = kWarps * 32;
+    const int64_t pieces = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t per = 0, total = 0, at = 0;
+    // one round over the sequences for the sum, another for the places (the same one where a round has them all)
+    for (int round = 0; round < 2; ++round) {
+        int64_t base = 0;
+        for (int s0 = 0; s0 < p.s.n_seq; s0 += kThreads) {
+            const int64_t n = s0 + tid < p.s.n_seq ? geometry(p, s0 + tid, R, tile).cost : 0;
+            int64_t inc = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += v;
+            }
+            if (lane == 31) sh.warp_sum[warp] = inc;
+            __syncthreads();
+            int64_t before = base, sum = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const int64_t v = sh.warp_sum[w];
+                if (w < warp) before += v;
+                sum += v;
+            }
+            const int64_t first = before + inc - n;
+            base += sum;
+            if (p.s.n_seq <= kThreads) {
+                total = base;
+                per = piece_tiles(total, pieces);
+                at = static_cast<int64_t>(blockIdx.x) * kWarps * per;
+                round = 1;
+            }
+            if (round == 1) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const int64_t mine = at + w * per;
+                    if (mine >= first && mine < first + n) {
+                        sh.base[w] = first;
+                        sh.seq[w] = s0 + tid;
+                    }
+                }
+            }
+            __syncthreads();
+            if (round == 1 && base > at + (kWarps - 1) * per) break;  // uniform
+        }
+        if (round == 0) {
+            total = base;
+            per = piece_tiles(total, pieces);
+            at = static_cast<int64_t>(blockIdx.x) * kWarps * per;
+            if (at >= total) break;
+        }
+    }
+    *all = total;
+    return per;
+}
+
+// What the joining launch needs to know of a piece whose first unit began in an earlier one and
 // ends here.
 struct Join {
     int64_t row;    // first row of the block (token * group + head), from the sequence's first
     int64_t begin;  // first row of the sequence
     int rows;       // rows of the block; 0: nothing to join
     int head;       // KV head
-    int first_cta;  // the CTA that the unit began in
+    int first_piece;  // the piece that the unit began in
     int pad;
 };
 
 template <int R, int D>
-__device__ __forceinline__ float* partial_of(void* ws, int ctas, int cta, int which) {
-    return reinterpret_cast<float*>(static_cast<char*>(ws) + static_cast<size_t>(ctas) * sizeof(Join)) +
-           (static_cast<int64_t>(cta) * 2 + which) * kPartialFloats<R, D>;
+__device__ __forceinline__ float* partial_of(void* ws, int64_t pieces, int64_t piece, int which) {
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + pieces * sizeof(Join)) +
+           (piece * 2 + which) * kPartialFloats<R, D>;
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -164,63 +196,70 @@ __device__ __forceinline__ void row_of(int64_t row, int group, int n_kv, int kv_
 }
 
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAttentionParams p) {
-    constexpr int W = kWarps<NT>, R = 8 * NT;
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const KvAttentionParams p) {
+    constexpr int R = 8 * NT, kTile = kTileOf<NT>;
     constexpr int DL = D / 4;        // elements of a token's K that a lane takes (its words: DL / 8)
     constexpr int KS = D / 16;       // k-steps of S^T, M tiles of O^T
     constexpr int kPlane = kTile * (D / 2 + D / kKvGroup);  // K's, then V's, in a tile
     constexpr int kScales = kTile * D / 2;                  // their scales within it
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Scratch<W> scratch;
-    __shared__ uint64_t bars[W * kSlots];
-    __shared__ float warp_max[W][R], warp_sum[W][R];
+    __shared__ Scratch scratch;
+    __shared__ uint64_t bars[kWarps * kSlots];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int group = p.n_heads / p.n_kv;
+    const int64_t pieces = static_cast<int64_t>(gridDim.x) * kWarps, piece = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
 
     if (lane == 0) {
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars[warp * kSlots + i], 1);
     }
     mbar_init_fence();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __syncthreads();
-    const int64_t total = scan_tiles<W>(p, R, -1, scratch);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinTiles) per = kMinTiles;
-    int64_t at = static_cast<int64_t>(blockIdx.x) * per;
+    int64_t total;
+    const int64_t per = find_pieces(p, R, kTile, &total, scratch);
+    int64_t at = piece * per;
     const int64_t end = at + per < total ? at + per : total;
-    Join* join = static_cast<Join*>(p.workspace) + blockIdx.x;
-    if (tid == 0) join->rows = 0;
+    Join* join = static_cast<Join*>(p.workspace) + piece;
+    if (lane == 0) join->rows = 0;
+    __syncwarp();
     if (at >= end) return;
-    scan_tiles<W>(p, R, at, scratch);
-    int s = scratch.found;
-    int64_t base = scratch.found_base;  // tiles before sequence s
-    Geometry geo = geometry(p, s, R);
+    int s = scratch.seq[warp];
+    int64_t base = scratch.base[warp];  // tiles before sequence s
+    Geometry geo = geometry(p, s, R, kTile);
 
-    unsigned char* slots = smem + warp * kSlots * kTileBytes<D>;
+    unsigned char* slots = smem + warp * kSlots * kTileBytes<D, NT>;
     uint64_t* bar = bars + warp * kSlots;
     uint32_t uses = 0;  // copies this warp has waited for
 
     while (at < end) {
         while (at >= base + geo.cost) {  // the next sequence with rows
             base += geo.cost;
-            geo = geometry(p, ++s, R);
+            geo = geometry(p, ++s, R, kTile);
         }
-        const int64_t unit = (at - base) / geo.tiles;  // head-major
-        const int64_t unit_begin = base + unit * geo.tiles;
+        const int64_t unit_cost = geo.tiles + kUnitTiles;
+        const int64_t unit = (at - base) / unit_cost;  // head-major
+        const int64_t unit_begin = base + unit * unit_cost;
         const int head = static_cast<int>(unit / geo.blocks);
         const int64_t row0 = (unit - head * geo.blocks) * R;
         const int64_t left = geo.rows * group - row0;
         const int rows = left < R ? static_cast<int>(left) : R;
-        const int64_t unit_end = unit_begin + geo.tiles;
+        // its tiles from `begin_tile` to `end_tile` are this warp's (the first of a unit's cost is its start)
+        const int64_t unit_end = unit_begin + unit_cost;
         const int64_t stop = end < unit_end ? end : unit_end;
-        const int n_tiles = static_cast<int>(stop - at);
-        const int64_t tile0 = geo.first + (at - unit_begin);
+        const int64_t begin_tile = at - unit_begin > kUnitTiles ? at - unit_begin - kUnitTiles : 0;
+        const int64_t end_tile = stop - unit_begin > kUnitTiles ? stop - unit_begin - kUnitTiles : 0;
+        const int n_tiles = static_cast<int>(end_tile - begin_tile);
+        const int64_t tile0 = geo.first + begin_tile;
+        if (n_tiles == 0) {
+            at = stop;
+            continue;
+        }
         const int64_t len = __ldg(p.s.kv_lens + s);
         const int64_t cap = kv_capacity(p.s);
         const int held = static_cast<int>(len < cap ? len : cap);
 
-        // what each lane copies of a tile: part (pages of 16 give two), and which of the four arrays
-        const int part_log2 = p.s.page_log2 < 5 ? p.s.page_log2 : 5;
+        // what each lane copies of a tile: its part (small pages give two or four), and which of four arrays
+        constexpr int kTileLog2 = kTile == 64 ? 6 : 5;
+        const int part_log2 = p.s.page_log2 < kTileLog2 ? p.s.page_log2 : kTileLog2;
         const int parts = kTile >> part_log2;
         const int64_t plane = kv_plane(p.s.page_log2, D);
         const int part = lane >> 2, which = lane & 3;  // K codes, K scales, V codes, V scales
@@ -230,7 +269,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
             const int64_t token = tile * kTile + (static_cast<int64_t>(part) << part_log2);
             return part < parts && token < held ? kv_page(p.s, s, token) : -1;
         };
-        // issues the copies of a tile; returns which of its two halves there are
+        // issues the copies of a tile; returns which of its sixteen-token parts there are
         auto fetch = [&](int64_t tile, int64_t page, int slot) -> uint32_t {
             const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && which == 0);
             const int n = __popc(there);
@@ -246,20 +285,20 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
                 const int64_t in_page = token & ((int64_t{1} << p.s.page_log2) - 1);
                 const uint8_t* src = p.cache + ((page * p.n_kv + head) * 2 + (which >> 1)) * plane +
                                      (is_scale ? (int64_t{D / 2} << p.s.page_log2) : 0) + in_page * row_bytes;
-                unsigned char* dst = slots + slot * kTileBytes<D> + (which >> 1) * kPlane + (is_scale ? kScales : 0) +
+                unsigned char* dst = slots + slot * kTileBytes<D, NT> + (which >> 1) * kPlane + (is_scale ? kScales : 0) +
                                      (part << part_log2) * row_bytes;
                 bulk_load(dst, src, row_bytes << part_log2, &bar[slot]);
             }
-            if (parts == 1) return there ? 3u : 0u;
-            return (there & 1) | ((there >> 3) & 2);
+            // (bit 4 i: part i; a part of 32 or 64 tokens is two or four sixteenths)
+            const uint32_t first = part_log2 == 4 ? there : part_log2 == 5 ? (there & 1) * 0x11 | (there >> 4 & 1) * 0x1100
+                                                                          : (there & 1) * 0x1111;
+            return (first & 1) | (first >> 3 & 2) | (first >> 6 & 4) | (first >> 9 & 8);
         };
         uint32_t halves[kSlots];
         int64_t next_page = -1;
-        const int mine = n_tiles > warp ? (n_tiles - warp + W - 1) / W : 0;  // this warp's tiles
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            halves[i] = i < mine ? fetch(tile0 + warp + i * W, page_at(tile0 + warp + i * W), i) : 0;
-        if (mine > kSlots) next_page = page_at(tile0 + warp + kSlots * W);
+        for (int i = 0; i < kSlots; ++i) halves[i] = i < n_tiles ? fetch(tile0 + i, page_at(tile0 + i), i) : 0;
+        if (n_tiles > kSlots) next_page = page_at(tile0 + kSlots);
 
         // the rows' queries (row 8 n + g, its elements DL c ..), scaled; and what each lane's
         // columns 8 n + 2 c, + 1 of S^T see: tokens [from, to)
@@ -291,6 +330,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
                 }
             }
             float unscale = 1.f;
+            const float f0 = p.scale * (p.k_scale ? __ldg(p.k_scale + head) : 1.f);
+            if (f0 < 0) {  // the factor of the scores is never below 0, so that it keeps their order
+#pragma unroll
+                for (int i = 0; i < DL; ++i) q[i] = -q[i];
+            }
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 float most = 0;
 #pragma unroll
@@ -307,7 +351,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
             }
 #pragma unroll
             for (int i = 0; i < DL / 2; ++i) qf[n][i] = pack_f16(q[2 * i], q[2 * i + 1]);
-            const float f = unscale * p.scale * (p.k_scale ? __ldg(p.k_scale + head) : 1.f);
+            // (nor 0, which would make a NaN of a place that is not seen)
+            const float f = fabsf(f0) * unscale < 1e-37f ? 1e-37f : fabsf(f0) * unscale;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 fac[2 * n + k] = __shfl_sync(0xffffffffu, f, 8 * c + 4 * k);
@@ -323,7 +368,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
         }
 
         float o[NT][KS][4];
-        float top[2 * NT], sum[2 * NT];
+        float top[2 * NT];
+        float2 sum[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -331,7 +377,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][t][k] = 0;
             top[2 * n] = top[2 * n + 1] = -INFINITY;
-            sum[2 * n] = sum[2 * n + 1] = 0;
+            sum[n] = make_float2(0, 0);
         }
         // tokens that all the lane's columns see
         int all_from = from[0], all_to = to[0];
@@ -342,35 +388,35 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
         }
         const int pg = g ^ ((g >> 1) & 1);  // the token of row g: pairs (4 i + 2, 4 i + 3) swapped, which
                                             // spreads V's loads over the banks
-        for (int i = 0; i < mine; ++i) {
+        for (int i = 0; i < n_tiles; ++i) {
             const int slot = i % kSlots;
-            const int64_t tile = tile0 + warp + static_cast<int64_t>(i) * W;
+            const int64_t tile = tile0 + i;
             if (!mbar_wait(&bar[slot], (uses / kSlots) & 1)) {
                 report_error(p.status, kDevErrKv);
-                mbar_wait(&bar[slot], (uses / kSlots) & 1);  // the copy lands before the CTA can leave
+                mbar_wait(&bar[slot], (uses / kSlots) & 1);  // the copy lands before the warp can leave
             }
             __syncwarp();
             ++uses;
-            const unsigned char* kc = slots + slot * kTileBytes<D>;
+            const unsigned char* kc = slots + slot * kTileBytes<D, NT>;
             const unsigned char* vc = kc + kPlane;
             const uint32_t there = halves[slot];
             const int token0 = static_cast<int>(tile) * kTile;
-            const bool whole = there == 3 && token0 >= all_from && token0 + kTile <= all_to;
-            float sc[2][NT][4];
-            uint32_t vs[2];  // V's scales of the lane's 4 tokens of each half
-            bool odd = false;
+            const bool whole = there == (1u << kTile / 16) - 1 && token0 >= all_from && token0 + kTile <= all_to;
             // the lane's tokens of V: pairs (2 c, 2 c + 1), the odd lanes' swapped, and 8 behind
             const int t0 = 2 * c + (c & 1), t1 = 2 * c + 1 - (c & 1);
+            uint32_t vs[kTile / 16];  // V's scales of the lane's 4 tokens of each 16
+            uint32_t nan = 0;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kTile / 16; ++b) {
                 const unsigned char* at_s = vc + kScales + 16 * b * (D / kKvGroup) + (g * KS >> 3);
                 vs[b] = at_s[t0 * (D / kKvGroup)] | at_s[t1 * (D / kKvGroup)] << 8 |
                         at_s[(t0 + 8) * (D / kKvGroup)] << 16 | static_cast<uint32_t>(at_s[(t1 + 8) * (D / kKvGroup)]) << 24;
-                odd |= any_e4m3_nan(vs[b]);
+                nan |= (vs[b] & 0x7f7f7f7fu) + 0x01010101u;
             }
-            odd = __any_sync(0xffffffffu, odd || !whole);
+            const bool odd = __any_sync(0xffffffffu, (nan & 0x80808080u) || !whole);
+            float2 sc[kTile / 16][NT][2];  // S^T: [token row g, + 8], columns 2 c, 2 c + 1
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kTile / 16; ++b) {
                 // ---- S^T: tokens 16 b + pg, + 8
                 uint32_t kw[2][DL / 8], ks[2][DL / 16];
 #pragma unroll
@@ -397,10 +443,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
                     ks[h][0] = __byte_perm(f, f, 0x1010);
                     if constexpr (D == 128) ks[h][1] = __byte_perm(f, f, 0x3232);
                 }
+                float acc[NT][4], acc2[NT][4];  // two chains, so that products wait less for one another
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[b][n][k] = 0;
+                    for (int k = 0; k < 4; ++k) acc[n][k] = acc2[n][k] = 0;
 #pragma unroll
                 for (int w = 0; w < DL / 8; ++w) {  // 8 codes: two k-steps
                     uint32_t f0[4], f1[4];
@@ -415,65 +462,86 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t a[4] = {f0[2 * k], f1[2 * k], f0[2 * k + 1], f1[2 * k + 1]};
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(sc[b][n], a, qf[n][4 * w + 2 * k], qf[n][4 * w + 2 * k + 1]);
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(k ? acc2[n] : acc[n], a, qf[n][4 * w + 2 * k], qf[n][4 * w + 2 * k + 1]);
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float v = sc[b][n][k] * fac[2 * n + (k & 1)];
-                        if (odd) {
+                    for (int k = 0; k < 4; ++k) acc[n][k] += acc2[n][k];
+                if (odd) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
                             const int tok = token0 + 16 * b + 8 * (k >> 1) + pg;
-                            if (!(there >> b & 1) || tok < from[2 * n + (k & 1)] || tok >= to[2 * n + (k & 1)]) v = -INFINITY;
+                            if (!(there >> b & 1) || tok < from[2 * n + (k & 1)] || tok >= to[2 * n + (k & 1)])
+                                acc[n][k] = -INFINITY;
                         }
-                        sc[b][n][k] = v;
-                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    sc[b][n][0] = make_float2(acc[n][0], acc[n][1]);
+                    sc[b][n][1] = make_float2(acc[n][2], acc[n][3]);
+                }
             }
-            // ---- the rows' maxima; what was summed up under a smaller one shrinks
-            float shift[2 * NT];
-            bool grew = false;
+            // ---- the rows' maxima, where a score passes one by far; what was summed up shrinks
+            bool past = false;
+            float most[2 * NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                float m0 = sc[0][n][0].x, m1 = sc[0][n][0].y;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float m = fmaxf(fmaxf(sc[0][n][k], sc[0][n][k + 2]), fmaxf(sc[1][n][k], sc[1][n][k + 2]));
+                for (int x = 1; x < kTile / 8; ++x) {
+                    m0 = fmaxf(m0, sc[x / 2][n][x & 1].x);
+                    m1 = fmaxf(m1, sc[x / 2][n][x & 1].y);
+                }
+                most[2 * n] = m0 * fac[2 * n];
+                most[2 * n + 1] = m1 * fac[2 * n + 1];
+                past |= most[2 * n] > top[2 * n] + kSlack || most[2 * n + 1] > top[2 * n + 1] + kSlack;
+            }
+            if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+                for (int x = 0; x < 2 * NT; ++x) {
+                    float m = most[x];
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    const int x = 2 * n + k;
                     const float now = fmaxf(top[x], m);
-                    shift[x] = top[x] == now ? 1.f : ex2(top[x] - now);
-                    grew |= top[x] != now;
+                    most[x] = top[x] == now ? 1.f : ex2(top[x] - now);
                     top[x] = now;
                 }
-            if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sum[2 * n] *= shift[2 * n];
-                    sum[2 * n + 1] *= shift[2 * n + 1];
+                    sum[n].x *= most[2 * n];
+                    sum[n].y *= most[2 * n + 1];
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[n][t][k] *= shift[2 * n + (k & 1)];
+                        for (int k = 0; k < 4; ++k) o[n][t][k] *= most[2 * n + (k & 1)];
                 }
             }
             // ---- O^T += V^T P^T
+            float2 less[NT], f2[NT];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int n = 0; n < NT; ++n) {
+                less[n] = make_float2(kPShift - (top[2 * n] == -INFINITY ? 0.f : top[2 * n]),
+                                      kPShift - (top[2 * n + 1] == -INFINITY ? 0.f : top[2 * n + 1]));
+                f2[n] = make_float2(fac[2 * n], fac[2 * n + 1]);
+            }
+#pragma unroll
+            for (int b = 0; b < kTile / 16; ++b) {
                 uint32_t pf[NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float e[4];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float m = top[2 * n + (k & 1)];
-                        e[k] = ex2(sc[b][n][k] - (m == -INFINITY ? 0.f : m) + kPShift);
-                        sum[2 * n + (k & 1)] += e[k];
+                    for (int h = 0; h < 2; ++h) {
+                        float2 e = ffma2(sc[b][n][h], f2[n], less[n]);
+                        e = make_float2(ex2(e.x), ex2(e.y));
+                        sum[n] = fadd2(sum[n], e);
+                        pf[n][h] = transpose8x8(pack_f16(e.x, e.y));
                     }
-                    pf[n][0] = transpose8x8(pack_f16(e[0], e[1]));
-                    pf[n][1] = transpose8x8(pack_f16(e[2], e[3]));
-                }
                 uint32_t vw[4][KS / 4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -521,13 +589,13 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
             }
             // ---- the slot is read: its next tile
             __syncwarp();
-            if (i + kSlots < mine) {
-                const int64_t next = tile + kSlots * W;
+            if (i + kSlots < n_tiles) {
+                const int64_t next = tile + kSlots;
                 const uint32_t h = fetch(next, next_page, slot);
 #pragma unroll
                 for (int k = 0; k < kSlots; ++k)
                     if (k == slot) halves[k] = h;
-                if (i + kSlots + 1 < mine) next_page = page_at(next + W);
+                if (i + kSlots + 1 < n_tiles) next_page = page_at(next + 1);
             }
         }
         // parities go by copies of each slot: an odd count of tiles leaves the slots apart
@@ -536,120 +604,175 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 1) kv_few_kernel(const KvAtte
             ++uses;
         }
 
-        // ---- the warps' results, joined through the slots' memory
+        // ---- the rows' results, or this piece's part of them
+        const bool begins = begin_tile == 0, ends = stop == unit_end;
+        float* partial = partial_of<R, D>(p.workspace, pieces, piece, begins ? 1 : 0);
 #pragma unroll
         for (int x = 0; x < 2 * NT; ++x) {
-            float v = sum[x];
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (g == 0) {
-                const int r = 8 * (x / 2) + 2 * c + (x & 1);
-                warp_max[warp][r] = top[x];
-                warp_sum[warp][r] = v;
-            }
-        }
-        __syncthreads();
-        float* part_o = reinterpret_cast<float*>(smem);  // [W][R][D]
+            float l = x & 1 ? sum[x / 2].y : sum[x / 2].x;
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int n = x / 2, r = 8 * n + 2 * c + (x & 1);
+            if (r >= rows) continue;
+            float v[D / 8];  // elements g D / 8 .. of the row
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < KS; ++t)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)  // row 8 n + 2 c + k, elements 2 KS g + ...: KS g' pairs
-                    *reinterpret_cast<float2*>(part_o + (warp * R + 8 * n + 2 * c + k) * D + g * (D / 8) + 2 * t) =
-                        make_float2(o[n][t][k], o[n][t][k + 2]);
-        __syncthreads();
-        const bool begins = at == unit_begin, ends = stop == unit_end;
-        float* partial = partial_of<R, D>(p.workspace, gridDim.x, blockIdx.x, begins ? 1 : 0);
-        for (int x = tid; x < rows * (D / 2); x += W * 32) {
-            const int r = x / (D / 2), d = 2 * (x - r * (D / 2));
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < W; ++w) m = fmaxf(m, warp_max[w][r]);
-            const float ref = m == -INFINITY ? 0.f : m;
-            float l = 0, v0 = 0, v1 = 0;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f = ex2(warp_max[w][r] - ref);
-                const float2 v = *reinterpret_cast<const float2*>(part_o + (w * R + r) * D + d);
-                l += f * warp_sum[w][r];
-                v0 += f * v.x;
-                v1 += f * v.y;
+            for (int t = 0; t < KS; ++t) {
+                v[2 * t] = o[n][t][x & 1];
+                v[2 * t + 1] = o[n][t][2 + (x & 1)];
             }
             if (begins && ends) {
                 int64_t token;
                 int h;
                 row_of(row0 + r, group, p.n_kv, head, token, h);
                 const float f = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + head) : 1.f) / l;
-                T* dst = static_cast<T*>(p.out) + (geo.begin + token) * p.out_stride + h * D + d;
-                dst[0] = from_f<T>(l == 0.f ? 0.f : v0 * f);
-                dst[1] = from_f<T>(l == 0.f ? 0.f : v1 * f);
-                if (p.lse && d == 0)
-                    p.lse[(geo.begin + token) * p.n_heads + h] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+                for (int t = 0; t < D / 8; ++t) v[t] = l == 0.f ? 0.f : v[t] * f;
+                T* dst = static_cast<T*>(p.out) + (geo.begin + token) * p.out_stride + h * D + g * (D / 8);
+                if (p.vector) {
+#pragma unroll
+                    for (int t = 0; t < D / 8; t += 8) {
+                        float w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = v[t + k];
+                        store_vec<T, 8>(dst + t, w);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < D / 8; ++t) dst[t] = from_f<T>(v[t]);
+                }
+                if (p.lse && g == 0)
+                    p.lse[(geo.begin + token) * p.n_heads + h] = l == 0.f ? -INFINITY : (top[x] - kPShift + log2f(l)) * 0.6931471805599453f;
             } else {
-                *reinterpret_cast<float2*>(partial + r * D + d) = make_float2(v0, v1);
-                if (d == 0) {
-                    partial[R * D + r] = m;
+#pragma unroll
+                for (int t = 0; t < D / 8; t += 2)
+                    *reinterpret_cast<float2*>(partial + r * D + g * (D / 8) + t) = make_float2(v[t], v[t + 1]);
+                if (g == 0) {
+                    partial[R * D + r] = top[x];
                     partial[R * D + R + r] = l;
                 }
             }
         }
-        if (tid == 0 && !begins && ends)
-            *join = Join{row0, geo.begin, rows, head, static_cast<int>(unit_begin / per), 0};
-        fence_async_smem();  // (the slots' next copies come behind these reads and writes)
-        __syncthreads();
+        if (lane == 0 && !begins && ends)
+            *join = Join{row0, geo.begin, rows, head, static_cast<int>((unit_begin + kUnitTiles) / per), 0};
+        __syncwarp();
         at = stop;
     }
 }
 
-// Joins the partial results of a unit that ends in CTA blockIdx.x: those of the CTA it began in
-// (its second), then the first of each that follows.
+// A running softmax sum of 4 (or 2) elements of a row.
+template <int E>
+struct Running {
+    float m, l, v[E];
+};
+template <int E>
+__device__ __forceinline__ void join_into(Running<E>& a, const Running<E>& b) {
+    const float now = fmaxf(a.m, b.m), ref = now == -INFINITY ? 0.f : now;
+    const float f = ex2(a.m - ref), h = ex2(b.m - ref);
+    a.l = f * a.l + h * b.l;
+#pragma unroll
+    for (int i = 0; i < E; ++i) a.v[i] = f * a.v[i] + h * b.v[i];
+    a.m = now;
+}
+
+// Joins the partial results of the units that end in a piece they did not begin in: those of the
+// piece it began in (its second), then the first of each that follows.  A CTA looks at pieces
+// blockIdx.x, + gridDim.x, ... and joins row blockIdx.y of theirs: of few pieces a warp alone, of
+// many all warps.
+constexpr int kJoinWarps = 8, kJoinMost = 32, kJoinFew = 8;
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(D) kv_join_kernel(const KvAttentionParams p, int ctas) {
-    constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttentionParams p, int pieces) {
+    constexpr int R = 8 * NT, E = D / 32;
+    using Sum = Running<E>;
+    __shared__ Join joins[kJoinMost];
+    __shared__ Sum sums[kJoinWarps][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Join j = static_cast<const Join*>(p.workspace)[blockIdx.x];
-    const int r = blockIdx.y, d = threadIdx.x;
-    if (r >= j.rows) return;
-    const int n = static_cast<int>(blockIdx.x) - j.first_cta + 1;
-    float m = -INFINITY, l = 0, v = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float* part = partial_of<R, D>(p.workspace, ctas, j.first_cta + i, i == 0 ? 1 : 0);
-        const float pm = part[R * D + r], pl = part[R * D + R + r], pv = part[r * D + d];
-        const float now = fmaxf(m, pm), ref = now == -INFINITY ? 0.f : now;
-        const float f = ex2(m - ref), h = ex2(pm - ref);
-        l = f * l + h * pl;
-        v = f * v + h * pv;
-        m = now;
+    // pieces [a, b) of a row, in order, 8 on their way at a time
+    auto part_of_row = [&](const Join& j, int r, int a, int b) {
+        Sum s{-INFINITY, 0.f, {}};
+        for (int x0 = a; x0 < b; x0 += 8) {
+            Sum o[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                o[x] = Sum{-INFINITY, 0.f, {}};
+                if (x0 + x < b) {
+                    const float* part = partial_of<R, D>(p.workspace, pieces, j.first_piece + x0 + x, x0 + x == 0 ? 1 : 0);
+                    o[x].m = part[R * D + r];
+                    o[x].l = part[R * D + R + r];
+#pragma unroll
+                    for (int i = 0; i < E; i += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(part + r * D + E * lane + i);
+                        o[x].v[i] = v.x, o[x].v[i + 1] = v.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) join_into(s, o[x]);
+        }
+        return s;
+    };
+    auto write_row = [&](const Join& j, int r, const Sum& s) {
+        int64_t token;
+        int h;
+        row_of(j.row + r, p.n_heads / p.n_kv, p.n_kv, j.head, token, h);
+        const float f = s.l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + j.head) : 1.f) / s.l;
+        T* dst = static_cast<T*>(p.out) + (j.begin + token) * p.out_stride + h * D + E * lane;
+#pragma unroll
+        for (int i = 0; i < E; ++i) dst[i] = from_f<T>(s.l == 0.f ? 0.f : s.v[i] * f);
+        if (p.lse && lane == 0)
+            p.lse[(j.begin + token) * p.n_heads + h] = s.l == 0.f ? -INFINITY : (s.m - kPShift + log2f(s.l)) * 0.6931471805599453f;
+    };
+    for (int first = blockIdx.x; first < pieces; first += kJoinMost * gridDim.x) {
+        __syncthreads();
+        bool many = false;
+        if (tid < kJoinMost) {
+            const int64_t piece = first + static_cast<int64_t>(tid) * gridDim.x;
+            Join j{};
+            if (piece < pieces) j = static_cast<const Join*>(p.workspace)[piece];
+            j.pad = j.rows > r ? static_cast<int>(piece) - j.first_piece + 1 : 0;  // its pieces
+            joins[tid] = j;
+            many = j.pad > kJoinFew;
+        }
+        many = __syncthreads_or(many);
+        for (int i = warp; i < kJoinMost; i += kJoinWarps) {
+            const int n = joins[i].pad;
+            if (n > 0 && n <= kJoinFew) write_row(joins[i], r, part_of_row(joins[i], r, 0, n));
+        }
+        if (!many) continue;
+        for (int i = 0; i < kJoinMost; ++i) {
+            const int n = joins[i].pad;
+            if (n <= kJoinFew) continue;
+            sums[warp][lane] = part_of_row(joins[i], r, n * warp / kJoinWarps, n * (warp + 1) / kJoinWarps);
+            __syncthreads();
+            if (warp == 0) {
+                Sum s = sums[0][lane];
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) join_into(s, sums[w][lane]);
+                write_row(joins[i], r, s);
+            }
+            __syncthreads();
+        }
     }
-    int64_t token;
-    int h;
-    row_of(j.row + r, p.n_heads / p.n_kv, p.n_kv, j.head, token, h);
-    const float f = (p.v_scale ? __ldg(p.v_scale + j.head) : 1.f) / l;
-    static_cast<T*>(p.out)[(j.begin + token) * p.out_stride + h * D + d] = from_f<T>(l == 0.f ? 0.f : v * f);
-    if (p.lse && d == 0)
-        p.lse[(j.begin + token) * p.n_heads + h] = l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * 0.6931471805599453f;
 }
 
 template <class T, int D, int NT>
 cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
-    constexpr int bytes = kWarps<NT> * kSlots * kTileBytes<D>, joined = kWarps<NT> * 8 * NT * D * 4;
-    constexpr int smem = bytes > joined ? bytes : joined;
+    constexpr int smem = kWarps * kSlots * kTileBytes<D, NT>;
+    const int ctas = sm_count * kCtasPerSm * kWaves;
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_few_kernel<T, D, NT>), smem); e != cudaSuccess) return e;
-    kv_few_kernel<T, D, NT><<<sm_count, kWarps<NT> * 32, smem, s>>>(p);
+    kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sm_count, 8 * NT);
-    cfg.blockDim = dim3(D);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, NT>, p, sm_count);
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, NT>, p, ctas * kWarps);
 }
 
 template <class T, int D>
@@ -662,7 +785,7 @@ cudaError_t by_rows(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
 }  // namespace
 
 size_t kv_few_workspace(int head_dim, int sm_count) {
-    return static_cast<size_t>(sm_count) * (sizeof(Join) + 2 * 16 * (head_dim + 2) * sizeof(float));
+    return static_cast<size_t>(sm_count) * kPiecesPerSm * (sizeof(Join) + 2 * 16 * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
