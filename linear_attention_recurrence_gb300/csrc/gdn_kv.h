@@ -54,8 +54,15 @@ struct KvAttentionParams {
     void* workspace;
     int* status;
 };
-// Up to 16 rows (tokens x heads of a group) at a time on the warps' own MMAs (gdn_kv_few.cu).
+// Sequences of at most so many rows (tokens x heads of a group) are gdn_kv_few.cu's, the others
+// gdn_kv_prompt.cu's, whatever else a call has; each launch leaves the other's alone.
+constexpr int kKvFewRows = 16;
+// On the warps' own MMAs, 8 or 16 rows at a time (gdn_kv_few.cu).
 size_t kv_few_workspace(int head_dim, int sm_count);
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s);
+// On tcgen05, 256 rows at a time (gdn_kv_prompt.cu).
+int64_t kv_prompt_ctas(int64_t T, int n_seq, int n_heads, int n_kv);  // at most so many, where no unit is split
+size_t kv_prompt_workspace(int64_t T, int n_seq, int n_heads, int n_kv, int head_dim, int sm_count);
+cudaError_t launch_kv_prompt(const KvAttentionParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace gdn

@@ -43,6 +43,9 @@ Range table_range(const KvSeqs& s) { return rows_range(s.table, s.n_seq, s.table
 size_t cache_bytes(const KvSeqs& s, int n_kv, int head_dim) {
     return static_cast<size_t>(s.n_pages) * n_kv * 2 * (static_cast<size_t>(head_dim / 2 + head_dim / kKvGroup) << s.page_log2);
 }
+// Whether some sequence of T rows in n_seq may have few rows, or many.
+bool may_have_few(int64_t T, int n_seq, int group) { return group <= kKvFewRows && (n_seq > 1 || T * group <= kKvFewRows); }
+bool may_have_prompts(int64_t T, int n_seq, int group) { return T * group > kKvFewRows; }
 // Whether every row of `e`-byte elements starts on a 16-byte boundary.
 bool rows16(const void* p, int64_t stride, int e) { return !p || (is_aligned(p, 16) && stride * e % 16 == 0); }
 }  // namespace
@@ -113,9 +116,13 @@ int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
 size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int n_heads, int n_kv_heads, int head_dim) {
     int sms = 0;
     if (T <= 0 || n_seq <= 0 || n_heads <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) ||
-        sm_count(&sms) != GDN_OK)
+        n_heads % n_kv_heads != 0 || sm_count(&sms) != GDN_OK)
         return 0;
-    return kv_few_workspace(head_dim, sms);
+    // (launches on one stream: they may use the same memory one after the other)
+    const bool few = may_have_few(T, n_seq, n_heads / n_kv_heads), prompts = may_have_prompts(T, n_seq, n_heads / n_kv_heads);
+    const size_t a = few ? kv_few_workspace(head_dim, sms) : 0;
+    const size_t b = prompts ? kv_prompt_workspace(T, n_seq, n_heads, n_kv_heads, head_dim, sms) : 0;
+    return a > b ? a : b;
 }
 
 int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t n_pages, int page_size,
@@ -160,11 +167,17 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     p.scale = scale * 1.4426950408889634f;
     p.n_heads = n_heads, p.n_kv = n_kv_heads, p.head_dim = head_dim, p.causal = causal, p.window = window, p.dtype = dtype;
     p.vector = rows16(q, q_stride, e) && rows16(out, out_stride, e);
+    if (kv_prompt_ctas(T, n_seq, n_heads, n_kv_heads) > INT32_MAX / 2) return unsupported("too many rows and heads");
     p.workspace = workspace;
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
     if (cudaError_t err = ssm_status_word(&p.status); err != cudaSuccess) return cuda_bad(err, "cache attention set-up");
-    cudaError_t err = launch_kv_few(p, sms, static_cast<cudaStream_t>(cuda_stream));
+    const int group = n_heads / n_kv_heads;
+    const bool even = !cu_seqlens, few_rows = p.s.per_seq * group <= kKvFewRows;
+    cudaError_t err = cudaSuccess;
+    if (even ? few_rows : may_have_few(T, n_seq, group)) err = launch_kv_few(p, sms, static_cast<cudaStream_t>(cuda_stream));
+    if (err == cudaSuccess && (even ? !few_rows : may_have_prompts(T, n_seq, group)))
+        err = launch_kv_prompt(p, sms, static_cast<cudaStream_t>(cuda_stream));
     if (err != cudaSuccess) return cuda_bad(err, "cache attention launch");
     internal_count_launch();
     return GDN_OK;

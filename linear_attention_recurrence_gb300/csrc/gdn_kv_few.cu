@@ -65,6 +65,8 @@ __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, 
     kv_rows(p.s, s, g.begin, e);
     g.rows = e - g.begin;
     if (g.rows == 0) return g;
+    const int group = p.n_heads / p.n_kv;
+    if (g.rows * group > kKvFewRows) return g;  // (the other kernel's)
     const int64_t len = __ldg(p.s.kv_lens + s);
     const int64_t cap = kv_capacity(p.s);
     const int64_t hi = len < cap ? (len < 0 ? 0 : len) : cap;
@@ -76,7 +78,6 @@ __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, 
     g.first = lo / tile;
     g.tiles = (hi + tile - 1) / tile - g.first;
     if (g.tiles < 1) g.tiles = 1;  // (its rows see nothing: the outputs are zeros)
-    const int group = p.n_heads / p.n_kv;
     g.blocks = (g.rows * group + R - 1) / R;
     g.cost = (g.tiles + kUnitTiles) * g.blocks * p.n_kv;
     return g;

@@ -60,6 +60,7 @@
 
 #include "gdn_ssm.cuh"
 #include "gdn_ssm.h"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace {
@@ -80,7 +81,6 @@ constexpr uint32_t TM_XW = 448;  // parts of w o x: ring of blocks of 16 tokens,
 constexpr uint32_t TM_COLS = 512;
 
 // shared memory, from a 1024-byte boundary
-constexpr uint32_t kBox = 16384;  // 128 rows x 64 elements, 128-byte swizzled
 constexpr uint32_t SM_C = 0, SM_B = 2 * kBox, SM_X = 4 * kBox, SM_STAGE = 6 * kBox;
 constexpr uint32_t SM_M = kStages * SM_STAGE;           // columns i < 64: 128 rows; i >= 64: rows 64-127
 constexpr uint32_t SM_GATE = SM_M + 24576;
@@ -140,44 +140,6 @@ struct TcParams {
     int n_heads, n_groups;
 };
 
-// ---- tcgen05, 16-bit operands ----
-__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
-    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
-           ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-// 128-byte swizzled operand whose rows are the K index (64 elements of M or N per row):
-// blocks of 64 elements kBox apart, groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t a) {
-    return static_cast<uint64_t>((a & 0x3FFFF) >> 4) | (static_cast<uint64_t>(kBox >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-// 128-byte swizzled operand whose rows are M or N (64 elements of K per row).
-__device__ __forceinline__ uint64_t desc_k(uint32_t a) {
-    return static_cast<uint64_t>((a & 0x3FFFF) >> 4) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_u16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
 // Fragments of a 16 x 16 tile, rows = columns of x (or lanes of tensor memory), columns =
 // tokens: register k of the four holds tokens 8 (k >> 1) + 2 (lane & 3), + 1 of row
 // (lane >> 2) + 8 (k & 1), 16 bits each (ldmatrix and stmatrix, transposed: in memory the
@@ -274,70 +236,10 @@ __device__ constexpr int arrivals(int b, bool out) {
     return 1;
 }
 
+using Sync = SyncOf<kDevErrTimeout>;
+
 // (out of line: its 4 uses per lane would be most of the gate warp's code)
 __device__ __noinline__ float softplus_call(float v) { return ssm_softplus(v); }
-
-struct Sync {
-    uint64_t* bar;
-    volatile int* abort_flag;
-    int* status;
-};
-// A poll suspends its thread for up to this long, so that waiting warps take few issue
-// slots from the working ones; a wait gives up after kTcPolls of them (seconds).
-constexpr uint32_t kSuspendNs = 20000, kTcPolls = 1u << 17;
-__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    return ok != 0;
-}
-// Waits for phase `n` (0, 1, ...) of a barrier.  False once some wait of the CTA gave up.
-// (All but the first poll out of line: the code of all roles has to fit the caches.)
-__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    for (uint32_t i = 0; i < kTcPolls; ++i) {
-        if (poll(bar, parity)) return true;
-        if (*abort_flag) return false;
-    }
-    *abort_flag = 1;
-    report_timeout(status);
-    return false;
-}
-__device__ __forceinline__ bool wait_phase(const Sync& s, int b, uint32_t n) {
-    return poll(&s.bar[b], n & 1) || wait_more(&s.bar[b], n & 1, s.abort_flag, s.status);
-}
-// The same for a whole warp: all lanes leave together, with one answer (the tensor-memory
-// instructions behind a wait need a converged warp).
-__device__ __forceinline__ bool wait_warp(const Sync& s, int b, uint32_t n) {
-    return __all_sync(0xffffffffu, wait_phase(s, b, n)) != 0;
-}
-// True in one lane of a converged warp.  (Not `lane == 0`: behind this predicate the compiler
-// knows one lane runs and keeps the operands of MMAs and copies in uniform registers.)
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-    return p != 0;
-}
-// Waits (with a limit) until phase n of a copy's barrier has completed, whatever else happened.
-__device__ __forceinline__ void land(uint64_t* bar, uint32_t n) {
-    for (uint32_t i = 0; i < kTcPolls && !poll(bar, n & 1); ++i) {
-    }
-}
-// Every MMA of the CTA ends before tensor memory is freed.
-__device__ __forceinline__ void finish_mma(uint64_t* bar) {
-    umma_commit(bar);
-    for (uint32_t n = 0; n < kTcPolls && !poll(bar, 0); ++n) {
-    }
-}
-// One arrival for the calling warp.
-__device__ __forceinline__ void warp_arrive(const Sync& s, int b) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&s.bar[b]);
-}
 
 // Where a lane's row of ldmatrix tile (lane >> 3) of the 16 columns from p0 and tokens 0-15
 // lies in an x tile: token 8 (tile >> 1) + (lane & 7), columns p0 + 8 (tile & 1) .. + 7.
