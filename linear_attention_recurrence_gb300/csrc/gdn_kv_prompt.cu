@@ -8,10 +8,10 @@
 // scores it came from and is the second product's operand there.  Why FP16, and why that is
 // exact for K, V and Q, is said in gdn_kv_few.cu.
 //
-// Warp roles (512 threads): warps 0-3 the softmax of tile 0, 4-7 of tile 1 (a thread a row);
-// 8-11 turn codes and scales into the operands' swizzled tiles, from registers that the next
+// Warp roles (640 threads): warps 0-3 the softmax of tile 0, 4-7 of tile 1 (a thread a row);
+// 8-15 turn codes and scales into the operands' swizzled tiles, from registers that the next
 // block's bytes already fill (K and V lie alike, a token a row: K is read with head_dim as the
-// sum, V with the tokens); 12 issues the MMAs.  While one tile's softmax runs, the other tile's
+// sum, V with the tokens); 16 and 17 issue the tiles' MMAs.  While one tile's softmax runs, the other tile's
 // products do.  A row's maximum is renewed only when a score passes it by 2^7; the row's own
 // thread then scales its part of O, which no product touches until its P is there.
 //
@@ -25,27 +25,33 @@
 namespace gdn {
 namespace {
 
-constexpr int kRows = 256, kBlock = 128;  // of a unit; tokens of a block
-constexpr int kThreads = 512;
-constexpr int kDequantWarp = 8, kMmaWarp = 12;
+constexpr int kRows = 256, kBlock = 128, kHalf = 64;  // of a unit; tokens of a block, and of a product
+constexpr int kThreads = 640;
+constexpr int kDequantWarp = 8, kMmaWarp = 16, kDequantWarps = kMmaWarp - kDequantWarp;
+// Registers of the softmax warps, those that bring K and V, and the rest: together what the
+// launch has (96 a thread).
+static_assert(256 * 128 + 256 * 88 + 128 * 48 == kThreads * 96, "registers");
 constexpr float kPShift = 8.f, kSlack = 7.f;  // as in gdn_kv_few.cu
 constexpr int kMaxSplits = 16;
 
 using Sync = SyncOf<kDevErrKv, false>;
 
-// barriers
-enum { B_K, B_V = B_K + 2, B_KFREE = B_V + 2, B_VFREE = B_KFREE + 2, B_S = B_VFREE + 2, B_P = B_S + 2, B_O = B_P + 2,
-       B_FIN = B_O + 2, NBAR };
-__device__ constexpr int arrivals(int b) {
-    if (b < B_KFREE) return 4;            // the warps that bring K and V
-    if (b >= B_P && b < B_O) return 4;    // a tile's softmax warps
-    return 1;                             // a commit
+// barriers: Q is there; K and V of a stage are; ... are read; by tile and half block: the scores are
+// there, their P is, the output's product with it is done
+enum { B_Q, B_K, B_V = B_K + 2, B_KFREE = B_V + 2, B_VFREE = B_KFREE + 2, B_S = B_VFREE + 2, B_P = B_S + 4, B_O = B_P + 4,
+       B_FIN = B_O + 4, NBAR = B_FIN + 2 };
+__device__ constexpr int arrivals(int b, int tiles) {
+    if (b == B_Q) return kDequantWarp;
+    if (b < B_KFREE) return kDequantWarps;  // the warps that bring K and V
+    if (b < B_S) return tiles;              // commits of each tile's products
+    if (b >= B_P && b < B_O) return 4;      // a tile's softmax warps
+    return 1;
 }
 
 template <int D>
 struct Smem {
     static constexpr uint32_t kTile = D / 64 * kBox;  // 128 rows
-    static constexpr uint32_t Q = 0, K = 2 * kTile, V = K + 2 * kTile, FAC = V + 2 * kTile, BAR = FAC + kRows * 4,
+    static constexpr uint32_t Q = 0, K = 2 * kTile, V = K + 2 * kTile, BAR = V + 2 * kTile,
                               MISC = BAR + NBAR * 8, TOTAL = MISC + 64;
 };
 static_assert(Smem<128>::TOTAL <= 227 * 1024, "shared memory");
@@ -69,6 +75,11 @@ __device__ __forceinline__ int64_t units_of(const KvAttentionParams& p, int s, i
 // Unit u of all sequences' units, a sequence's last (which sees most) first.
 __device__ bool find_unit(const KvAttentionParams& p, int64_t u, Unit* out, Found& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!p.s.cu) {  // sequences of the same rows
+        const int64_t rows = p.s.per_seq, each = (rows * (p.n_heads / p.n_kv) + kRows - 1) / kRows, s = u / each;
+        *out = Unit{s * rows, rows, (each - 1 - (u - s * each)) * kRows, static_cast<int>(s)};
+        return s < p.s.n_seq;
+    }
     if (tid == 0) sh.unit.s = -1;
     int64_t base = 0;
     for (int s0 = 0; s0 < p.s.n_seq; s0 += kThreads) {
@@ -134,6 +145,22 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+template <class T, int E>
+__device__ __forceinline__ void load_row(const T* p, bool vector, float (&q)[E]) {
+    if (vector) {
+#pragma unroll
+        for (int i = 0; i < E; i += 8) {
+            float v[8];
+            load_vec<T, 8>(p + i, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[i + k] = v[k];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) q[i] = to_f<T>(p[i]);
+    }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentionParams p, int splits, int64_t units) {
     using SM = Smem<D>;
@@ -148,7 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SM::MISC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SM::MISC + 8);
-    float* fac = reinterpret_cast<float*>(sm + SM::FAC);
     const Sync sy{bar, abort_flag, p.status};
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int group = p.n_heads / p.n_kv;
@@ -182,123 +208,122 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
 
     if (tid == 0) {
 #pragma unroll
-        for (int b = 0; b < NBAR; ++b) mbar_init(&bar[b], arrivals(b));
+        for (int b = 0; b < NBAR; ++b) mbar_init(&bar[b], arrivals(b, two ? 2 : 1));
         *abort_flag = 0;
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
-    // pages that are none, in this CTA's blocks (their tokens are not seen)
-    bool hole = false;
-    for (int64_t at = (static_cast<int64_t>(first) * kBlock >> p.s.page_log2) + tid;
-         at << p.s.page_log2 < (static_cast<int64_t>(first + n) * kBlock < held ? static_cast<int64_t>(first + n) * kBlock : held);
-         at += kThreads)
-        hole |= kv_page(p.s, un.s, at << p.s.page_log2) < 0;
-    // ---- Q: two threads a row
-    {
-        const int r = tid >> 1, half = tid & 1;
-        constexpr int E = D / 2;
-        const float f0 = p.scale * (p.k_scale ? __ldg(p.k_scale + head) : 1.f);
-        float q[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) q[i] = 0;
-        if (r < rows) {
-            const int64_t row = un.row0 + r, token = row / group;
-            const int h = static_cast<int>(row - token * group) * p.n_kv + head;
-            const T* src = static_cast<const T*>(p.q) + (un.begin + token) * p.q_stride + h * D + E * half;
-            if (p.vector) {
-#pragma unroll
-                for (int i = 0; i < E; i += 8) {
-                    float v[8];
-                    load_vec<T, 8>(src + i, v);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) q[i + k] = v[k];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) q[i] = to_f<T>(src[i]);
-            }
-        }
-        float up = f0 < 0 ? -1.f : 1.f, unscale = 1.f;  // (the factor of the scores is never below 0)
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            float most = 0;
-#pragma unroll
-            for (int i = 0; i < E; ++i) most = fmaxf(most, fabsf(q[i]));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            // a power of two that brings the largest to 2^13 .. 2^14
-            int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
-            e = e < -100 ? -100 : e > 127 ? 13 : e;  // (infinities and NaN as they are)
-            up *= __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
-            unscale = __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
-        }
-        unsigned char* dst = sm + SM::Q + (r / kBlock) * SM::kTile + (D == 128 ? half * kBox : 0) + (r % kBlock) * 128;
-#pragma unroll
-        for (int i = 0; i < E; i += 8) {
-            uint4 v;
-            v.x = pack_f16(q[i] * up, q[i + 1] * up);
-            v.y = pack_f16(q[i + 2] * up, q[i + 3] * up);
-            v.z = pack_f16(q[i + 4] * up, q[i + 5] * up);
-            v.w = pack_f16(q[i + 6] * up, q[i + 7] * up);
-            const int chunk = (D == 128 ? 0 : 4 * half) + i / 8;
-            *reinterpret_cast<uint4*>(dst + ((chunk ^ (r & 7)) << 4)) = v;
-        }
-        // (nor 0, which would make a NaN of a place that is not seen)
-        if (half == 0) fac[r] = fabsf(f0) * unscale < 1e-37f ? 1e-37f : fabsf(f0) * unscale;
-        fence_async_smem();
-    }
     tc_fence_before_sync();
-    const bool holes = __syncthreads_or(hole);
+    __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp < kDequantWarp) {
         // ---- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         const int t = warp >> 2, r = t * kBlock + (warp & 3) * 32 + lane;  // tile, row
-        if (t == 0 || two) {
+        if (t == 1 && !two) {
+            warp_arrive(sy, B_Q);
+        } else {
             const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const uint32_t ts = tm + lanes + TM_S + t * kBlock, to = tm + lanes + TM_O + t * D;
-            const float f = fac[r];
+            // ---- the row's queries
+            const float f0 = p.scale * (p.k_scale ? __ldg(p.k_scale + head) : 1.f);
+            float up = f0 < 0 ? -1.f : 1.f, f = fabsf(f0);  // (the factor of the scores is never below 0)
+            {
+                constexpr int E = 64;
+                const int64_t row = un.row0 + (r < rows ? r : 0), token = row / group;
+                const int h = static_cast<int>(row - token * group) * p.n_kv + head;
+                const T* src = static_cast<const T*>(p.q) + (un.begin + token) * p.q_stride + h * D;
+                float most = 0;
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+                    for (int b = 0; b < D; b += E) {
+                        float q[E];
+                        load_row<T, E>(src + b, p.vector, q);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) most = fmaxf(most, fabsf(q[i]));
+                    }
+                    // a power of two that brings the largest to 2^13 .. 2^14
+                    int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+                    e = e < -100 ? -100 : e > 127 ? 13 : e;  // (infinities and NaN as they are)
+                    up *= __uint_as_float(static_cast<uint32_t>(13 - e + 127) << 23);
+                    f *= __uint_as_float(static_cast<uint32_t>(e - 13 + 127) << 23);
+                }
+                if (r >= rows) up = 0.f;
+                unsigned char* dst = sm + SM::Q + t * SM::kTile + (r % kBlock) * 128;
+#pragma unroll
+                for (int b = 0; b < D; b += E) {
+                    float q[E];
+                    load_row<T, E>(src + b, p.vector, q);
+#pragma unroll
+                    for (int i = 0; i < E; i += 8) {
+                        uint4 v;
+                        v.x = pack_f16(q[i] * up, q[i + 1] * up);
+                        v.y = pack_f16(q[i + 2] * up, q[i + 3] * up);
+                        v.z = pack_f16(q[i + 4] * up, q[i + 5] * up);
+                        v.w = pack_f16(q[i + 6] * up, q[i + 7] * up);
+                        *reinterpret_cast<uint4*>(dst + (b / 64) * kBox + (((i / 8) ^ (r & 7)) << 4)) = v;
+                    }
+                }
+                f = f < 1e-37f ? 1e-37f : f;  // (nor 0, which would make a NaN of a place that is not seen)
+                fence_async_smem();
+                warp_arrive(sy, B_Q);
+            }
+            // pages that are none, in this CTA's blocks (their tokens are not seen)
+            const int64_t at1 = static_cast<int64_t>(first + n) * kBlock < held ? static_cast<int64_t>(first + n) * kBlock : held;
+            bool holes = false;
+            for (int64_t at = static_cast<int64_t>(first) * kBlock + (static_cast<int64_t>(lane) << p.s.page_log2); at < at1;
+                 at += int64_t{32} << p.s.page_log2)
+                holes |= kv_page(p.s, un.s, at) < 0;
+            holes = __any_sync(0xffffffffu, holes);
             const int64_t place = len - un.rows + (un.row0 + r) / group;
             int from = 0, upto = held;
             if (p.causal && place + 1 < held) upto = place + 1 > 0 ? static_cast<int>(place + 1) : 0;
             if (p.window > 0 && place - p.window + 1 > 0) from = static_cast<int>(place - p.window + 1);
             if (r >= rows) from = 0, upto = INT32_MAX;  // (never looked at)
             float top = -INFINITY;
-            float2 sum = make_float2(0, 0);
+            float2 sums[4] = {};
             bool ok = true;
-            for (int j = 0; j < n; ++j) {
-                if (!(ok = wait_warp(sy, B_S + t, j))) break;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int at = 2 * t + (i & 1);  // of the tile's two places
+                const uint32_t ps = ts + (i & 1) * kHalf;
+                if (!(ok = wait_warp(sy, B_S + at, i / 2))) break;
                 tc_fence_after_sync();
-                float s[kBlock];
-                tmem_ld64(ts, s);
-                tmem_ld64(ts + 64, s + 64);
-                const int token0 = (first + j) * kBlock;
-                if (__any_sync(0xffffffffu, token0 < from || token0 + kBlock > upto) || holes) {
+                float s[kHalf];
+                tmem_ld64(ps, s);
+                const int token0 = first * kBlock + i * kHalf;
+                if (__any_sync(0xffffffffu, token0 < from || token0 + kHalf > upto) || holes) {
 #pragma unroll
-                    for (int b = 0; b < kBlock / 16; ++b) {
+                    for (int b = 0; b < kHalf / 16; ++b) {
                         const bool there = !holes || kv_page(p.s, un.s, token0 + 16 * b) >= 0;
 #pragma unroll
-                        for (int i = 16 * b; i < 16 * b + 16; ++i)
-                            if (!there || token0 + i < from || token0 + i >= upto) s[i] = -INFINITY;
+                        for (int x = 16 * b; x < 16 * b + 16; ++x)
+                            if (!there || token0 + x < from || token0 + x >= upto) s[x] = -INFINITY;
                     }
                 }
-                float m = s[0];
+                float m4[4] = {s[0], s[1], s[2], s[3]};  // (four chains: few warps share a scheduler)
 #pragma unroll
-                for (int i = 1; i < kBlock; ++i) m = fmaxf(m, s[i]);
-                m *= f;
+                for (int x = 4; x < kHalf; x += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], x + 4 < kHalf ? fmaxf(s[x + k], s[x + 4 + k]) : s[x + k]);
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * f;
                 if (__any_sync(0xffffffffu, m > top + kSlack)) {
                     const float now = fmaxf(top, m), less = top == now ? 1.f : ex2(top - now);
                     top = now;
-                    sum = fmul2(sum, make_float2(less, less));
-                    if (j > 0) {  // (S of this block came behind O's last product)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sums[x] = fmul2(sums[x], make_float2(less, less));
+                    if (i > 0) {
+                        if (!(ok = wait_warp(sy, B_O + (at ^ 1), (i - 1) / 2))) break;
+                        tc_fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
                             tmem_ld16(to + c, o);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float2 v = fmul2(make_float2(o[i], o[i + 1]), make_float2(less, less));
-                                o[i] = v.x, o[i + 1] = v.y;
+                            for (int x = 0; x < 16; x += 2) {
+                                const float2 v = fmul2(make_float2(o[x], o[x + 1]), make_float2(less, less));
+                                o[x] = v.x, o[x + 1] = v.y;
                             }
                             tmem_st16(to + c, o);
                         }
@@ -306,24 +331,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
                 }
                 const float less = kPShift - (top == -INFINITY ? 0.f : top);
 #pragma unroll
-                for (int c = 0; c < kBlock; c += 32) {
+                for (int c = 0; c < kHalf; c += 32) {
                     uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 e = ffma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(f, f), make_float2(less, less));
+                    for (int x = 0; x < 16; ++x) {
+                        float2 e = ffma2(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), make_float2(f, f), make_float2(less, less));
                         e = make_float2(ex2(e.x), ex2(e.y));
-                        sum = fadd2(sum, e);
-                        w[i] = pack_f16(e.x, e.y);
+                        sums[x & 3] = fadd2(sums[x & 3], e);
+                        w[x] = pack_f16(e.x, e.y);
                     }
-                    tmem_st_u16(ts + c / 2, w);
+                    tmem_st_u16(ps + c / 2, w);
                 }
                 tmem_wait_st();
                 tc_fence_before_sync();
-                warp_arrive(sy, B_P + t);
+                warp_arrive(sy, B_P + at);
             }
-            if (ok && n > 0) ok = wait_warp(sy, B_O + t, n - 1);
+            if (ok && n > 0) ok = wait_warp(sy, B_O + 2 * t + 1, n - 1);
             tc_fence_after_sync();
-            const float l = sum.x + sum.y;
+            const float l = ((sums[0].x + sums[1].x) + (sums[2].x + sums[3].x)) + ((sums[0].y + sums[1].y) + (sums[2].y + sums[3].y));
             if (ok && splits > 1) {
                 float* o = reinterpret_cast<float*>(reinterpret_cast<Part*>(p.workspace) + units * p.n_kv) +
                            static_cast<int64_t>(blockIdx.x) * kPartFloats<D>;
@@ -372,25 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
         }
     } else if (warp < kMmaWarp) {
         // ---- K and V: an item is 32 codes of a token
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        constexpr int Q4 = D / 32, PER = 32 / Q4, ITEMS = kBlock / (4 * PER);  // items of a token; tokens a warp covers; items a thread
-        const int w = warp - kDequantWarp, quarter = lane % Q4, tok = w * PER + lane / Q4;  // + 4 PER i
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        constexpr int Q4 = D / 32, PER = 32 / Q4, ITEMS = kBlock / (kDequantWarps * PER);  // items of a token; tokens a warp covers; items a thread
+        const int w = warp - kDequantWarp, quarter = lane % Q4, tok = w * PER + lane / Q4;  // + kDequantWarps PER i
         const int64_t plane = kv_plane(p.s.page_log2, D);
         struct Raw {
             uint4 code[ITEMS];
             uint32_t scale[ITEMS];  // of its two groups; K: those of V in the upper half
         };
         Raw raw[2];
+        // pages of block j's tokens, looked up a block ahead
+        int32_t page[ITEMS];
+        auto look_up = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const int at = (first + j) * kBlock + tok + kDequantWarps * PER * i;
+                page[i] = at < held ? static_cast<int32_t>(kv_page(p.s, un.s, at)) : -1;
+            }
+        };
         auto fetch = [&](int j, int which, Raw& r) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const int at = (first + j) * kBlock + tok + 4 * PER * i;
-                const int64_t page = at < held ? kv_page(p.s, un.s, at) : -1;
+                const int at = (first + j) * kBlock + tok + kDequantWarps * PER * i;
                 r.code[i] = make_uint4(0, 0, 0, 0);
                 r.scale[i] = 0;
-                if (page >= 0) {
+                if (page[i] >= 0) {
                     const int in_page = at & ((1 << p.s.page_log2) - 1);
-                    const uint8_t* k = p.cache + (page * p.n_kv + head) * 2 * plane;
+                    const uint8_t* k = p.cache + (static_cast<int64_t>(page[i]) * p.n_kv + head) * 2 * plane;
                     const uint8_t* mine = k + which * plane;
                     const int64_t scales = (int64_t{D / 2} << p.s.page_log2) + in_page * (D / kKvGroup) + 2 * quarter;
                     r.code[i] = __ldg(reinterpret_cast<const uint4*>(mine + in_page * (D / 2) + 16 * quarter));
@@ -402,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
         auto put = [&](int which, const Raw& r, unsigned char* dst) {
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
-                const int token = tok + 4 * PER * i;
+                const int token = tok + kDequantWarps * PER * i;
                 uint32_t two = r.scale[i] & 0xffff;
                 if (which == 0) {
                     if (any_e4m3_nan(r.scale[i] >> 16)) two = 0x7f7f;  // a NaN scale of the token's V is one of its K
@@ -430,10 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
                 }
             }
         };
-        if (n > 0) fetch(0, 0, raw[0]);
+        if (n > 0) {
+            look_up(0);
+            fetch(0, 0, raw[0]);
+        }
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
             fetch(j, 1, raw[1]);
+            if (j + 1 < n) look_up(j + 1);
             if (j >= 2 && !wait_warp(sy, B_KFREE + st, j / 2 - 1)) break;
             put(0, raw[0], sm + SM::K + st * SM::kTile);
             fence_async_smem();
@@ -445,51 +482,50 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
             warp_arrive(sy, B_V + st);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == kMmaWarp && n > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        // a tile's products are a warp's each, so that one tile's wait for its last product (whose
+        // operand P the next scores overwrite) leaves the tensor cores the other's
+        const int t = warp - kMmaWarp;
+        if (t < (two ? 2 : 1) && n > 0) {
             if (elect_one()) {
-                constexpr uint32_t ID_S = idesc_f16(false, 128, kBlock, false, false);
+                constexpr uint32_t ID_S = idesc_f16(false, 128, kHalf, false, false);
                 constexpr uint32_t ID_O = idesc_f16(false, 128, D, false, true);  // V: N-major
                 const uint32_t sm0 = smem_addr(sm);
-                auto scores = [&](int t, int j) {
-                    const uint32_t q = sm0 + SM::Q + t * SM::kTile, k = sm0 + SM::K + (j & 1) * SM::kTile;
+                auto scores = [&](int i) {  // of half block i
+                    const uint32_t q = sm0 + SM::Q + t * SM::kTile, k = sm0 + SM::K + (i / 2 & 1) * SM::kTile + (i & 1) * (kHalf * 128);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const uint64_t dq = desc_k(q + b * kBox), dk = desc_k(k + b * kBox);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mma_ss(tm + TM_S + t * kBlock, dq + 2 * x, dk + 2 * x, ID_S, b > 0 || x > 0);
+                        for (int x = 0; x < 4; ++x)
+                            mma_ss(tm + TM_S + t * kBlock + (i & 1) * kHalf, dq + 2 * x, dk + 2 * x, ID_S, b > 0 || x > 0);
                     }
-                    umma_commit(&bar[B_S + t]);
+                    umma_commit(&bar[B_S + 2 * t + (i & 1)]);
+                    if (i & 1) umma_commit(&bar[B_KFREE + (i / 2 & 1)]);
                 };
-                auto output = [&](int t, int j) {
-                    const uint64_t dv = desc_mn(sm0 + SM::V + (j & 1) * SM::kTile);
-#pragma unroll
-                    for (int x = 0; x < kBlock / 16; ++x)
-                        mma_ts(tm + TM_O + t * D, tm + TM_S + t * kBlock + 8 * x, dv + 128 * x, ID_O, j > 0 || x > 0);
-                    umma_commit(&bar[B_O + t]);
-                };
-                const int tiles = two ? 2 : 1;
-                bool ok = wait_phase(sy, B_K, 0);
+                bool ok = wait_phase(sy, B_Q, 0) && wait_phase(sy, B_K, 0);
+                tc_fence_after_sync();
                 if (ok) {
+                    scores(0);
+                    scores(1);
+                }
+                for (int i = 0; ok && i < 2 * n; ++i) {
+                    const int at = 2 * t + (i & 1);
+                    if (!(ok = wait_phase(sy, B_V + (i / 2 & 1), i / 4) && wait_phase(sy, B_P + at, i / 2))) break;
                     tc_fence_after_sync();
-                    for (int t = 0; t < tiles; ++t) scores(t, 0);
-                    umma_commit(&bar[B_KFREE]);
+                    const uint64_t dv = desc_mn(sm0 + SM::V + (i / 2 & 1) * SM::kTile + (i & 1) * (kHalf * 128));
+#pragma unroll
+                    for (int x = 0; x < kHalf / 16; ++x)
+                        mma_ts(tm + TM_O + t * D, tm + TM_S + t * kBlock + (i & 1) * kHalf + 8 * x, dv + 128 * x, ID_O, i > 0 || x > 0);
+                    umma_commit(&bar[B_O + at]);
+                    if (i & 1) umma_commit(&bar[B_VFREE + (i / 2 & 1)]);
+                    if (i + 2 >= 2 * n) continue;
+                    // the scores after next take this half's place, once its product is done; the next are there
+                    if (!(ok = wait_phase(sy, B_K + ((i / 2 + 1) & 1), (i / 2 + 1) / 2) && wait_phase(sy, B_O + at, i / 2))) break;
+                    tc_fence_after_sync();
+                    scores(i + 2);
                 }
-                for (int j = 0; ok && j < n; ++j) {
-                    for (int t = 0; ok && t < tiles; ++t) {
-                        if (!(ok = (t > 0 || wait_phase(sy, B_V + (j & 1), j / 2)) && wait_phase(sy, B_P + t, j))) break;
-                        tc_fence_after_sync();
-                        output(t, j);
-                        if (t == tiles - 1) umma_commit(&bar[B_VFREE + (j & 1)]);
-                        if (j + 1 < n) {
-                            if (!(ok = (t > 0 || wait_phase(sy, B_K + ((j + 1) & 1), (j + 1) / 2)) && wait_phase(sy, B_O + t, j))) break;
-                            tc_fence_after_sync();
-                            scores(t, j + 1);
-                            if (t == tiles - 1) umma_commit(&bar[B_KFREE + ((j + 1) & 1)]);
-                        }
-                    }
-                }
-                finish_mma(&bar[B_FIN]);
+                finish_mma(&bar[B_FIN + t]);
             }
             __syncwarp();
         }
