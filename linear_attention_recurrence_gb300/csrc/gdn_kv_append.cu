@@ -11,8 +11,8 @@
 //
 // Quantisation has one right answer (nearest, ties to even, of the exact quotient).  The FP32
 // arithmetic is off by a few 2^-24 of the pair's size; where the two ends of its error interval
-// round to different scales or codes, the group is done again in FP64.  Ties, which 16-bit
-// values without a rotation hit often, are such places.
+// round to different scales or codes, those are decided in FP64 (one group in some thousands).
+// Ties, which 16-bit values without a rotation hit often, need none of it: see `quantise`.
 //
 // What bounds it: memory (the queries in and out are most of it).
 #include "gdn_kv.cuh"
@@ -77,6 +77,16 @@ __device__ __forceinline__ uint32_t e2m1x2(float hi, float lo) {
     return r & 0xff;
 }
 
+// 2^64 times inv_freq / 2 pi, modulo 2^64: 1 / 2 pi as the sum of two FP64 numbers, the
+// product with its rounding error.
+__device__ uint64_t turns_per_position(float inv_freq) {
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    const double x = inv_freq, p = x * kHi, e = fma(x, kHi, -p) + x * kLo;
+    const double up = (p - floor(p)) * 4294967296.0, hi = floor(up);
+    const double rest = ((up - hi) + e * 4294967296.0) * 4294967296.0;
+    return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rest));
+}
+
 // Where one group comes from, for the exact path.
 template <class T>
 struct Source {
@@ -85,6 +95,7 @@ struct Source {
     int64_t pos;
     int first, rotary, interleaved;  // rotary 0: no rotation
 };
+// Element i of the group in FP64 (the angle to 2^-64 of a turn a position).
 template <class T>
 __device__ double exact_element(const Source<T>& s, int i) {
     const int e = s.first + i;
@@ -94,47 +105,44 @@ __device__ double exact_element(const Source<T>& s, int i) {
     const int pair = s.interleaved ? e / 2 : e % half;
     const bool second = s.interleaved ? (e & 1) : e >= half;
     const double other = to_f<T>(s.row[s.interleaved ? (e ^ 1) : second ? e - half : e + half]);
-    const double angle = static_cast<double>(s.pos) * static_cast<double>(s.inv_freq[pair]);
     double sn, cs;
-    sincos(angle, &sn, &cs);
+    sincospi(static_cast<double>(static_cast<int64_t>(static_cast<uint64_t>(s.pos) * turns_per_position(s.inv_freq[pair]))) * 0x1p-63,
+             &sn, &cs);
     return second ? __dadd_rn(__dmul_rn(x, cs), __dmul_rn(other, sn)) : __dsub_rn(__dmul_rn(x, cs), __dmul_rn(other, sn));
+}
+// The group's scale byte, where `mask` has the elements that may be its largest.
+template <class T>
+__device__ __noinline__ uint32_t exact_scale(const Source<T>& s, uint32_t mask, float head_scale) {
+    double top = 0;
+    for (; mask; mask &= mask - 1) {
+        const double y = exact_element(s, __ffs(mask) - 1);
+        if (y != y) return 0x7f;
+        top = fmax(top, fabs(y));
+    }
+    const double sc = e4m3_exact(top / (6.0 * static_cast<double>(head_scale)));
+    if (sc != sc) return 0x7f;
+    if (sc < 0.015625) return static_cast<uint32_t>(sc * 512);
+    const int e = ilogb(sc);
+    return static_cast<uint32_t>((e + 7) * 8 + static_cast<int>(scalbn(sc, 3 - e)) - 8);
+}
+// `codes` with those that differ in `diff` made right.
+template <class T>
+__device__ __noinline__ uint64_t exact_codes(const Source<T>& s, uint64_t codes, uint64_t diff, float scale, float head_scale) {
+    const double by = static_cast<double>(scale) * static_cast<double>(head_scale);
+    while (diff) {
+        const int i = (__ffsll(static_cast<long long>(diff)) - 1) / 4;
+        const double y = exact_element(s, i);
+        const uint64_t c = e2m1_exact(fabs(y) / by) | (y < 0 ? 8u : 0u);
+        codes = (codes & ~(uint64_t{15} << (4 * i))) | c << (4 * i);
+        diff &= ~(uint64_t{15} << (4 * i));
+    }
+    return codes;
 }
 
 struct Held {
     uint64_t codes;
     uint32_t scale;  // e4m3
 };
-template <class T>
-__device__ __noinline__ Held quantise_exact(const Source<T>& s, float head_scale) {
-    double top = 0;
-    bool nan = false;
-    for (int i = 0; i < kKvGroup; ++i) {
-        const double y = exact_element(s, i);
-        nan |= y != y;
-        top = fmax(top, fabs(y));
-    }
-    Held h{0, 0};
-    const double hs = head_scale;
-    const double sc = e4m3_exact(top / (6.0 * hs));
-    if (nan || sc != sc) {
-        h.scale = 0x7f;
-        return h;
-    }
-    int e = 0;
-    if (sc >= 0.015625) {
-        e = ilogb(sc);
-        h.scale = static_cast<uint32_t>((e + 7) * 8 + static_cast<int>(scalbn(sc, 3 - e)) - 8);
-    } else {
-        h.scale = static_cast<uint32_t>(sc * 512);
-    }
-    for (int i = 0; i < kKvGroup; ++i) {
-        const double y = exact_element(s, i);
-        uint32_t c = sc > 0 ? e2m1_exact(fabs(y) / (sc * hs)) : 0;
-        if (y < 0 && sc > 0) c |= 8;
-        h.codes |= static_cast<uint64_t>(c) << (4 * i);
-    }
-    return h;
-}
 
 // Rounded to 17 significant bits.
 __device__ __forceinline__ float snap(float v) { return __uint_as_float((__float_as_uint(v) + 0x40) & ~0x7fu); }
@@ -162,7 +170,14 @@ __device__ __forceinline__ Held quantise(const float (&y)[kKvGroup], float err, 
     const uint32_t two = e4m3x2(a + ea, fmaxf(a - ea, 0.f));
     Held h;
     h.scale = two & 0xff;
-    bool odd = (two >> 8) != h.scale || !(a < 1e30f) || !(err < 1e30f);
+    const bool odd = !(a < 1e30f) || !(err < 1e30f);
+    if ((two >> 8) != h.scale || odd) {
+        const float least = __uint_as_float(most) - 2 * err;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < kKvGroup; ++i) mask |= odd || fabsf(y[i]) >= least ? 1u << i : 0u;
+        h.scale = exact_scale(s, mask, head_scale);
+    }
     const uint32_t sc16 = e4m3_to_f16(h.scale);
     const float sc = __half2float(__ushort_as_half(static_cast<unsigned short>(sc16 & 0xffff)));
     const float inv = sc > 0 ? __fdividef(inv_scale, sc) : 0.f;
@@ -176,9 +191,9 @@ __device__ __forceinline__ Held quantise(const float (&y)[kKvGroup], float err, 
         lo[i / 8] |= e2m1x2(w - ew, u - eu) << (4 * (i & 7));
         hi[i / 8] |= e2m1x2(w + ew, u + eu) << (4 * (i & 7));
     }
-    odd |= (lo[0] != hi[0] || lo[1] != hi[1]) && sc > 0;
     h.codes = sc > 0 ? (static_cast<uint64_t>(lo[1]) << 32 | lo[0]) : 0;
-    if (odd) h = quantise_exact(s, head_scale);
+    if ((lo[0] != hi[0] || lo[1] != hi[1]) && sc > 0)
+        h.codes = exact_codes(s, h.codes, static_cast<uint64_t>(lo[1] ^ hi[1]) << 32 | (lo[0] ^ hi[0]), sc, head_scale);
     return h;
 }
 
@@ -215,16 +230,6 @@ __device__ __forceinline__ void store_n(T* p, bool vector, const float (&f)[N]) 
     }
 }
 
-// 2^64 times inv_freq / 2 pi, modulo 2^64: 1 / 2 pi as the sum of two FP64 numbers, the
-// product with its rounding error.
-__device__ uint64_t turns_per_position(float inv_freq) {
-    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-    const double x = inv_freq, p = x * kHi, e = fma(x, kHi, -p) + x * kLo;
-    const double up = (p - floor(p)) * 4294967296.0, hi = floor(up);
-    const double rest = ((up - hi) + e * 4294967296.0) * 4294967296.0;
-    return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(rest));
-}
-
 // A CTA takes `per_cta` tokens and the units [blockIdx.y, + gridDim.y, ...) x kThreads of each.
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParams p, int per_cta) {
@@ -255,11 +260,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     for (int i = tid; i < per_cta * half; i += kThreads) {
         const int k = i / half, j = i - k * half;
         const uint64_t a = static_cast<uint64_t>(items[k].pos) * turns_per_position(__ldg(p.inv_freq + j));
-        // the nearest 32-bit fraction of a turn, in [-1/2, 1/2)
+        // the nearest 32-bit fraction of a turn, in [-1/2, 1/2), as an FP32 number and its rest
         const int32_t top = static_cast<int32_t>((a + 0x80000000ull) >> 32);
+        const float near = static_cast<float>(top);
+        const float rest = static_cast<float>(static_cast<int64_t>(top) - static_cast<int64_t>(near)) * (6.2831853f * 0x1p-32f);
         float sn, cs;
-        sincospif(static_cast<float>(top) * 0x1p-31f, &sn, &cs);
-        turn[i] = make_float2(cs, sn);
+        sincospif(near * 0x1p-31f, &sn, &cs);
+        turn[i] = make_float2(fmaf(-sn, rest, cs), fmaf(cs, rest, sn));
     }
     __syncthreads();
     constexpr int U = D / 32;  // units of a row
@@ -308,8 +315,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
                     size = fmaxf(size, fmaxf(fabsf(m) + fabsf(n), fabsf(r) + fabsf(s)));
                 }
             }
-            // sincospif is good to 2 ulp, the angle to 2^-32 of a turn, and three roundings
-            err[0] = err[1] = size * 0x1p-21f;
+            // the sine and cosine are good to 1 ulp of the function and half of one of the correction, the
+            // angle to 2^-32 of a turn; products and sum are rounded: 2^-22.5 of the pair's size
+            err[0] = err[1] = size * 0x1p-22f;
         }
         if (kind == 0) {
             T* dst = static_cast<T*>(p.q_out) + it.row * p.q_out_stride + head * D;
