@@ -7,8 +7,8 @@
 // ragged lengths fill the device evenly; a unit that several warps share leaves partial results
 // in the workspace, which a second launch joins in order of the tokens.
 //
-// A warp copies a tile's codes and scales into its own two slots of shared memory
-// (cp.async.bulk) and computes, transposed so that the few rows are the narrow side of m16n8k16
+// A warp copies a tile's codes and scales into its own two slots of shared memory (cp.async: the
+// bytes of small pages are too few for bulk copies) and computes, transposed so that the few rows are the narrow side of m16n8k16
 // products:
 //     S^T = K Q^T   (16 tokens x 8 rows, over head_dim), running maximum and sum of each row,
 //     O^T += V^T P^T   (16 of head_dim x 8 rows, over 16 tokens)
@@ -173,6 +173,15 @@ __device__ __forceinline__ float* partial_of(void* ws, int64_t pieces, int64_t p
            (piece * 2 + which) * kPartialFloats<R, D>;
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -199,21 +208,17 @@ __device__ __forceinline__ void row_of(int64_t row, int group, int n_kv, int kv_
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const KvAttentionParams p) {
     constexpr int R = 8 * NT, kTile = kTileOf<NT>;
+    constexpr int B = NT == 1 ? 2 : 1;  // sixteens of tokens that are computed at a time
     constexpr int DL = D / 4;        // elements of a token's K that a lane takes (its words: DL / 8)
     constexpr int KS = D / 16;       // k-steps of S^T, M tiles of O^T
     constexpr int kPlane = kTile * (D / 2 + D / kKvGroup);  // K's, then V's, in a tile
     constexpr int kScales = kTile * D / 2;                  // their scales within it
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Scratch scratch;
-    __shared__ uint64_t bars[kWarps * kSlots];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int group = p.n_heads / p.n_kv;
     const int64_t pieces = static_cast<int64_t>(gridDim.x) * kWarps, piece = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
 
-    if (lane == 0) {
-        for (int i = 0; i < kSlots; ++i) mbar_init(&bars[warp * kSlots + i], 1);
-    }
-    mbar_init_fence();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t total;
     const int64_t per = find_pieces(p, R, kTile, &total, scratch);
@@ -228,8 +233,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
     Geometry geo = geometry(p, s, R, kTile);
 
     unsigned char* slots = smem + warp * kSlots * kTileBytes<D, NT>;
-    uint64_t* bar = bars + warp * kSlots;
-    uint32_t uses = 0;  // copies this warp has waited for
 
     while (at < end) {
         while (at >= base + geo.cost) {  // the next sequence with rows
@@ -258,48 +261,70 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
         const int64_t cap = kv_capacity(p.s);
         const int held = static_cast<int>(len < cap ? len : cap);
 
-        // what each lane copies of a tile: its part (small pages give two or four), and which of four arrays
-        constexpr int kTileLog2 = kTile == 64 ? 6 : 5;
+        // A tile is one page's, or 2 or 4 small ones': lane i looks up part i of it.
+        constexpr int kTileLog2 = kTile == 64 ? 6 : 5, kParts = kTile / 16;
         const int part_log2 = p.s.page_log2 < kTileLog2 ? p.s.page_log2 : kTileLog2;
-        const int parts = kTile >> part_log2;
         const int64_t plane = kv_plane(p.s.page_log2, D);
-        const int part = lane >> 2, which = lane & 3;  // K codes, K scales, V codes, V scales
-        const bool is_scale = which & 1;
-        const int row_bytes = is_scale ? D / kKvGroup : D / 2;
-        auto page_at = [&](int64_t tile) -> int64_t {
-            const int64_t token = tile * kTile + (static_cast<int64_t>(part) << part_log2);
-            return part < parts && token < held ? kv_page(p.s, s, token) : -1;
+        const int64_t scales_at = int64_t{D / 2} << p.s.page_log2;
+        // the address of that part's first token of K's codes, or nullptr; its place in the page
+        auto part_at = [&](int64_t tile) -> const uint8_t* {
+            const int64_t token = tile * kTile + (static_cast<int64_t>(lane) << part_log2);
+            const int64_t page = lane < kTile >> part_log2 && token < held ? kv_page(p.s, s, token) : -1;
+            return page < 0 ? nullptr : p.cache + (page * p.n_kv + head) * 2 * plane;
         };
-        // issues the copies of a tile; returns which of its sixteen-token parts there are
-        auto fetch = [&](int64_t tile, int64_t page, int slot) -> uint32_t {
-            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && which == 0);
-            const int n = __popc(there);
-            if (lane == 0) {
-                if (n)
-                    mbar_arrive_expect_tx(&bar[slot], n * 2 * ((D / 2 + D / kKvGroup) << part_log2));
-                else
-                    mbar_arrive(&bar[slot]);
+        // starts a tile's copies, 16 bytes a lane at a time; returns which of its sixteens of tokens there are
+        auto fetch = [&](int64_t tile, const uint8_t* mine, int slot) -> uint32_t {
+            const uint32_t parts = __ballot_sync(0xffffffffu, mine != nullptr);
+            unsigned char* dst = slots + slot * kTileBytes<D, NT> + 16 * lane;
+            const int in_page = static_cast<int>(tile * kTile) & ((1 << p.s.page_log2) - 1);
+            constexpr int TPI = 1024 / D, TPL = 256 / D;  // tokens of a warp's 512 bytes of codes; of a lane's 16 of scales
+            if (part_log2 == kTileLog2) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), 0));
+                if (src) {
+                    const uint8_t* codes = src + in_page * (D / 2) + 16 * lane;
+                    const uint8_t* scales = src + scales_at + in_page * (D / kKvGroup) + 16 * lane;
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+                        for (int i = 0; i < kTile / TPI; ++i) cp_async16(dst + which * kPlane + 512 * i, codes + which * plane + 512 * i);
+                        if (lane < kTile / TPL) cp_async16(dst + which * kPlane + kScales, scales + which * plane);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTile / TPI; ++i) {
+                    const int part = (i * TPI) >> part_log2;
+                    const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), part));
+                    if (src) {
+                        src += (i * TPI - (part << part_log2)) * (D / 2) + 16 * lane;
+#pragma unroll
+                        for (int which = 0; which < 2; ++which) cp_async16(dst + which * kPlane + 512 * i, src + which * plane);
+                    }
+                }
+                const int token = (lane % (kTile / TPL)) * TPL, part = token >> part_log2;
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), part));
+                if (src && lane < kTile / TPL) {
+                    src += scales_at + (token - (part << part_log2)) * (D / kKvGroup);
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) cp_async16(dst + which * kPlane + kScales, src + which * plane);
+                }
             }
-            __syncwarp();
-            if (page >= 0) {
-                const int64_t token = tile * kTile + (static_cast<int64_t>(part) << part_log2);
-                const int64_t in_page = token & ((int64_t{1} << p.s.page_log2) - 1);
-                const uint8_t* src = p.cache + ((page * p.n_kv + head) * 2 + (which >> 1)) * plane +
-                                     (is_scale ? (int64_t{D / 2} << p.s.page_log2) : 0) + in_page * row_bytes;
-                unsigned char* dst = slots + slot * kTileBytes<D, NT> + (which >> 1) * kPlane + (is_scale ? kScales : 0) +
-                                     (part << part_log2) * row_bytes;
-                bulk_load(dst, src, row_bytes << part_log2, &bar[slot]);
+            uint32_t there = parts;
+            if (part_log2 > 4) {
+                there = 0;
+#pragma unroll
+                for (int b = 0; b < kParts; ++b) there |= (parts >> ((16 * b) >> part_log2) & 1) << b;
             }
-            // (bit 4 i: part i; a part of 32 or 64 tokens is two or four sixteenths)
-            const uint32_t first = part_log2 == 4 ? there : part_log2 == 5 ? (there & 1) * 0x11 | (there >> 4 & 1) * 0x1100
-                                                                          : (there & 1) * 0x1111;
-            return (first & 1) | (first >> 3 & 2) | (first >> 6 & 4) | (first >> 9 & 8);
+            return there;
         };
         uint32_t halves[kSlots];
-        int64_t next_page = -1;
+        const uint8_t* next_part = nullptr;
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) halves[i] = i < n_tiles ? fetch(tile0 + i, page_at(tile0 + i), i) : 0;
-        if (n_tiles > kSlots) next_page = page_at(tile0 + kSlots);
+        for (int i = 0; i < kSlots; ++i) {
+            halves[i] = i < n_tiles ? fetch(tile0 + i, part_at(tile0 + i), i) : 0;
+            cp_async_commit();
+        }
+        if (n_tiles > kSlots) next_part = part_at(tile0 + kSlots);
 
         // the rows' queries (row 8 n + g, its elements DL c ..), scaled; and what each lane's
         // columns 8 n + 2 c, + 1 of S^T see: tokens [from, to)
@@ -369,7 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
         }
 
         float o[NT][KS][4];
-        float top[2 * NT];
+        float top[2 * NT], less[2 * NT];
         float2 sum[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -378,6 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[n][t][k] = 0;
             top[2 * n] = top[2 * n + 1] = -INFINITY;
+            less[2 * n] = less[2 * n + 1] = kPShift;
             sum[n] = make_float2(0, 0);
         }
         // tokens that all the lane's columns see
@@ -392,12 +418,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
         for (int i = 0; i < n_tiles; ++i) {
             const int slot = i % kSlots;
             const int64_t tile = tile0 + i;
-            if (!mbar_wait(&bar[slot], (uses / kSlots) & 1)) {
-                report_error(p.status, kDevErrKv);
-                mbar_wait(&bar[slot], (uses / kSlots) & 1);  // the copy lands before the warp can leave
-            }
+            cp_async_wait<kSlots - 1>();
             __syncwarp();
-            ++uses;
             const unsigned char* kc = slots + slot * kTileBytes<D, NT>;
             const unsigned char* vc = kc + kPlane;
             const uint32_t there = halves[slot];
@@ -405,186 +427,189 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
             const bool whole = there == (1u << kTile / 16) - 1 && token0 >= all_from && token0 + kTile <= all_to;
             // the lane's tokens of V: pairs (2 c, 2 c + 1), the odd lanes' swapped, and 8 behind
             const int t0 = 2 * c + (c & 1), t1 = 2 * c + 1 - (c & 1);
-            uint32_t vs[kTile / 16];  // V's scales of the lane's 4 tokens of each 16
-            uint32_t nan = 0;
+#pragma unroll 1
+            for (int at16 = 0; at16 < kTile / 16; at16 += B) {  // B times 16 tokens
+                const unsigned char* k16 = kc + 16 * at16 * (D / 2);
+                const unsigned char* v16 = vc + 16 * at16 * (D / 2);
+                const unsigned char* ks16 = kc + kScales + 16 * at16 * (D / kKvGroup);
+                const unsigned char* vs16 = vc + kScales + 16 * at16 * (D / kKvGroup);
+                const uint32_t there16 = there >> at16;
+                uint32_t vs[B];  // V's scales of the lane's 4 tokens of each 16
+                uint32_t nan = 0;
 #pragma unroll
-            for (int b = 0; b < kTile / 16; ++b) {
-                const unsigned char* at_s = vc + kScales + 16 * b * (D / kKvGroup) + (g * KS >> 3);
-                vs[b] = at_s[t0 * (D / kKvGroup)] | at_s[t1 * (D / kKvGroup)] << 8 |
-                        at_s[(t0 + 8) * (D / kKvGroup)] << 16 | static_cast<uint32_t>(at_s[(t1 + 8) * (D / kKvGroup)]) << 24;
-                nan |= (vs[b] & 0x7f7f7f7fu) + 0x01010101u;
-            }
-            const bool odd = __any_sync(0xffffffffu, (nan & 0x80808080u) || !whole);
-            float2 sc[kTile / 16][NT][2];  // S^T: [token row g, + 8], columns 2 c, 2 c + 1
-#pragma unroll
-            for (int b = 0; b < kTile / 16; ++b) {
-                // ---- S^T: tokens 16 b + pg, + 8
-                uint32_t kw[2][DL / 8], ks[2][DL / 16];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int tok = 16 * b + 8 * h + pg;
-                    const unsigned char* at_k = kc + tok * (D / 2) + c * (DL / 2);
-                    uint32_t two;
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(at_k);
-                        kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
-                        two = *reinterpret_cast<const uint16_t*>(kc + kScales + tok * (D / kKvGroup) + 2 * c);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(at_k);
-                        kw[h][0] = v.x, kw[h][1] = v.y;
-                        two = kc[kScales + tok * (D / kKvGroup) + c];
-                    }
-                    if (odd) {  // a NaN scale of the token's V is one of its K
-                        const unsigned char* at_v = vc + kScales + tok * (D / kKvGroup) + c * (DL / 16);
-                        uint32_t v = at_v[0];
-                        if (D == 128) v |= at_v[1] << 8;
-                        if (any_e4m3_nan(v)) two = 0x7f7f;
-                    }
-                    const uint32_t f = e4m3_to_f16(two);
-                    ks[h][0] = __byte_perm(f, f, 0x1010);
-                    if constexpr (D == 128) ks[h][1] = __byte_perm(f, f, 0x3232);
+                for (int b = 0; b < B; ++b) {
+                    const unsigned char* at_s = vs16 + 16 * b * (D / kKvGroup) + (g * KS >> 3);
+                    vs[b] = at_s[t0 * (D / kKvGroup)] | at_s[t1 * (D / kKvGroup)] << 8 |
+                            at_s[(t0 + 8) * (D / kKvGroup)] << 16 | static_cast<uint32_t>(at_s[(t1 + 8) * (D / kKvGroup)]) << 24;
+                    nan |= (vs[b] & 0x7f7f7f7fu) + 0x01010101u;
                 }
-                float acc[NT][4], acc2[NT][4];  // two chains, so that products wait less for one another
+                const bool odd = __any_sync(0xffffffffu, (nan & 0x80808080u) || !whole);
+                const int token16 = token0 + 16 * at16;
+                float2 sc[B][NT][2];  // S^T: [token row g, + 8], columns 2 c, 2 c + 1
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int b = 0; b < B; ++b) {
+                    // ---- S^T: tokens 16 b + pg, + 8
+                    uint32_t kw[2][DL / 8], ks[2][DL / 16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[n][k] = acc2[n][k] = 0;
-#pragma unroll
-                for (int w = 0; w < DL / 8; ++w) {  // 8 codes: two k-steps
-                    uint32_t f0[4], f1[4];
-                    e2m1_to_f16(kw[0][w], f0);
-                    e2m1_to_f16(kw[1][w], f1);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f0[k] = hmul2(f0[k], ks[0][w / 2]);
-                        f1[k] = hmul2(f1[k], ks[1][w / 2]);
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = 16 * b + 8 * h + pg;
+                        const unsigned char* at_k = k16 + tok * (D / 2) + c * (DL / 2);
+                        uint32_t two;
+                        if constexpr (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(at_k);
+                            kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
+                            two = *reinterpret_cast<const uint16_t*>(ks16 + tok * (D / kKvGroup) + 2 * c);
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(at_k);
+                            kw[h][0] = v.x, kw[h][1] = v.y;
+                            two = ks16[tok * (D / kKvGroup) + c];
+                        }
+                        if (odd) {  // a NaN scale of the token's V is one of its K
+                            const unsigned char* at_v = vs16 + tok * (D / kKvGroup) + c * (DL / 16);
+                            uint32_t v = at_v[0];
+                            if (D == 128) v |= at_v[1] << 8;
+                            if (any_e4m3_nan(v)) two = 0x7f7f;
+                        }
+                        const uint32_t f = e4m3_to_f16(two);
+                        ks[h][0] = __byte_perm(f, f, 0x1010);
+                        if constexpr (D == 128) ks[h][1] = __byte_perm(f, f, 0x3232);
                     }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t a[4] = {f0[2 * k], f1[2 * k], f0[2 * k + 1], f1[2 * k + 1]};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16816(k ? acc2[n] : acc[n], a, qf[n][4 * w + 2 * k], qf[n][4 * w + 2 * k + 1]);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[n][k] += acc2[n][k];
-                if (odd) {
+                    float acc[NT][4], acc2[NT][4];  // two chains, so that products wait less for one another
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[n][k] = acc2[n][k] = 0;
+#pragma unroll
+                    for (int w = 0; w < DL / 8; ++w) {  // 8 codes: two k-steps
+                        uint32_t f0[4], f1[4];
+                        e2m1_to_f16(kw[0][w], f0);
+                        e2m1_to_f16(kw[1][w], f1);
+#pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int tok = token0 + 16 * b + 8 * (k >> 1) + pg;
-                            if (!(there >> b & 1) || tok < from[2 * n + (k & 1)] || tok >= to[2 * n + (k & 1)])
-                                acc[n][k] = -INFINITY;
+                            f0[k] = hmul2(f0[k], ks[0][w / 2]);
+                            f1[k] = hmul2(f1[k], ks[1][w / 2]);
                         }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t a[4] = {f0[2 * k], f1[2 * k], f0[2 * k + 1], f1[2 * k + 1]};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma16816(k ? acc2[n] : acc[n], a, qf[n][4 * w + 2 * k], qf[n][4 * w + 2 * k + 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[n][k] += acc2[n][k];
+                    if (odd) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int tok = token16 + 16 * b + 8 * (k >> 1) + pg;
+                                if (!(there16 >> b & 1) || tok < from[2 * n + (k & 1)] || tok >= to[2 * n + (k & 1)])
+                                    acc[n][k] = -INFINITY;
+                            }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sc[b][n][0] = make_float2(acc[n][0], acc[n][1]);
+                        sc[b][n][1] = make_float2(acc[n][2], acc[n][3]);
+                    }
                 }
+                // ---- the rows' maxima, where a score passes one by far; what was summed up shrinks
+                bool past = false;
+                float most[2 * NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sc[b][n][0] = make_float2(acc[n][0], acc[n][1]);
-                    sc[b][n][1] = make_float2(acc[n][2], acc[n][3]);
-                }
-            }
-            // ---- the rows' maxima, where a score passes one by far; what was summed up shrinks
-            bool past = false;
-            float most[2 * NT];
+                    float m0 = sc[0][n][0].x, m1 = sc[0][n][0].y;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float m0 = sc[0][n][0].x, m1 = sc[0][n][0].y;
-#pragma unroll
-                for (int x = 1; x < kTile / 8; ++x) {
-                    m0 = fmaxf(m0, sc[x / 2][n][x & 1].x);
-                    m1 = fmaxf(m1, sc[x / 2][n][x & 1].y);
-                }
-                most[2 * n] = m0 * fac[2 * n];
-                most[2 * n + 1] = m1 * fac[2 * n + 1];
-                past |= most[2 * n] > top[2 * n] + kSlack || most[2 * n + 1] > top[2 * n + 1] + kSlack;
-            }
-            if (__any_sync(0xffffffffu, past)) {
-#pragma unroll
-                for (int x = 0; x < 2 * NT; ++x) {
-                    float m = most[x];
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    const float now = fmaxf(top[x], m);
-                    most[x] = top[x] == now ? 1.f : ex2(top[x] - now);
-                    top[x] = now;
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sum[n].x *= most[2 * n];
-                    sum[n].y *= most[2 * n + 1];
-#pragma unroll
-                    for (int t = 0; t < KS; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[n][t][k] *= most[2 * n + (k & 1)];
-                }
-            }
-            // ---- O^T += V^T P^T
-            float2 less[NT], f2[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                less[n] = make_float2(kPShift - (top[2 * n] == -INFINITY ? 0.f : top[2 * n]),
-                                      kPShift - (top[2 * n + 1] == -INFINITY ? 0.f : top[2 * n + 1]));
-                f2[n] = make_float2(fac[2 * n], fac[2 * n + 1]);
-            }
-#pragma unroll
-            for (int b = 0; b < kTile / 16; ++b) {
-                uint32_t pf[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float2 e = ffma2(sc[b][n][h], f2[n], less[n]);
-                        e = make_float2(ex2(e.x), ex2(e.y));
-                        sum[n] = fadd2(sum[n], e);
-                        pf[n][h] = transpose8x8(pack_f16(e.x, e.y));
+                    for (int x = 1; x < 2 * B; ++x) {
+                        m0 = fmaxf(m0, sc[x / 2][n][x & 1].x);
+                        m1 = fmaxf(m1, sc[x / 2][n][x & 1].y);
                     }
-                uint32_t vw[4][KS / 4];
+                    most[2 * n] = m0 * fac[2 * n];
+                    most[2 * n + 1] = m1 * fac[2 * n + 1];
+                    past |= most[2 * n] > top[2 * n] + kSlack || most[2 * n + 1] > top[2 * n + 1] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int tok = 16 * b + (k & 1 ? t1 : t0) + 8 * (k >> 1);
-                    const unsigned char* at_v = vc + tok * (D / 2) + g * KS;
-                    if constexpr (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(at_v);
-                        vw[k][0] = v.x, vw[k][1] = v.y;
-                    } else {
-                        vw[k][0] = *reinterpret_cast<const uint32_t*>(at_v);
+                    for (int x = 0; x < 2 * NT; ++x) {
+                        float m = most[x];
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        const float now = fmaxf(top[x], m);
+                        most[x] = top[x] == now ? 1.f : ex2(top[x] - now);
+                        top[x] = now;
+                        less[x] = kPShift - (now == -INFINITY ? 0.f : now);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sum[n].x *= most[2 * n];
+                        sum[n].y *= most[2 * n + 1];
+#pragma unroll
+                        for (int t = 0; t < KS; ++t)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[n][t][k] *= most[2 * n + (k & 1)];
                     }
                 }
-                uint32_t s0 = vs[b] & 0xffff, s1 = vs[b] >> 16;
-                if (odd) {  // what no row sees, or holds a NaN, counts as 0
-                    uint32_t keep = 0;
+                // ---- O^T += V^T P^T
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float2 e = ffma2(sc[b][n][h], make_float2(fac[2 * n], fac[2 * n + 1]), make_float2(less[2 * n], less[2 * n + 1]));
+                            e = make_float2(ex2(e.x), ex2(e.y));
+                            sum[n] = fadd2(sum[n], e);
+                            pf[n][h] = transpose8x8(pack_f16(e.x, e.y));
+                        }
+                    uint32_t vw[4][KS / 4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int tok = token0 + 16 * b + (k & 1 ? t1 : t0) + 8 * (k >> 1);
-                        if ((there >> b & 1) && tok < held && !any_e4m3_nan(vs[b] >> (8 * k) & 0xff)) keep |= 0xffu << (8 * k);
+                        const int tok = 16 * b + (k & 1 ? t1 : t0) + 8 * (k >> 1);
+                        const unsigned char* at_v = v16 + tok * (D / 2) + g * KS;
+                        if constexpr (D == 128) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(at_v);
+                            vw[k][0] = v.x, vw[k][1] = v.y;
+                        } else {
+                            vw[k][0] = *reinterpret_cast<const uint32_t*>(at_v);
+                        }
                     }
-                    s0 &= keep & 0xffff;
-                    s1 &= keep >> 16;
-                }
-                s0 = e4m3_to_f16(s0);
-                s1 = e4m3_to_f16(s1);
+                    uint32_t s0 = vs[b] & 0xffff, s1 = vs[b] >> 16;
+                    if (odd) {  // what no row sees, or holds a NaN, counts as 0
+                        uint32_t keep = 0;
 #pragma unroll
-                for (int w = 0; w < KS / 4; ++w) {
-                    // bytes of two tokens' codes of one element
-                    const uint32_t lo0 = (vw[0][w] & 0x0f0f0f0fu) | ((vw[1][w] << 4) & 0xf0f0f0f0u);
-                    const uint32_t hi0 = ((vw[0][w] >> 4) & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u);
-                    const uint32_t lo1 = (vw[2][w] & 0x0f0f0f0fu) | ((vw[3][w] << 4) & 0xf0f0f0f0u);
-                    const uint32_t hi1 = ((vw[2][w] >> 4) & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u);
-                    uint32_t a0[4], a1[4], a2[4], a3[4];
-                    e2m1_to_f16(lo0, a0);
-                    e2m1_to_f16(hi0, a1);
-                    e2m1_to_f16(lo1, a2);
-                    e2m1_to_f16(hi1, a3);
+                        for (int k = 0; k < 4; ++k) {
+                            const int tok = token16 + 16 * b + (k & 1 ? t1 : t0) + 8 * (k >> 1);
+                            if ((there16 >> b & 1) && tok < held && !any_e4m3_nan(vs[b] >> (8 * k) & 0xff)) keep |= 0xffu << (8 * k);
+                        }
+                        s0 &= keep & 0xffff;
+                        s1 &= keep >> 16;
+                    }
+                    s0 = e4m3_to_f16(s0);
+                    s1 = e4m3_to_f16(s1);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a[4] = {hmul2(a0[k], s0), hmul2(a1[k], s0), hmul2(a2[k], s1), hmul2(a3[k], s1)};
+                    for (int w = 0; w < KS / 4; ++w) {
+                        // bytes of two tokens' codes of one element
+                        const uint32_t lo0 = (vw[0][w] & 0x0f0f0f0fu) | ((vw[1][w] << 4) & 0xf0f0f0f0u);
+                        const uint32_t hi0 = ((vw[0][w] >> 4) & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u);
+                        const uint32_t lo1 = (vw[2][w] & 0x0f0f0f0fu) | ((vw[3][w] << 4) & 0xf0f0f0f0u);
+                        const uint32_t hi1 = ((vw[2][w] >> 4) & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u);
+                        uint32_t a0[4], a1[4], a2[4], a3[4];
+                        e2m1_to_f16(lo0, a0);
+                        e2m1_to_f16(hi0, a1);
+                        e2m1_to_f16(lo1, a2);
+                        e2m1_to_f16(hi1, a3);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[n][4 * w + k], a, pf[n][0], pf[n][1]);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a[4] = {hmul2(a0[k], s0), hmul2(a1[k], s0), hmul2(a2[k], s1), hmul2(a3[k], s1)};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma16816(o[n][4 * w + k], a, pf[n][0], pf[n][1]);
+                        }
                     }
                 }
             }
@@ -592,17 +617,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
             __syncwarp();
             if (i + kSlots < n_tiles) {
                 const int64_t next = tile + kSlots;
-                const uint32_t h = fetch(next, next_page, slot);
+                const uint32_t h = fetch(next, next_part, slot);
 #pragma unroll
                 for (int k = 0; k < kSlots; ++k)
                     if (k == slot) halves[k] = h;
-                if (i + kSlots + 1 < n_tiles) next_page = page_at(next + 1);
+                if (i + kSlots + 1 < n_tiles) next_part = part_at(next + 1);
             }
-        }
-        // parities go by copies of each slot: an odd count of tiles leaves the slots apart
-        if (uses % kSlots) {
-            if (lane == 0) mbar_arrive(&bar[uses % kSlots]);
-            ++uses;
+            cp_async_commit();
         }
 
         // ---- the rows' results, or this piece's part of them
@@ -682,7 +703,7 @@ __device__ __forceinline__ void join_into(Running<E>& a, const Running<E>& b) {
 // many all warps.
 constexpr int kJoinWarps = 8, kJoinMost = 32, kJoinFew = 8;
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttentionParams p, int pieces) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAttentionParams p, int pieces) {
     constexpr int R = 8 * NT, E = D / 32;
     using Sum = Running<E>;
     __shared__ Join joins[kJoinMost];
@@ -765,7 +786,9 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sm_count, 8 * NT);
+    // (a row of the grid for each row that a unit may have)
+    const int64_t rows = p.s.cu ? 8 * NT : p.s.per_seq * (p.n_heads / p.n_kv);
+    cfg.gridDim = dim3(sm_count, static_cast<unsigned>(rows < 8 * NT ? rows : 8 * NT));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr;
