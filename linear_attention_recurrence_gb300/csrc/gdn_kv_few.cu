@@ -443,8 +443,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
                             at_s[(t0 + 8) * (D / kKvGroup)] << 16 | static_cast<uint32_t>(at_s[(t1 + 8) * (D / kKvGroup)]) << 24;
                     nan |= (vs[b] & 0x7f7f7f7fu) + 0x01010101u;
                 }
-                const bool odd = __any_sync(0xffffffffu, (nan & 0x80808080u) || !whole);
+                const bool odd = __any_sync(0xffffffffu, (nan & 0x80808080u) || !whole);  // not all seen by all, or a NaN
                 const int token16 = token0 + 16 * at16;
+                // (two copies of the code: branches within would keep instructions of different sixteens apart)
+                auto step = [&](auto odd_tag) {
+                constexpr bool odd = decltype(odd_tag)::value;
                 float2 sc[B][NT][2];  // S^T: [token row g, + 8], columns 2 c, 2 c + 1
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
                             kw[h][0] = v.x, kw[h][1] = v.y;
                             two = ks16[tok * (D / kKvGroup) + c];
                         }
-                        if (odd) {  // a NaN scale of the token's V is one of its K
+                        if constexpr (odd) {  // a NaN scale of the token's V is one of its K
                             const unsigned char* at_v = vs16 + tok * (D / kKvGroup) + c * (DL / 16);
                             uint32_t v = at_v[0];
                             if (D == 128) v |= at_v[1] << 8;
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) acc[n][k] += acc2[n][k];
-                    if (odd) {
+                    if constexpr (odd) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
                         }
                     }
                     uint32_t s0 = vs[b] & 0xffff, s1 = vs[b] >> 16;
-                    if (odd) {  // what no row sees, or holds a NaN, counts as 0
+                    if constexpr (odd) {  // what no row sees, or holds a NaN, counts as 0
                         uint32_t keep = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -612,6 +615,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const K
                         }
                     }
                 }
+                };
+                if (odd)
+                    step(std::true_type{});
+                else
+                    step(std::false_type{});
             }
             // ---- the slot is read: its next tile
             __syncwarp();
