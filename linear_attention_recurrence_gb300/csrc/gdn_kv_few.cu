@@ -32,22 +32,24 @@ namespace gdn {
 namespace {
 
 constexpr int kSlots = 2;    // tiles in shared memory a warp
-constexpr int kUnitTiles = 1;  // what a unit's start and end count for, in tiles
+constexpr int kUnitTiles = 2;  // what a unit's start and end count for, in tiles
 // A row's maximum is renewed only once a score passes it by more than 2^kSlack: probabilities,
 // times 2^kPShift, stay below 2^(kPShift + kSlack) (FP16 ends at 2^16).
 constexpr float kPShift = 8.f, kSlack = 7.f;
 
 // Warps are apart from one another: a unit's start (its lengths, pages and queries, one load after
 // the other) and its end overlap with the other warps' work.  CTAs are only what they come in.
-constexpr int kWarps = 4, kCtasPerSm = 3;
+constexpr int kWarps = 4;
+template <int NT>
+constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 // Where there is enough to do, pieces a warp of the resident ones: CTAs that end early make room.
 constexpr int kWaves = 2;
-constexpr int kPiecesPerSm = kWarps * kCtasPerSm * kWaves;
+constexpr int kPiecesPerSm = kWarps * kCtasPerSm<1> * kWaves;  // at most
 // Tiles of a piece: a wave's share at most, down to kMinTiles, and no fewer than the waves leave.
-constexpr int kMinTiles = 2, kSmallPiece = 8;
+constexpr int kMinTiles = 2, kSmallPiece = 16;
 
 template <int NT>
-constexpr int kTileOf = NT == 1 ? 64 : 32;
+constexpr int kTileOf = 64;
 template <int D, int NT>
 constexpr int kTileBytes = 2 * kTileOf<NT> * (D / 2 + D / kKvGroup);
 
@@ -206,9 +208,9 @@ __device__ __forceinline__ void row_of(int64_t row, int group, int n_kv, int kv_
 }
 
 template <class T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_few_kernel(const KvAttentionParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(const KvAttentionParams p) {
     constexpr int R = 8 * NT, kTile = kTileOf<NT>;
-    constexpr int B = NT == 1 ? 2 : 1;  // sixteens of tokens that are computed at a time
+    constexpr int B = 2;  // sixteens of tokens that are computed at a time
     constexpr int DL = D / 4;        // elements of a token's K that a lane takes (its words: DL / 8)
     constexpr int KS = D / 16;       // k-steps of S^T, M tiles of O^T
     constexpr int kPlane = kTile * (D / 2 + D / kKvGroup);  // K's, then V's, in a tile
@@ -709,7 +711,7 @@ __device__ __forceinline__ void join_into(Running<E>& a, const Running<E>& b) {
 // piece it began in (its second), then the first of each that follows.  A CTA looks at pieces
 // blockIdx.x, + gridDim.x, ... and joins row blockIdx.y of theirs: of few pieces a warp alone, of
 // many all warps.
-constexpr int kJoinWarps = 8, kJoinMost = 32, kJoinFew = 8;
+constexpr int kJoinWarps = 8, kJoinMost = 32, kJoinFew = 32;
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAttentionParams p, int pieces) {
     constexpr int R = 8 * NT, E = D / 32;
@@ -718,27 +720,52 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAtt
     __shared__ Sum sums[kJoinWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // pieces [a, b) of a row, in order, 8 on their way at a time
+    // pieces [a, b) of a row: their maxima and sums a lane each, then their elements in order
     auto part_of_row = [&](const Join& j, int r, int a, int b) {
         Sum s{-INFINITY, 0.f, {}};
-        for (int x0 = a; x0 < b; x0 += 8) {
-            Sum o[8];
+        for (int x0 = a; x0 < b; x0 += 32) {
+            const int n = b - x0 < 32 ? b - x0 : 32;
+            const float* first = partial_of<R, D>(p.workspace, pieces, j.first_piece + x0, 0);
+            constexpr int64_t kNext = 2 * kPartialFloats<R, D>;
+            const int second = x0 == 0 ? kPartialFloats<R, D> : 0;  // (of the piece that the unit began in)
+            float pm = -INFINITY, pl = 0;
+            if (lane < n) {
+                const float* mine = first + lane * kNext + (lane == 0 ? second : 0) + R * D + r;
+                pm = mine[0];
+                pl = mine[R];
+            }
+            Sum o{pm, 0.f, {}};
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                o[x] = Sum{-INFINITY, 0.f, {}};
-                if (x0 + x < b) {
-                    const float* part = partial_of<R, D>(p.workspace, pieces, j.first_piece + x0 + x, x0 + x == 0 ? 1 : 0);
-                    o[x].m = part[R * D + r];
-                    o[x].l = part[R * D + R + r];
+            for (int off = 16; off > 0; off >>= 1) o.m = fmaxf(o.m, __shfl_xor_sync(0xffffffffu, o.m, off));
+            const float w = ex2(pm - (o.m == -INFINITY ? 0.f : o.m));
+            o.l = w * pl;
 #pragma unroll
-                    for (int i = 0; i < E; i += 2) {
-                        const float2 v = *reinterpret_cast<const float2*>(part + r * D + E * lane + i);
-                        o[x].v[i] = v.x, o[x].v[i + 1] = v.y;
+            for (int off = 16; off > 0; off >>= 1) o.l += __shfl_xor_sync(0xffffffffu, o.l, off);
+            for (int x = 0; x < n; x += 8) {
+                float2 v[8][E / 2];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float* mine = first + (x + k) * kNext + (x + k == 0 ? second : 0) + r * D + E * lane;
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i)
+                        v[k][i] = x + k < n ? *reinterpret_cast<const float2*>(mine + 2 * i) : make_float2(0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, w, (x + k) & 31);
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) {
+                        if (x + k < n) {
+                            o.v[2 * i] = fmaf(f, v[k][i].x, o.v[2 * i]);
+                            o.v[2 * i + 1] = fmaf(f, v[k][i].y, o.v[2 * i + 1]);
+                        }
                     }
                 }
             }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) join_into(s, o[x]);
+            if (x0 == a)
+                s = o;
+            else
+                join_into(s, o);
         }
         return s;
     };
@@ -789,7 +816,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAtt
 template <class T, int D, int NT>
 cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     constexpr int smem = kWarps * kSlots * kTileBytes<D, NT>;
-    const int ctas = sm_count * kCtasPerSm * kWaves;
+    const int ctas = sm_count * kCtasPerSm<NT> * kWaves;
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_few_kernel<T, D, NT>), smem); e != cudaSuccess) return e;
     kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
