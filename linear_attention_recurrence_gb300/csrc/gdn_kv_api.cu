@@ -43,9 +43,14 @@ Range table_range(const KvSeqs& s) { return rows_range(s.table, s.n_seq, s.table
 size_t cache_bytes(const KvSeqs& s, int n_kv, int head_dim) {
     return static_cast<size_t>(s.n_pages) * n_kv * 2 * (static_cast<size_t>(head_dim / 2 + head_dim / kKvGroup) << s.page_log2);
 }
-// Whether some sequence of T rows in n_seq may have few rows, or many.
-bool may_have_few(int64_t T, int n_seq, int group) { return group <= kKvFewRows && (n_seq > 1 || T * group <= kKvFewRows); }
-bool may_have_prompts(int64_t T, int n_seq, int group) { return T * group > kKvFewRows; }
+// Whether some sequence may have few rows, or many: with cu_seqlens, of the T rows any number may be
+// a sequence's.
+bool may_have_few(int64_t rows_each, int group, bool even) {
+    return even ? rows_each * group <= gdn::kKvFewRows : group <= gdn::kKvFewRows;
+}
+bool may_have_prompts(int64_t T, int64_t rows_each, int group, bool even) {
+    return (even ? rows_each : T) * group > gdn::kKvFewRows;
+}
 // Whether every row of `e`-byte elements starts on a 16-byte boundary.
 bool rows16(const void* p, int64_t stride, int e) { return !p || (is_aligned(p, 16) && stride * e % 16 == 0); }
 }  // namespace
@@ -118,8 +123,9 @@ size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int n_heads, int n
     if (T <= 0 || n_seq <= 0 || n_heads <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) ||
         n_heads % n_kv_heads != 0 || sm_count(&sms) != GDN_OK)
         return 0;
-    // (launches on one stream: they may use the same memory one after the other)
-    const bool few = may_have_few(T, n_seq, n_heads / n_kv_heads), prompts = may_have_prompts(T, n_seq, n_heads / n_kv_heads);
+    // (whether the call will have cu_seqlens or not; launches on one stream may use the same memory)
+    const int group = n_heads / n_kv_heads;
+    const bool few = may_have_few(0, group, false), prompts = may_have_prompts(T, 0, group, false);
     const size_t a = few ? kv_few_workspace(head_dim, sms) : 0;
     const size_t b = prompts ? kv_prompt_workspace(T, n_seq, n_heads, n_kv_heads, head_dim, sms) : 0;
     return a > b ? a : b;
@@ -173,10 +179,10 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     if (int rc = sm_count(&sms)) return rc;
     if (cudaError_t err = ssm_status_word(&p.status); err != cudaSuccess) return cuda_bad(err, "cache attention set-up");
     const int group = n_heads / n_kv_heads;
-    const bool even = !cu_seqlens, few_rows = p.s.per_seq * group <= kKvFewRows;
+    const bool even = !cu_seqlens;
     cudaError_t err = cudaSuccess;
-    if (even ? few_rows : may_have_few(T, n_seq, group)) err = launch_kv_few(p, sms, static_cast<cudaStream_t>(cuda_stream));
-    if (err == cudaSuccess && (even ? !few_rows : may_have_prompts(T, n_seq, group)))
+    if (may_have_few(p.s.per_seq, group, even)) err = launch_kv_few(p, sms, static_cast<cudaStream_t>(cuda_stream));
+    if (err == cudaSuccess && may_have_prompts(T, p.s.per_seq, group, even))
         err = launch_kv_prompt(p, sms, static_cast<cudaStream_t>(cuda_stream));
     if (err != cudaSuccess) return cuda_bad(err, "cache attention launch");
     internal_count_launch();

@@ -30,7 +30,7 @@ constexpr int kThreads = 640;
 constexpr int kDequantWarp = 8, kMmaWarp = 16, kDequantWarps = kMmaWarp - kDequantWarp;
 // Registers of the softmax warps, those that bring K and V, and the rest: together what the
 // launch has (96 a thread).
-static_assert(256 * 128 + 256 * 88 + 128 * 48 == kThreads * 96, "registers");
+static_assert(256 * 144 + 256 * 72 + 128 * 48 == kThreads * 96, "registers");
 constexpr float kPShift = 8.f, kSlack = 7.f;  // as in gdn_kv_few.cu
 constexpr int kMaxSplits = 16;
 
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
 
     if (warp < kDequantWarp) {
         // ---- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         const int t = warp >> 2, r = t * kBlock + (warp & 3) * 32 + lane;  // tile, row
         if (t == 1 && !two) {
             warp_arrive(sy, B_Q);
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
         }
     } else if (warp < kMmaWarp) {
         // ---- K and V: an item is 32 codes of a token
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         constexpr int Q4 = D / 32, PER = 32 / Q4, ITEMS = kBlock / (kDequantWarps * PER);  // items of a token; tokens a warp covers; items a thread
         const int w = warp - kDequantWarp, quarter = lane % Q4, tok = w * PER + lane / Q4;  // + kDequantWarps PER i
         const int64_t plane = kv_plane(p.s.page_log2, D);

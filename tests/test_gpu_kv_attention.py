@@ -220,6 +220,67 @@ def test_prompts_and_single_tokens_in_one_call():
     check([1, 200, 1, 1, 30, 1], [500, 200, 3, 64, 900, 17], 6, 2, 128, 16, "bf16")
 
 
+@pytest.mark.parametrize("bounds", [[0, 1], [7, 8], [3, 99], [0, 0], [0, 100], [2, 3, 40, 41]])
+def test_rows_of_no_sequence_around_the_sequences(bounds):
+    """A batch padded before and behind: what a sequence is goes by its bounds alone."""
+    gen = torch.Generator().manual_seed(4)
+    n = len(bounds) - 1
+    new = [b - a for a, b in zip(bounds, bounds[1:])]
+    lens = [m + 60 for m in new]
+    q, cache, table, kv, _, _, _ = make(new, lens, 3, 1, 128, 16, "bf16", gen, pad=100 - sum(new))
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu, out=out, lse=lse)
+    want = ref.attention(q, cache, table, kv, 16, cu=cu)
+    inside = slice(bounds[0], bounds[-1])
+    compare(out[inside], lse[inside], q, [w[inside] for w in want], sum(new), max(lens))
+    outside = [*range(bounds[0]), *range(bounds[-1], 100)]
+    assert bool((out[outside] == 7).all()) and bool((lse[outside] == 7).all())
+
+
+@pytest.mark.parametrize("D,H,G", [(128, 3, 1), (64, 16, 2)])
+def test_prompts_run_alike_whatever_the_workspace_held(D, H, G):
+    """The same call twice, its workspace full of NaN in between: the same bits; on two streams at once too."""
+    gen = torch.Generator().manual_seed(5)
+    q, cache, table, kv, cu, ks, vs = make([200, 1, 90, 4], [4200, 900, 90, 33], H, G, D, 32, "bf16", gen, True)
+    args = dict(cu_seqlens=cu, k_scale=ks, v_scale=vs)
+    first = gdn.gdn_kv_attention(q, cache, table, kv, **args)
+    torch.full((64 << 20,), math.nan, device="cuda")  # (freed at once: what the next call is given)
+    again = gdn.gdn_kv_attention(q, cache, table, kv, **args)
+    assert torch.equal(first, again)
+    torch.cuda.synchronize()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(3)]
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 3]):
+            outs.append(gdn.gdn_kv_attention(q, cache, table, kv, **args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for o in outs)
+    assert gdn.gdn_device_status() == 0
+
+
+def test_a_prompt_captured_and_replayed():
+    gen = torch.Generator().manual_seed(6)
+    q, cache, table, kv, cu, _, _ = make([150, 20], [1150, 70], 6, 2, 128, 64, "fp16", gen)
+    out = torch.empty_like(q)
+    want = gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu, out=out)
+    for _ in range(3):
+        out.fill_(9)
+        graph.replay()
+        assert torch.equal(out, want)
+    q.mul_(0.5)
+    graph.replay()
+    assert torch.equal(out, gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu))
+
+
+def test_more_sequences_than_a_warp_has_lanes():
+    gen = torch.Generator().manual_seed(8)
+    new = torch.randint(0, 40, (70,), generator=gen).tolist()
+    check(new, [n + 10 * (i % 5) + 1 for i, n in enumerate(new)], 3, 1, 128, 16, "bf16", window=33)
+
+
 def test_far_pages():
     """Offsets past 32 bits."""
     dev, page, G, D = "cuda", 256, 4, 128
