@@ -372,7 +372,7 @@ cudaError_t launch(const KvAppendParams& p, int sm_count, cudaStream_t s) {
     // several tokens a CTA where there are tokens for all multiprocessors, a token's units over
     // several CTAs where there are few
     int per = 1;
-    while (per < 4 && p.s.T >= static_cast<int64_t>(sm_count) * 8 * per * 2) per *= 2;
+    while (per < 4 && p.s.T >= static_cast<int64_t>(sm_count) * 4 * per) per *= 2;
     const int64_t x = (p.s.T + per - 1) / per;
     const int pieces = (per * units + kThreads - 1) / kThreads;
     int y = 1;
