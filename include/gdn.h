@@ -26,8 +26,8 @@
  *   w           [d]               norm weight, shared by all value heads
  *   y_fp16      [T][n_vh][d]      IEEE binary16 bits
  * Value head h reads key head h % n_kh.
- * The selective state space operators (gdn_ssm_*) and gdn_block_norm state their
- * own layouts: activations of a gdn_dtype with a stride between rows.
+ * The selective state space operators (gdn_ssm_*), gdn_block_norm and the paged cache's
+ * (gdn_kv_*) state their own layouts: activations of a gdn_dtype with a stride between rows.
  *
  * Ownership: every pointer is a DEVICE pointer owned by the caller, on the
  * current CUDA device.  The library allocates only (a) a 4-byte status word per
@@ -71,8 +71,8 @@ typedef enum gdn_mode {
  * of the two modes' GPU time per call on GB300 (48 value heads, d = 128). */
 #define GDN_AUTO_CHUNKED_MIN_T 64
 
-/* Activation types of the gdn_ssm_* operators and gdn_block_norm (their parameters
- * and states are FP32 in every case). */
+/* Activation types of the gdn_ssm_* operators, gdn_block_norm and the gdn_kv_* operators
+ * (their parameters and states are FP32 in every case). */
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
 
 typedef enum gdn_status {

@@ -56,7 +56,9 @@ struct KvAttentionParams {
 };
 // Sequences of at most so many rows (tokens x heads of a group) are gdn_kv_few.cu's, the others
 // gdn_kv_prompt.cu's, whatever else a call has; each launch leaves the other's alone.
-constexpr int kKvFewRows = 16;
+// Few / prompt, us: 16 sequences of up to 6000 tokens, 16 KV heads of 128, of 12 rows 53 / 162, of
+// 24 115 / 188, of 48 214 / 159, one sequence of 32768, of 30 rows 63 / 86, of 60 120 / 87.
+constexpr int kKvFewRows = 32;
 // On the warps' own MMAs, 8 or 16 rows at a time (gdn_kv_few.cu).
 size_t kv_few_workspace(int head_dim, int sm_count);
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s);

@@ -14,7 +14,11 @@
 // round to different scales or codes, those are decided in FP64 (one group in some thousands).
 // Ties, which 16-bit values without a rotation hit often, need none of it: see `quantise`.
 //
-// What bounds it: memory (the queries in and out are most of it).
+// What bounds it: the latency of a unit's loads behind one another at 16 to 24 warps a
+// multiprocessor (registers), then instructions (640 a unit and warp, issued in half the cycles), then
+// memory. 48 + 2 x 16 heads of 128: 8191 tokens, 16 bits, 94 us (3.8 TB/s); 64 + 2 x 8 of 64, 2048 tokens
+// of FP32 32 us; one token 10 us from launch to end. With whole groups done again in FP64 148, 82 and, for 250 tokens,
+// 61 us (now 14): FP64 runs at a sixty-fourth of FP32's rate.
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -369,8 +373,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
 template <class T, int D>
 cudaError_t launch(const KvAppendParams& p, int sm_count, cudaStream_t s) {
     const int units = ((p.q ? p.n_heads : 0) + 2 * p.n_kv) * (D / 32);
-    // several tokens a CTA where there are tokens for all multiprocessors, a token's units over
-    // several CTAs where there are few
+    // several tokens a CTA where there are tokens for all multiprocessors, which share its start (2048
+    // tokens of FP32: 4 a CTA 33 us, 1 41; 8191 of FP16: 4 96, 2 107), a token's units over several CTAs
+    // where there are few
     int per = 1;
     while (per < 4 && p.s.T >= static_cast<int64_t>(sm_count) * 4 * per) per *= 2;
     const int64_t x = (p.s.T + per - 1) / per;

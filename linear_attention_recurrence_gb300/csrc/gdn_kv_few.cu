@@ -2,8 +2,8 @@
 // requests, drafted tokens.
 //
 // A unit is one (sequence, KV head, block of R = 8 or 16 rows), a row being a (token, head of
-// the KV head's group); its work is the tiles of 64 tokens (32 where R is 16) that one of its rows
-// may see.  All units' tiles, in order, are cut into equal pieces, one for each warp, so that
+// the KV head's group); its work is the tiles of 64 tokens that one of its rows may
+// see.  All units' tiles, in order, are cut into equal pieces, one for each warp, so that
 // ragged lengths fill the device evenly; a unit that several warps share leaves partial results
 // in the workspace, which a second launch joins in order of the tokens.
 //
@@ -25,14 +25,21 @@
 // A token whose values hold a NaN scale gives its scores NaN instead, so that rows that do not
 // see it keep clear of it.
 //
-// What bounds it: memory.
+// What bounds it: the instructions, their latency and the half-rate pipes (a code's conversion and
+// scaling are four instructions a token and lane each; 19 a token and head in all, issued in 57% of
+// the cycles), then memory. 48 query and 16 KV heads of 128, BF16: 64 requests of up to 8192 tokens
+// 139 us (0.64 GB at 4.6 TB/s; the join 9 of it), one of 32768 33 us, 16 of up to 6000 with 4 tokens
+// each 51 us; 64 and 8 heads of 64, FP16: 250 requests of up to 1500 51 us. Steps, the first of
+// these: warps of a CTA on one unit 310 us; CTAs of 4 warps 233; tiles of 64 tokens and maxima renewed
+// seldom 180; a piece for each warp 157; plain asynchronous copies in place of bulk ones 150; code of
+// their own for whole tiles 147; a unit's start counted in its pieces 140.
 #include "gdn_kv.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kSlots = 2;    // tiles in shared memory a warp
-constexpr int kUnitTiles = 2;  // what a unit's start and end count for, in tiles
+constexpr int kUnitTiles = 2;  // what a unit's start and end count for, in tiles (250 requests: 1 61 us, 2 55, 4 74)
 // A row's maximum is renewed only once a score passes it by more than 2^kSlack: probabilities,
 // times 2^kPShift, stay below 2^(kPShift + kSlack) (FP16 ends at 2^16).
 constexpr float kPShift = 8.f, kSlack = 7.f;
@@ -41,17 +48,18 @@ constexpr float kPShift = 8.f, kSlack = 7.f;
 // the other) and its end overlap with the other warps' work.  CTAs are only what they come in.
 constexpr int kWarps = 4;
 template <int NT>
-constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
-// Where there is enough to do, pieces a warp of the resident ones: CTAs that end early make room.
+constexpr int kCtasPerSm = NT == 1 ? 3 : 2;  // (16 rows in 168 registers spill: 16 x 4 tokens 88 us, in 255 78)
+// Where there is enough to do, so many pieces for each resident warp: CTAs that end early make room.
+// (64 requests: 2 158 us, 3 170, whose joins are more.)
 constexpr int kWaves = 2;
 constexpr int kPiecesPerSm = kWarps * kCtasPerSm<1> * kWaves;  // at most
 // Tiles of a piece: a wave's share at most, down to kMinTiles, and no fewer than the waves leave.
+// (Small pieces of 8, 16, 64 tiles: 16 x 4 tokens 74, 57, 57 us; 64 requests 147, 147, 152.)
 constexpr int kMinTiles = 2, kSmallPiece = 16;
 
-template <int NT>
-constexpr int kTileOf = 64;
-template <int D, int NT>
-constexpr int kTileBytes = 2 * kTileOf<NT> * (D / 2 + D / kKvGroup);
+constexpr int kTile = 64;  // tokens a warp takes at a time
+template <int D>
+constexpr int kTileBytes = 2 * kTile * (D / 2 + D / kKvGroup);
 
 // A partial result: R rows of head_dim sums, then R maxima (base 2) and R sums.
 template <int R, int D>
@@ -61,7 +69,7 @@ struct Geometry {
     int64_t begin, rows, tiles, first, blocks, cost;
 };
 // What sequence s has to do: `tiles` for each of n_kv * blocks units.
-__device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, int R, int tile) {
+__device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, int R) {
     Geometry g{};
     int64_t e;
     kv_rows(p.s, s, g.begin, e);
@@ -77,8 +85,8 @@ __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, 
         lo = len - g.rows - p.window + 1;
         lo = lo < 0 ? 0 : lo;
     }
-    g.first = lo / tile;
-    g.tiles = (hi + tile - 1) / tile - g.first;
+    g.first = lo / kTile;
+    g.tiles = (hi + kTile - 1) / kTile - g.first;
     if (g.tiles < 1) g.tiles = 1;  // (its rows see nothing: the outputs are zeros)
     g.blocks = (g.rows * group + R - 1) / R;
     g.cost = (g.tiles + kUnitTiles) * g.blocks * p.n_kv;
@@ -101,7 +109,7 @@ __device__ __forceinline__ int64_t piece_tiles(int64_t total, int64_t pieces) {
 
 // Sums up all sequences' tiles and finds, for each of the CTA's warps, the sequence that its
 // piece begins in.  Returns the tiles of a piece; 0: nothing is left for this CTA.
-__device__ int64_t find_pieces(const KvAttentionParams& p, int R, int tile, int64_t* all, Scratch& sh) {
+__device__ int64_t find_pieces(const KvAttentionParams& p, int R, int64_t* all, Scratch& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kThreads = kWarps * 32;
     const int64_t pieces = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -110,7 +118,7 @@ __device__ int64_t find_pieces(const KvAttentionParams& p, int R, int tile, int6
     for (int round = 0; round < 2; ++round) {
         int64_t base = 0;
         for (int s0 = 0; s0 < p.s.n_seq; s0 += kThreads) {
-            const int64_t n = s0 + tid < p.s.n_seq ? geometry(p, s0 + tid, R, tile).cost : 0;
+            const int64_t n = s0 + tid < p.s.n_seq ? geometry(p, s0 + tid, R).cost : 0;
             int64_t inc = n;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -209,7 +217,7 @@ __device__ __forceinline__ void row_of(int64_t row, int group, int n_kv, int kv_
 
 template <class T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(const KvAttentionParams p) {
-    constexpr int R = 8 * NT, kTile = kTileOf<NT>;
+    constexpr int R = 8 * NT;
     constexpr int B = 2;  // sixteens of tokens that are computed at a time
     constexpr int DL = D / 4;        // elements of a token's K that a lane takes (its words: DL / 8)
     constexpr int KS = D / 16;       // k-steps of S^T, M tiles of O^T
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t total;
-    const int64_t per = find_pieces(p, R, kTile, &total, scratch);
+    const int64_t per = find_pieces(p, R, &total, scratch);
     int64_t at = piece * per;
     const int64_t end = at + per < total ? at + per : total;
     Join* join = static_cast<Join*>(p.workspace) + piece;
@@ -232,14 +240,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
     if (at >= end) return;
     int s = scratch.seq[warp];
     int64_t base = scratch.base[warp];  // tiles before sequence s
-    Geometry geo = geometry(p, s, R, kTile);
+    Geometry geo = geometry(p, s, R);
 
-    unsigned char* slots = smem + warp * kSlots * kTileBytes<D, NT>;
+    unsigned char* slots = smem + warp * kSlots * kTileBytes<D>;
 
     while (at < end) {
         while (at >= base + geo.cost) {  // the next sequence with rows
             base += geo.cost;
-            geo = geometry(p, ++s, R, kTile);
+            geo = geometry(p, ++s, R);
         }
         const int64_t unit_cost = geo.tiles + kUnitTiles;
         const int64_t unit = (at - base) / unit_cost;  // head-major
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
         const int held = static_cast<int>(len < cap ? len : cap);
 
         // A tile is one page's, or 2 or 4 small ones': lane i looks up part i of it.
-        constexpr int kTileLog2 = kTile == 64 ? 6 : 5, kParts = kTile / 16;
+        constexpr int kTileLog2 = 6, kParts = kTile / 16;
         const int part_log2 = p.s.page_log2 < kTileLog2 ? p.s.page_log2 : kTileLog2;
         const int64_t plane = kv_plane(p.s.page_log2, D);
         const int64_t scales_at = int64_t{D / 2} << p.s.page_log2;
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
         // starts a tile's copies, 16 bytes a lane at a time; returns which of its sixteens of tokens there are
         auto fetch = [&](int64_t tile, const uint8_t* mine, int slot) -> uint32_t {
             const uint32_t parts = __ballot_sync(0xffffffffu, mine != nullptr);
-            unsigned char* dst = slots + slot * kTileBytes<D, NT> + 16 * lane;
+            unsigned char* dst = slots + slot * kTileBytes<D> + 16 * lane;
             const int in_page = static_cast<int>(tile * kTile) & ((1 << p.s.page_log2) - 1);
             constexpr int TPI = 1024 / D, TPL = 256 / D;  // tokens of a warp's 512 bytes of codes; of a lane's 16 of scales
             if (part_log2 == kTileLog2) {
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
             const int64_t tile = tile0 + i;
             cp_async_wait<kSlots - 1>();
             __syncwarp();
-            const unsigned char* kc = slots + slot * kTileBytes<D, NT>;
+            const unsigned char* kc = slots + slot * kTileBytes<D>;
             const unsigned char* vc = kc + kPlane;
             const uint32_t there = halves[slot];
             const int token0 = static_cast<int>(tile) * kTile;
@@ -815,7 +823,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAtt
 
 template <class T, int D, int NT>
 cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
-    constexpr int smem = kWarps * kSlots * kTileBytes<D, NT>;
+    constexpr int smem = kWarps * kSlots * kTileBytes<D>;
     const int ctas = sm_count * kCtasPerSm<NT> * kWaves;
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_few_kernel<T, D, NT>), smem); e != cudaSuccess) return e;
     kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
