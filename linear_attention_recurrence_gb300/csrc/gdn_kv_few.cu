@@ -2,14 +2,14 @@
 // requests, drafted tokens.
 //
 // A unit is one (sequence, KV head, block of R = 8 or 16 rows), a row being a (token, head of
-// the KV head's group); its work is the tiles of 64 tokens that one of its rows may
-// see.  All units' tiles, in order, are cut into equal pieces, one for each warp, so that
-// ragged lengths fill the device evenly; a unit that several warps share leaves partial results
-// in the workspace, which a second launch joins in order of the tokens.
+// the KV head's group); its work is the tiles of 64 tokens that one of its rows may see.  All
+// units' tiles, in order, are cut into equal pieces, one for each warp, so that ragged lengths
+// fill the device evenly; a unit that several warps share leaves partial results in the
+// workspace, which a second launch joins in order of the tokens.
 //
 // A warp copies a tile's codes and scales into its own two slots of shared memory (cp.async: the
-// bytes of small pages are too few for bulk copies) and computes, transposed so that the few rows are the narrow side of m16n8k16
-// products:
+// bytes of small pages are too few for bulk copies) and computes, transposed so that the few rows
+// are the narrow side of m16n8k16 products:
 //     S^T = K Q^T   (16 tokens x 8 rows, over head_dim), running maximum and sum of each row,
 //     O^T += V^T P^T   (16 of head_dim x 8 rows, over 16 tokens)
 // The order of head_dim in the first product's sum and of its lanes in the second is free, so
@@ -25,9 +25,9 @@
 // A token whose values hold a NaN scale gives its scores NaN instead, so that rows that do not
 // see it keep clear of it.
 //
-// What bounds it: the instructions, their latency and the half-rate pipes (a code's conversion and
-// scaling are four instructions a token and lane each; 19 a token and head in all, issued in 57% of
-// the cycles), then memory. 48 query and 16 KV heads of 128, BF16: 64 requests of up to 8192 tokens
+// What bounds it: the instructions, their latency and the half-rate pipes (19 a token and KV head,
+// of which 4 convert codes, 4 scale them and 1 multiplies; issued in 57% of the cycles), then memory.
+// 48 query and 16 KV heads of 128, BF16: 64 requests of up to 8192 tokens
 // 139 us (0.64 GB at 4.6 TB/s; the join 9 of it), one of 32768 33 us, 16 of up to 6000 with 4 tokens
 // each 51 us; 64 and 8 heads of 64, FP16: 250 requests of up to 1500 51 us. Steps, the first of
 // these: warps of a CTA on one unit 310 us; CTAs of 4 warps 233; tiles of 64 tokens and maxima renewed
@@ -52,7 +52,8 @@ constexpr int kCtasPerSm = NT == 1 ? 3 : 2;  // (16 rows in 168 registers spill:
 // Where there is enough to do, so many pieces for each resident warp: CTAs that end early make room.
 // (64 requests: 2 158 us, 3 170, whose joins are more.)
 constexpr int kWaves = 2;
-constexpr int kPiecesPerSm = kWarps * kCtasPerSm<1> * kWaves;  // at most
+template <int NT>
+constexpr int kPiecesPerSm = kWarps * kCtasPerSm<NT> * kWaves;
 // Tiles of a piece: a wave's share at most, down to kMinTiles, and no fewer than the waves leave.
 // (Small pieces of 8, 16, 64 tiles: 16 x 4 tokens 74, 57, 57 us; 64 requests 147, 147, 152.)
 constexpr int kMinTiles = 2, kSmallPiece = 16;
@@ -852,7 +853,9 @@ cudaError_t by_rows(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
 }  // namespace
 
 size_t kv_few_workspace(int head_dim, int sm_count) {
-    return static_cast<size_t>(sm_count) * kPiecesPerSm * (sizeof(Join) + 2 * 16 * (head_dim + 2) * sizeof(float));
+    const size_t row = 2 * (head_dim + 2) * sizeof(float);
+    const size_t a = kPiecesPerSm<1> * (sizeof(Join) + 8 * row), b = kPiecesPerSm<2> * (sizeof(Join) + 16 * row);
+    return sm_count * (a > b ? a : b);
 }
 
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
