@@ -454,7 +454,7 @@ int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
  * that see it NaN throughout.  The order of a row's sums goes by the other sequences of the call;
  * the same call gives the same bits.
  * workspace: gdn_kv_attention_workspace_bytes() bytes, 16-byte aligned, the call's own until it
- * has finished.
+ * has finished (NULL where that is 0).
  */
 int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t n_pages, int page_size,
                      const int32_t* block_table, int64_t table_stride, int max_pages, const int32_t* kv_lens,
@@ -463,8 +463,10 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
                      int n_kv_heads, int head_dim, int dtype, void* workspace, size_t workspace_bytes,
                      void* cuda_stream);
 
-/* Bytes of workspace a gdn_kv_attention call of these sizes needs (0: none). */
-size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int n_heads, int n_kv_heads, int head_dim);
+/* Bytes of workspace a gdn_kv_attention call of these sizes needs (0: none); even: 1 where
+ * cu_seqlens is NULL. */
+size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int even, int page_size, int max_pages, int n_heads,
+                                        int n_kv_heads, int head_dim);
 
 /*
  * Process-wide options.  The library reads no environment variable: the A/B

@@ -51,6 +51,7 @@ struct KvAttentionParams {
     float scale;  // of the scores, times log2 e
     int n_heads, n_kv, head_dim, causal, window, dtype;
     bool vector;  // q's and out's rows on 16-byte boundaries
+    bool whole;   // (gdn_kv_few.cu's: its units are not cut)
     void* workspace;
     int* status;
 };
@@ -60,11 +61,11 @@ struct KvAttentionParams {
 // 24 115 / 188, of 48 214 / 159, one sequence of 32768, of 30 rows 63 / 86, of 60 120 / 87.
 constexpr int kKvFewRows = 32;
 // On the warps' own MMAs, 8 or 16 rows at a time (gdn_kv_few.cu).
-size_t kv_few_workspace(int head_dim, int sm_count);
+size_t kv_few_workspace(const KvSeqs& q, int n_kv, int head_dim, int sm_count);
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s);
 // On tcgen05, 256 rows at a time (gdn_kv_prompt.cu).
 int64_t kv_prompt_ctas(int64_t T, int n_seq, int n_heads, int n_kv);  // at most so many, where no unit is split
-size_t kv_prompt_workspace(int64_t T, int n_seq, int n_heads, int n_kv, int head_dim, int sm_count);
+size_t kv_prompt_workspace(const KvSeqs& q, bool even, int n_heads, int n_kv, int head_dim, int sm_count);
 cudaError_t launch_kv_prompt(const KvAttentionParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace gdn

@@ -51,6 +51,14 @@ bool may_have_few(int64_t rows_each, int group, bool even) {
 bool may_have_prompts(int64_t T, int64_t rows_each, int group, bool even) {
     return (even ? rows_each : T) * group > gdn::kKvFewRows;
 }
+// (Launches on one stream may use the same memory.)
+size_t workspace_of(const KvSeqs& q, int n_heads, int n_kv, int head_dim, int sms) {
+    const int group = n_heads / n_kv;
+    const bool even = !q.cu;
+    const size_t a = may_have_few(q.per_seq, group, even) ? kv_few_workspace(q, n_kv, head_dim, sms) : 0;
+    const size_t b = may_have_prompts(q.T, q.per_seq, group, even) ? kv_prompt_workspace(q, even, n_heads, n_kv, head_dim, sms) : 0;
+    return a > b ? a : b;
+}
 // Whether every row of `e`-byte elements starts on a 16-byte boundary.
 bool rows16(const void* p, int64_t stride, int e) { return !p || (is_aligned(p, 16) && stride * e % 16 == 0); }
 }  // namespace
@@ -118,17 +126,17 @@ int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
     return GDN_OK;
 }
 
-size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int n_heads, int n_kv_heads, int head_dim) {
+size_t gdn_kv_attention_workspace_bytes(int64_t T, int n_seq, int even, int page_size, int max_pages, int n_heads,
+                                        int n_kv_heads, int head_dim) {
     int sms = 0;
-    if (T <= 0 || n_seq <= 0 || n_heads <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) ||
-        n_heads % n_kv_heads != 0 || sm_count(&sms) != GDN_OK)
+    KvSeqs q{};
+    // (the bounds themselves are not looked at: any will do)
+    const int32_t some = 0;
+    if (T <= 0 || n_seq <= 0 ||
+        check_cache(&q, T, n_seq, even ? nullptr : &some, 0, page_size, max_pages, max_pages, n_heads, n_kv_heads, head_dim) ||
+        sm_count(&sms) != GDN_OK)
         return 0;
-    // (whether the call will have cu_seqlens or not; launches on one stream may use the same memory)
-    const int group = n_heads / n_kv_heads;
-    const bool few = may_have_few(0, group, false), prompts = may_have_prompts(T, 0, group, false);
-    const size_t a = few ? kv_few_workspace(head_dim, sms) : 0;
-    const size_t b = prompts ? kv_prompt_workspace(T, n_seq, n_heads, n_kv_heads, head_dim, sms) : 0;
-    return a > b ? a : b;
+    return workspace_of(q, n_heads, n_kv_heads, head_dim, sms);
 }
 
 int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t n_pages, int page_size,
@@ -159,14 +167,16 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     if (!is_aligned(cache, 16) || !is_aligned(workspace, 16)) return bad("the cache and the workspace must be 16-byte aligned");
     p.s.table = block_table;
     p.s.kv_lens = kv_lens;
-    const size_t need = gdn_kv_attention_workspace_bytes(T, n_seq, n_heads, n_kv_heads, head_dim);
+    int sms = 0;
+    const int no_device = sm_count(&sms);  // (told behind what the arguments have wrong)
+    const size_t need = no_device ? 0 : workspace_of(p.s, n_heads, n_kv_heads, head_dim, sms);
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is missing or too small");
     const size_t scale4 = static_cast<size_t>(n_kv_heads) * 4;
     const Range ins[] = {rows_range(q, T, q_stride, qw, e), {cache, cache_bytes(p.s, n_kv_heads, head_dim)},
                          {k_scale, k_scale ? scale4 : 0}, {v_scale, v_scale ? scale4 : 0}, table_range(p.s),
                          lens_range(p.s), cu_range(p.s)};
     const Range outs[] = {rows_range(out, T, out_stride, qw, e),
-                          {lse, lse ? static_cast<size_t>(T) * n_heads * 4 : 0}, {workspace, need}};
+                          {lse, lse ? static_cast<size_t>(T) * n_heads * 4 : 0}, {workspace, workspace ? need : 0}};
     if (any_overlap(ins, outs)) return bad("an output overlaps another argument");
     p.q = q, p.out = out, p.lse = lse, p.q_stride = q_stride, p.out_stride = out_stride;
     p.k_scale = k_scale, p.v_scale = v_scale, p.cache = static_cast<const uint8_t*>(cache);
@@ -175,8 +185,7 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     p.vector = rows16(q, q_stride, e) && rows16(out, out_stride, e);
     if (kv_prompt_ctas(T, n_seq, n_heads, n_kv_heads) > INT32_MAX / 2) return unsupported("too many rows and heads");
     p.workspace = workspace;
-    int sms = 0;
-    if (int rc = sm_count(&sms)) return rc;
+    if (no_device) return no_device;
     if (cudaError_t err = ssm_status_word(&p.status); err != cudaSuccess) return cuda_bad(err, "cache attention set-up");
     const int group = n_heads / n_kv_heads;
     const bool even = !cu_seqlens;

@@ -69,6 +69,21 @@ constexpr int kPartialFloats = R * (D + 2);
 struct Geometry {
     int64_t begin, rows, tiles, first, blocks, cost;
 };
+// Where no sequence has more tiles than this (by its row of the table), a unit is a warp's as a whole
+// and nothing is joined: kWholeTiles, and kWholeTilesMany where there are units for all resident warps.
+// Whole / joined, us, 16 KV heads of 128: 1 request of 256 tokens 14 / 16, of 512 20 / 16; 16 of 512 22 / 22,
+// of 1024 35 / 27; 200 of 256 47 / 51, of 512 70 / 90, of 1024 113 / 123, of 2048 201 / 201; 8 of 64, 250 of up to
+// 700 39 / 41, of up to 1500 63 / 55.
+constexpr int kWholeTiles = 4, kWholeTilesMany = 16;
+bool whole_units(const KvSeqs& q, int n_kv, int sm_count) {
+    const bool many = static_cast<int64_t>(q.n_seq) * n_kv >= static_cast<int64_t>(sm_count) * kWarps * kCtasPerSm<1>;
+    return (static_cast<int64_t>(q.max_pages) << q.page_log2) <= (many ? kWholeTilesMany : kWholeTiles) * kTile;
+}
+// A unit's part of the call's cost: its tiles, and its start and end.
+__device__ __forceinline__ int64_t unit_cost(const KvAttentionParams& p, int64_t tiles) {
+    return p.whole ? 1 : tiles + kUnitTiles;
+}
+
 // What sequence s has to do: `tiles` for each of n_kv * blocks units.
 __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, int R) {
     Geometry g{};
@@ -90,7 +105,7 @@ __device__ __forceinline__ Geometry geometry(const KvAttentionParams& p, int s, 
     g.tiles = (hi + kTile - 1) / kTile - g.first;
     if (g.tiles < 1) g.tiles = 1;  // (its rows see nothing: the outputs are zeros)
     g.blocks = (g.rows * group + R - 1) / R;
-    g.cost = (g.tiles + kUnitTiles) * g.blocks * p.n_kv;
+    g.cost = unit_cost(p, g.tiles) * g.blocks * p.n_kv;
     return g;
 }
 
@@ -100,8 +115,9 @@ struct Scratch {
     int seq[kWarps];       // and the sequence
 };
 
-// Tiles of a piece, of `total` tiles, over the resident warps or kWaves times as many.
-__device__ __forceinline__ int64_t piece_tiles(int64_t total, int64_t pieces) {
+// Tiles of a piece, of `total` tiles, over the resident warps or kWaves times as many.  (Whole units: units.)
+__device__ __forceinline__ int64_t piece_tiles(int64_t total, int64_t pieces, bool whole) {
+    if (whole) return (total + pieces - 1) / pieces;
     const int64_t one = (total * kWaves + pieces - 1) / pieces, all = (total + pieces - 1) / pieces;
     const int64_t small = one < kSmallPiece ? one : kSmallPiece;
     const int64_t per = all > small ? all : small;
@@ -139,7 +155,7 @@ __device__ int64_t find_pieces(const KvAttentionParams& p, int R, int64_t* all, 
             base += sum;
             if (p.s.n_seq <= kThreads) {
                 total = base;
-                per = piece_tiles(total, pieces);
+                per = piece_tiles(total, pieces, p.whole);
                 at = static_cast<int64_t>(blockIdx.x) * kWarps * per;
                 round = 1;
             }
@@ -158,7 +174,7 @@ __device__ int64_t find_pieces(const KvAttentionParams& p, int R, int64_t* all, 
         }
         if (round == 0) {
             total = base;
-            per = piece_tiles(total, pieces);
+            per = piece_tiles(total, pieces, p.whole);
             at = static_cast<int64_t>(blockIdx.x) * kWarps * per;
             if (at >= total) break;
         }
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
     int64_t at = piece * per;
     const int64_t end = at + per < total ? at + per : total;
     Join* join = static_cast<Join*>(p.workspace) + piece;
-    if (lane == 0) join->rows = 0;
+    if (lane == 0 && !p.whole) join->rows = 0;
     __syncwarp();
     if (at >= end) return;
     int s = scratch.seq[warp];
@@ -250,18 +266,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
             base += geo.cost;
             geo = geometry(p, ++s, R);
         }
-        const int64_t unit_cost = geo.tiles + kUnitTiles;
-        const int64_t unit = (at - base) / unit_cost;  // head-major
-        const int64_t unit_begin = base + unit * unit_cost;
+        const int64_t cost = unit_cost(p, geo.tiles);
+        const int64_t unit = (at - base) / cost;  // head-major
+        const int64_t unit_begin = base + unit * cost;
         const int head = static_cast<int>(unit / geo.blocks);
         const int64_t row0 = (unit - head * geo.blocks) * R;
         const int64_t left = geo.rows * group - row0;
         const int rows = left < R ? static_cast<int>(left) : R;
         // its tiles from `begin_tile` to `end_tile` are this warp's (the first of a unit's cost is its start)
-        const int64_t unit_end = unit_begin + unit_cost;
+        const int64_t unit_end = unit_begin + cost;
         const int64_t stop = end < unit_end ? end : unit_end;
         const int64_t begin_tile = at - unit_begin > kUnitTiles ? at - unit_begin - kUnitTiles : 0;
-        const int64_t end_tile = stop - unit_begin > kUnitTiles ? stop - unit_begin - kUnitTiles : 0;
+        const int64_t end_tile = p.whole ? geo.tiles : stop - unit_begin > kUnitTiles ? stop - unit_begin - kUnitTiles : 0;
         const int n_tiles = static_cast<int>(end_tile - begin_tile);
         const int64_t tile0 = geo.first + begin_tile;
         if (n_tiles == 0) {
@@ -828,7 +844,7 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     const int ctas = sm_count * kCtasPerSm<NT> * kWaves;
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_few_kernel<T, D, NT>), smem); e != cudaSuccess) return e;
     kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || p.whole) return e;
     cudaLaunchConfig_t cfg{};
     // (a row of the grid for each row that a unit may have)
     const int64_t rows = p.s.cu ? 8 * NT : p.s.per_seq * (p.n_heads / p.n_kv);
@@ -852,13 +868,16 @@ cudaError_t by_rows(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
 
 }  // namespace
 
-size_t kv_few_workspace(int head_dim, int sm_count) {
+size_t kv_few_workspace(const KvSeqs& q, int n_kv, int head_dim, int sm_count) {
+    if (whole_units(q, n_kv, sm_count)) return 0;
     const size_t row = 2 * (head_dim + 2) * sizeof(float);
     const size_t a = kPiecesPerSm<1> * (sizeof(Join) + 8 * row), b = kPiecesPerSm<2> * (sizeof(Join) + 16 * row);
     return sm_count * (a > b ? a : b);
 }
 
-cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
+cudaError_t launch_kv_few(const KvAttentionParams& params, int sm_count, cudaStream_t s) {
+    KvAttentionParams p = params;
+    p.whole = whole_units(p.s, p.n_kv, sm_count);
     if (p.dtype == GDN_BF16)
         return p.head_dim == 128 ? by_rows<__nv_bfloat16, 128>(p, sm_count, s) : by_rows<__nv_bfloat16, 64>(p, sm_count, s);
     return p.head_dim == 128 ? by_rows<__half, 128>(p, sm_count, s) : by_rows<__half, 64>(p, sm_count, s);

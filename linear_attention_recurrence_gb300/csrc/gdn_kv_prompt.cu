@@ -596,25 +596,22 @@ int64_t unit_bound(int64_t T, int n_seq, int group, bool even) {
 // CTAs that share a unit: 1 where units fill the device, else by the blocks that the busiest
 // multiprocessor walks (a CTA's start and end take about two, the joining launch four; 509 tokens
 // behind 16384, 96 CTAs: 3 splits 221 us, none 299).
-int splits_of(int64_t ctas, int64_t blocks, int sm_count, int most) {
+int splits_of(const KvSeqs& q, int64_t ctas, int sm_count) {
+    const int64_t blocks = ((static_cast<int64_t>(q.max_pages) << q.page_log2) + kBlock - 1) / kBlock;
     int best = 1;
     int64_t least = INT64_MAX;
-    for (int s = 1; s <= most && (s == 1 || blocks / s >= 4); ++s) {
+    for (int s = 1; s <= kMaxSplits && (s == 1 || (ctas * s <= 2 * sm_count && blocks / s >= 4)); ++s) {
         const int64_t cost = (ctas * s + sm_count - 1) / sm_count * ((blocks + s - 1) / s + 2) + (s > 1 ? 4 : 0);
         if (cost < least) least = cost, best = s;
     }
     return best;
 }
-int most_splits(int64_t ctas, int sm_count) {
-    const int64_t most = ctas > 0 ? 2 * sm_count / ctas : 1;
-    return static_cast<int>(most < 1 ? 1 : most > kMaxSplits ? kMaxSplits : most);
-}
 
 template <class T, int D>
 cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     const int64_t units = unit_bound(p.s.T, p.s.n_seq, p.n_heads / p.n_kv, p.s.cu == nullptr);
-    const int64_t ctas = units * p.n_kv, blocks = ((static_cast<int64_t>(p.s.max_pages) << p.s.page_log2) + kBlock - 1) / kBlock;
-    const int splits = splits_of(ctas, blocks, sm_count, most_splits(ctas, sm_count));
+    const int64_t ctas = units * p.n_kv;
+    const int splits = splits_of(p.s, ctas, sm_count);
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_prompt_kernel<T, D>), Smem<D>::TOTAL); e != cudaSuccess)
         return e;
     kv_prompt_kernel<T, D><<<static_cast<unsigned>(ctas * splits), kThreads, Smem<D>::TOTAL, s>>>(p, splits, units);
@@ -637,17 +634,10 @@ int64_t kv_prompt_ctas(int64_t T, int n_seq, int n_heads, int n_kv) {
     return unit_bound(T, n_seq, n_heads / n_kv, false) * n_kv;
 }
 
-size_t kv_prompt_workspace(int64_t T, int n_seq, int n_heads, int n_kv, int head_dim, int sm_count) {
-    size_t need = 0;
-    for (const bool even : {false, true}) {  // (whichever of the two forms of the bounds the call will have)
-        if (even && T % n_seq != 0) continue;
-        const int64_t ctas = unit_bound(T, n_seq, n_heads / n_kv, even) * n_kv;
-        const int most = most_splits(ctas, sm_count);
-        if (most == 1) continue;
-        const size_t n = static_cast<size_t>(ctas) * (sizeof(Part) + sizeof(float) * most * kRows * (head_dim + 2));
-        need = n > need ? n : need;
-    }
-    return need;
+size_t kv_prompt_workspace(const KvSeqs& q, bool even, int n_heads, int n_kv, int head_dim, int sm_count) {
+    const int64_t ctas = unit_bound(q.T, q.n_seq, n_heads / n_kv, even) * n_kv;
+    const int splits = splits_of(q, ctas, sm_count);
+    return splits == 1 ? 0 : static_cast<size_t>(ctas) * (sizeof(Part) + sizeof(float) * splits * kRows * (head_dim + 2));
 }
 
 cudaError_t launch_kv_prompt(const KvAttentionParams& p, int sm_count, cudaStream_t s) {

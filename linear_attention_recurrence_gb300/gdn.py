@@ -119,7 +119,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.gdn_kv_attention.argtypes = [vp, i64, vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, vp, f32, i32, i32, vp,
                                          i64, vp, i64, i32, i32, i32, i32, vp, sz, vp]
         lib.gdn_kv_attention.restype = i32
-        lib.gdn_kv_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        lib.gdn_kv_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
         lib.gdn_kv_attention_workspace_bytes.restype = sz
         lib.gdn_last_error.argtypes = []
         lib.gdn_last_error.restype = ctypes.c_char_p
@@ -737,11 +737,12 @@ def gdn_kv_attention(q, cache, block_table, kv_lens, k_scale=None, v_scale=None,
     op, os_ = _rows(out, "out", shape, ty, dev)
     lsep = _dense(lse, "lse", (T, H), f32, dev)
     lib = _lib or load_library()
+    sizes = (T, n, cu is None, page, width, H, G, D)
     if _current_device() == dev:  # (it goes by the device's multiprocessors)
-        need = lib.gdn_kv_attention_workspace_bytes(T, n, H, G, D)
+        need = lib.gdn_kv_attention_workspace_bytes(*sizes)
     else:
         with torch.cuda.device(dev):
-            need = lib.gdn_kv_attention_workspace_bytes(T, n, H, G, D)
+            need = lib.gdn_kv_attention_workspace_bytes(*sizes)
     ws = _empty((need,), torch.uint8, dev, stream) if need else None
     _launch(lib.gdn_kv_attention, dev, stream, qp, qs, cp, pages, page, tp, ts, width, lp, cu, n, ksp, vsp,
             D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, max(os_, H * D) if T <= 1 else os_, lsep,
