@@ -745,7 +745,7 @@ def gdn_kv_attention(q, cache, block_table, kv_lens, k_scale=None, v_scale=None,
             need = lib.gdn_kv_attention_workspace_bytes(*sizes)
     ws = _empty((need,), torch.uint8, dev, stream) if need else None
     _launch(lib.gdn_kv_attention, dev, stream, qp, qs, cp, pages, page, tp, ts, width, lp, cu, n, ksp, vsp,
-            D ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, max(os_, H * D) if T <= 1 else os_, lsep,
+            D ** -0.5 if scale is None else scale, 1 if causal else 0, min(window, 2 ** 31 - 1), op, max(os_, H * D) if T <= 1 else os_, lsep,
             T, H, G, D, dt, None if ws is None else ws.data_ptr(), need)
     return out
 

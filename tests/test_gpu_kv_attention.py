@@ -175,6 +175,30 @@ def test_queries_of_any_size():
         assert bool(out[3, 0].isnan().all()) and not bool(out[4].isnan().any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new", [[1] * 5, [5], [120, 5]])
+def test_infinite_queries(new, dtype):
+    """A row with an infinity is NaN where a score is infinite or NaN; its neighbours are as ever."""
+    def infinite(q, cache, table, kv):
+        q[1, 1, 7] = math.inf
+        q[3, 0, 100] = -math.inf
+    out, _ = check(new, [200] * len(new), 3, 1, 128, 32, dtype, change=infinite)
+    assert not bool(out[[0, 2, 4]].isnan().any())
+    assert bool(out[1, 1].isnan().all()) and bool(out[3, 0].isnan().all())
+
+
+def test_windows_of_any_size():
+    """A window beyond 32 bits is one that leaves nothing out."""
+    gen = torch.Generator().manual_seed(4)
+    for new, lens in (([1, 2], [40, 300]), ([150], [200])):
+        q, cache, table, kv, cu, _, _ = make(new, lens, 3, 1, 64, 16, "bf16", gen)
+        want = gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu)
+        for window in (2 ** 31 - 1, 2 ** 32 + 5, 2 ** 63 - 1):
+            assert torch.equal(want, gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu, window=window))
+        with pytest.raises(gdn.GDNError):
+            gdn.gdn_kv_attention(q, cache, table, kv, cu_seqlens=cu, window=-1)
+
+
 def test_scores_of_any_size():
     check([1, 2], [300, 50], 6, 2, 128, 64, "bf16", scale=20.0)
     check([140], [300], 6, 2, 128, 64, "bf16", scale=20.0)
