@@ -280,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
                 fence_async_smem();
                 warp_arrive(sy, B_Q);
             }
-            // pages that are none, in this CTA's blocks (their tokens are not seen)
+            // pages that are none, in this CTA's blocks (their tokens are not seen), from the one that the
+            // first block lies in (a page may be longer than a block)
+            const int64_t at0 = static_cast<int64_t>(first) * kBlock >> p.s.page_log2 << p.s.page_log2;
             const int64_t at1 = static_cast<int64_t>(first + n) * kBlock < held ? static_cast<int64_t>(first + n) * kBlock : held;
             bool holes = false;
-            for (int64_t at = static_cast<int64_t>(first) * kBlock + (static_cast<int64_t>(lane) << p.s.page_log2); at < at1;
-                 at += int64_t{32} << p.s.page_log2)
+            for (int64_t at = at0 + (static_cast<int64_t>(lane) << p.s.page_log2); at < at1; at += int64_t{32} << p.s.page_log2)
                 holes |= kv_page(p.s, un.s, at) < 0;
             holes = __any_sync(0xffffffffu, holes);
             const int64_t place = len - un.rows + (un.row0 + r) / group;
