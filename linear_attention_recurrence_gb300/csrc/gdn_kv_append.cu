@@ -174,7 +174,9 @@ __device__ __forceinline__ Held quantise(const float (&y)[kKvGroup], float err, 
     const uint32_t two = e4m3x2(a + ea, fmaxf(a - ea, 0.f));
     Held h;
     h.scale = two & 0xff;
-    const bool odd = !(a < 1e30f) || !(err < 1e30f);
+    // (a head's scale far from 1: FP32's quotients and their bounds would leave its normal range)
+    const bool far = !(inv_scale > 0x1p-100f && inv_scale < 0x1p100f);
+    const bool odd = far || !(a < 1e30f) || !(err < 1e30f);
     if ((two >> 8) != h.scale || odd) {
         const float least = __uint_as_float(most) - 2 * err;
         uint32_t mask = 0;
@@ -196,8 +198,8 @@ __device__ __forceinline__ Held quantise(const float (&y)[kKvGroup], float err, 
         hi[i / 8] |= e2m1x2(w + ew, u + eu) << (4 * (i & 7));
     }
     h.codes = sc > 0 ? (static_cast<uint64_t>(lo[1]) << 32 | lo[0]) : 0;
-    if ((lo[0] != hi[0] || lo[1] != hi[1]) && sc > 0)
-        h.codes = exact_codes(s, h.codes, static_cast<uint64_t>(lo[1] ^ hi[1]) << 32 | (lo[0] ^ hi[0]), sc, head_scale);
+    const uint64_t open = far ? ~uint64_t{0} : static_cast<uint64_t>(lo[1] ^ hi[1]) << 32 | (lo[0] ^ hi[0]);
+    if (open && sc > 0) h.codes = exact_codes(s, h.codes, open, sc, head_scale);
     return h;
 }
 
