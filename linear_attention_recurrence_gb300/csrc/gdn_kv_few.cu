@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
                 }
             }
             float unscale = 1.f;
-            const float f0 = p.scale * (p.k_scale ? __ldg(p.k_scale + head) : 1.f);
-            if (f0 < 0) {  // the factor of the scores is never below 0, so that it keeps their order
+            const float ks = p.k_scale ? __ldg(p.k_scale + head) : 1.f;
+            if ((p.scale < 0) != (ks < 0)) {  // the factor of the scores is never below 0, so that it keeps their order
 #pragma unroll
                 for (int i = 0; i < DL; ++i) q[i] = -q[i];
             }
@@ -404,8 +404,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
             }
 #pragma unroll
             for (int i = 0; i < DL / 2; ++i) qf[n][i] = pack_f16(q[2 * i], q[2 * i + 1]);
-            // (nor 0, which would make a NaN of a place that is not seen)
-            const float f = fabsf(f0) * unscale < 1e-37f ? 1e-37f : fabsf(f0) * unscale;
+            // (the head's scale last: queries sized against it keep the product in FP32's range)
+            const float f0 = fabsf(p.scale) * unscale * fabsf(ks);
+            const float f = f0 < 1e-37f ? 1e-37f : f0;  // (nor 0, which would make a NaN of a place that is not seen)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 fac[2 * n + k] = __shfl_sync(0xffffffffu, f, 8 * c + 4 * k);
@@ -682,9 +683,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<NT>) kv_few_kernel(con
                 int64_t token;
                 int h;
                 row_of(row0 + r, group, p.n_kv, head, token, h);
-                const float f = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + head) : 1.f) / l;
+                const float f = l == 0.f ? 0.f : 1.f / l, vs = p.v_scale ? __ldg(p.v_scale + head) : 1.f;
 #pragma unroll
-                for (int t = 0; t < D / 8; ++t) v[t] = l == 0.f ? 0.f : v[t] * f;
+                for (int t = 0; t < D / 8; ++t) v[t] = l == 0.f ? 0.f : v[t] * f * vs;
                 T* dst = static_cast<T*>(p.out) + (geo.begin + token) * p.out_stride + h * D + g * (D / 8);
                 if (p.vector) {
 #pragma unroll
@@ -798,10 +799,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) kv_join_kernel(const KvAtt
         int64_t token;
         int h;
         row_of(j.row + r, p.n_heads / p.n_kv, p.n_kv, j.head, token, h);
-        const float f = s.l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + j.head) : 1.f) / s.l;
+        const float f = s.l == 0.f ? 0.f : 1.f / s.l, vs = p.v_scale ? __ldg(p.v_scale + j.head) : 1.f;
         T* dst = static_cast<T*>(p.out) + (j.begin + token) * p.out_stride + h * D + E * lane;
 #pragma unroll
-        for (int i = 0; i < E; ++i) dst[i] = from_f<T>(s.l == 0.f ? 0.f : s.v[i] * f);
+        for (int i = 0; i < E; ++i) dst[i] = from_f<T>(s.l == 0.f ? 0.f : s.v[i] * f * vs);
         if (p.lse && lane == 0)
             p.lse[(j.begin + token) * p.n_heads + h] = s.l == 0.f ? -INFINITY : (s.m - kPShift + log2f(s.l)) * 0.6931471805599453f;
     };
