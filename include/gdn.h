@@ -398,8 +398,10 @@ int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_
  * The paged 4-bit cache of softmax attention layers: gdn_kv_append puts new tokens' keys and
  * values into it, rotated by position, gdn_kv_attention attends over it.  The pages have no
  * counterpart; packed rows, strides, alignment, overlap, streams and graphs are as for the
- * selective state space operators above.  Query head h reads key/value head h % n_kv_heads
- * (a layer whose neighbouring heads share one is reordered with its weights, as above).
+ * selective state space operators above, but that an output may be columns of the same wider
+ * rows as other arguments' columns (of one stride): a joint q, k, v row rotated in place, say.
+ * Query head h reads key/value head h % n_kv_heads (a layer whose neighbouring heads share one
+ * is reordered with its weights, as above).
  *
  * Sequences: sequence s has rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 (cu_seqlens NULL: T / n_seq
  * rows each), the last of the kv_lens[s] tokens in its cache: row i of n has place

@@ -22,19 +22,31 @@ inline int elem_bytes(int dtype) { return dtype == GDN_F32 ? 4 : 2; }
 inline bool known_dtype(int dtype) { return dtype == GDN_F32 || dtype == GDN_BF16 || dtype == GDN_F16; }
 inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// A byte range of an argument; an empty one overlaps nothing.
+// A byte range of an argument; an empty one overlaps nothing.  Rows that lie apart (columns of a
+// wider row, say) may have their distance and width too.
 struct Range {
     const void* p;
     size_t n;
+    size_t stride = 0, width = 0;  // in bytes; 0: not looked at
 };
 inline Range rows_range(const void* p, int64_t rows, int64_t stride, int64_t width, int elem) {
     if (!p || rows <= 0) return {nullptr, 0};
     return {p, static_cast<size_t>((rows - 1) * stride + width) * elem};
 }
+// The same, where other columns of the same wider rows are no overlap.
+inline Range columns_range(const void* p, int64_t rows, int64_t stride, int64_t width, int elem) {
+    Range r = rows_range(p, rows, stride, width, elem);
+    if (r.n && rows > 1) r.stride = static_cast<size_t>(stride) * elem, r.width = static_cast<size_t>(width) * elem;
+    return r;
+}
 inline bool overlaps(const Range& a, const Range& b) {
     if (!a.n || !b.n) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
+    if (a0 >= b0 + b.n || b0 >= a0 + a.n) return false;
+    if (!a.stride || a.stride != b.stride || a.width > a.stride) return true;
+    // rows the same distance apart: b's columns from a's first one on, around the row's end
+    const size_t at = b0 >= a0 ? (b0 - a0) % a.stride : (a.stride - (a0 - b0) % a.stride) % a.stride;
+    return at < a.width || at + b.width > a.stride;
 }
 template <int I, int O>
 bool any_overlap(const Range (&ins)[I], const Range (&outs)[O]) {

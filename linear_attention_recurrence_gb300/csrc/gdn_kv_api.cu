@@ -102,12 +102,12 @@ int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
     p.s.table = block_table;
     p.s.kv_lens = kv_lens;
     const size_t scale4 = static_cast<size_t>(n_kv_heads) * 4;
-    const Range ins[] = {in_place ? Range{nullptr, 0} : rows_range(q, T, q_stride, qw, e), rows_range(k, T, k_stride, kw, e),
-                         rows_range(v, T, v_stride, kw, e), {inv_freq, inv_freq ? static_cast<size_t>(rotary_dim) * 2 : 0},
+    const Range ins[] = {in_place ? Range{nullptr, 0} : columns_range(q, T, q_stride, qw, e), columns_range(k, T, k_stride, kw, e),
+                         columns_range(v, T, v_stride, kw, e), {inv_freq, inv_freq ? static_cast<size_t>(rotary_dim) * 2 : 0},
                          {positions, positions ? static_cast<size_t>(T) * 4 : 0}, {k_scale, k_scale ? scale4 : 0},
                          {v_scale, v_scale ? scale4 : 0}, table_range(p.s), lens_range(p.s), cu_range(p.s)};
-    const Range outs[] = {rows_range(q_out, T, q_out_stride, qw, e), rows_range(k_out, T, k_out_stride, kw, e),
-                          rows_range(v_out, T, v_out_stride, kw, e), {cache, cache_bytes(p.s, n_kv_heads, head_dim)}};
+    const Range outs[] = {columns_range(q_out, T, q_out_stride, qw, e), columns_range(k_out, T, k_out_stride, kw, e),
+                          columns_range(v_out, T, v_out_stride, kw, e), {cache, cache_bytes(p.s, n_kv_heads, head_dim)}};
     if (any_overlap(ins, outs)) return bad("an output overlaps another argument");
     p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_out = k_out, p.v_out = v_out;
     p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
@@ -172,10 +172,10 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     const size_t need = no_device ? 0 : workspace_of(p.s, n_heads, n_kv_heads, head_dim, sms);
     if (need && (!workspace || workspace_bytes < need)) return bad("the workspace is missing or too small");
     const size_t scale4 = static_cast<size_t>(n_kv_heads) * 4;
-    const Range ins[] = {rows_range(q, T, q_stride, qw, e), {cache, cache_bytes(p.s, n_kv_heads, head_dim)},
+    const Range ins[] = {columns_range(q, T, q_stride, qw, e), {cache, cache_bytes(p.s, n_kv_heads, head_dim)},
                          {k_scale, k_scale ? scale4 : 0}, {v_scale, v_scale ? scale4 : 0}, table_range(p.s),
                          lens_range(p.s), cu_range(p.s)};
-    const Range outs[] = {rows_range(out, T, out_stride, qw, e),
+    const Range outs[] = {columns_range(out, T, out_stride, qw, e),
                           {lse, lse ? static_cast<size_t>(T) * n_heads * 4 : 0}, {workspace, workspace ? need : 0}};
     if (any_overlap(ins, outs)) return bad("an output overlaps another argument");
     p.q = q, p.out = out, p.lse = lse, p.q_stride = q_stride, p.out_stride = out_stride;
