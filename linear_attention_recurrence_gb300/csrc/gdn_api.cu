@@ -12,6 +12,7 @@
 #include "gdn.h"
 #include "gdn_internal.h"
 #include "gdn_ssm.h"
+#include "gdn_status.h"
 #include "gdn_device.cuh"
 
 namespace {
@@ -714,14 +715,7 @@ int gdn_device_status(void* cuda_stream) {
     e = gdn::ssm_take_status(dev, &ssm_word);
     if (e != cudaSuccess) return cuda_fail(e, "status read (selective scan, block norm and cache attention)");
     if (word == 0 && na_word == 0 && ssm_word == 0) return GDN_OK;
-    std::string msg = "a kernel gave up a bounded wait (status word " + std::to_string(word | na_word | ssm_word) + ")";
-    if (na_word != 0) msg += " in gdn_recurrence_chunked_noalloc";
-    if (ssm_word & gdn::kDevErrBlockNorm) msg += " in gdn_block_norm";
-    if (ssm_word & gdn::kDevErrKv) msg += " in gdn_kv_attention";
-    if (ssm_word & ~(gdn::kDevErrBlockNorm | gdn::kDevErrKv)) msg += " in gdn_ssm_scan";
-    if (ssm_word & gdn::kDevErrLayout) msg += " (its shared memory does not start where it has to)";
-    if (word & gdn::kDevErrNormTimeout) msg += " (the fused sequential norm's exchange between CTAs)";
-    if (word & gdn::kDevErrRingTimeout) msg += " (a chunk prep's wait for a free slot of the tile ring)";
+    std::string msg = gdn::status_message(word, na_word, ssm_word);
     uint32_t diag[3] = {0, 0, 0};
     if ((word & gdn::kDevErrFlagTimeout) && d && d->sync &&
         cudaMemcpy(diag, d->sync + 2, sizeof(diag), cudaMemcpyDeviceToHost) == cudaSuccess)

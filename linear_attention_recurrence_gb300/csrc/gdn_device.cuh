@@ -7,16 +7,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-namespace gdn {
+#include "gdn_status.h"
 
-// Status word values written by kernels (read by gdn_device_status()).
-constexpr int kDevErrTimeout = 1;      // a wait for an asynchronous copy gave up
-constexpr int kDevErrFlagTimeout = 2;  // a wait for another CTA's flag gave up (chunked prep hand-off)
-constexpr int kDevErrNormTimeout = 4;  // a wait for another CTA's sums of squares gave up (fused sequential norm)
-constexpr int kDevErrRingTimeout = 8;  // a chunk prep's wait for a free slot of the tile ring gave up
-constexpr int kDevErrLayout = 16;      // shared memory did not start where the kernel needs it
-constexpr int kDevErrBlockNorm = 32;   // the block norm's wait for a row's copies gave up
-constexpr int kDevErrKv = 64;          // a wait of the paged cache's attention gave up
+namespace gdn {
 
 // A wait gives up after this many unsuccessful mbarrier.try_wait polls (each
 // poll may itself suspend the thread for a hardware-chosen interval).  Legit
