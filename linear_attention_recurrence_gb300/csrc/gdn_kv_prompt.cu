@@ -179,7 +179,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const KvAttentio
     extern __shared__ __align__(1024) unsigned char kv_prompt_smem[];
     unsigned char* sm = kv_prompt_smem;
     if (smem_addr(sm) % 1024 != 0) {
-        if (threadIdx.x == 0) report_error(p.status, kDevErrKvLayout);
+        if (threadIdx.x == 0) {
+            report_error(p.status, kDevErrKvLayout);
+            // (the joining launch finds no unit, rather than what the workspace held)
+            if (splits > 1 && blockIdx.x % splits == 0) static_cast<Part*>(p.workspace)[blockIdx.x / splits].rows = 0;
+        }
         return;
     }
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + SM::BAR);
