@@ -60,6 +60,7 @@ struct KvAttentionParams {
 // Few / prompt, us: 16 sequences of up to 6000 tokens, 16 KV heads of 128, of 12 rows 53 / 162, of
 // 24 115 / 188, of 48 214 / 159, one sequence of 32768, of 30 rows 63 / 86, of 60 120 / 87.
 constexpr int kKvFewRows = 32;
+// The launches of each count themselves (gdn_launch_count).
 // On the warps' own MMAs, 8 or 16 rows at a time (gdn_kv_few.cu).
 size_t kv_few_workspace(const KvSeqs& q, int n_kv, int head_dim, int sm_count);
 cudaError_t launch_kv_few(const KvAttentionParams& p, int sm_count, cudaStream_t s);

@@ -194,7 +194,6 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     if (err == cudaSuccess && may_have_prompts(T, p.s.per_seq, group, even))
         err = launch_kv_prompt(p, sms, static_cast<cudaStream_t>(cuda_stream));
     if (err != cudaSuccess) return cuda_bad(err, "cache attention launch");
-    internal_count_launch();
     return GDN_OK;
 }
 

@@ -845,7 +845,9 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     const int ctas = sm_count * kCtasPerSm<NT> * kWaves;
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_few_kernel<T, D, NT>), smem); e != cudaSuccess) return e;
     kv_few_kernel<T, D, NT><<<ctas, kWarps * 32, smem, s>>>(p);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || p.whole) return e;
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    internal_count_launch();
+    if (p.whole) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
     // (a row of the grid for each row that a unit may have)
     const int64_t rows = p.s.cu ? 8 * NT : p.s.per_seq * (p.n_heads / p.n_kv);
@@ -857,7 +859,9 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, NT>, p, ctas * kWarps);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D, NT>, p, ctas * kWarps);
+    if (e == cudaSuccess) internal_count_launch();
+    return e;
 }
 
 template <class T, int D>

@@ -626,7 +626,9 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     if (cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kv_prompt_kernel<T, D>), Smem<D>::TOTAL); e != cudaSuccess)
         return e;
     kv_prompt_kernel<T, D><<<static_cast<unsigned>(ctas * splits), kThreads, Smem<D>::TOTAL, s>>>(p, splits, units);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess || splits == 1) return e;
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    internal_count_launch();
+    if (splits == 1) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), kRows / 8);
     cfg.blockDim = dim3(256);
@@ -636,7 +638,9 @@ cudaError_t launch(const KvAttentionParams& p, int sm_count, cudaStream_t s) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<T, D>, p, splits, units);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prompt_join_kernel<T, D>, p, splits, units);
+    if (e == cudaSuccess) internal_count_launch();
+    return e;
 }
 
 }  // namespace
