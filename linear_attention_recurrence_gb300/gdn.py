@@ -637,11 +637,13 @@ def gdn_block_norm(b, residual, w_pre, w_post=None, gate=None, gate_sigmoid: boo
 def gdn_kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device=None):
     """An empty cache of ``n_pages`` pages for gdn_kv_append and gdn_kv_attention:
     [n_pages][n_kv_heads][2][page_size * 9 head_dim / 16] bytes (gdn.h has the layout)."""
-    return torch.zeros((n_pages, n_kv_heads, 2, page_size * 9 * head_dim // 16), dtype=torch.uint8,
-                       device=torch.device("cuda") if device is None else device)
+    cache = torch.zeros((n_pages, n_kv_heads, 2, page_size * 9 * head_dim // 16), dtype=torch.uint8,
+                        device=torch.device("cuda") if device is None else device)
+    cache.gdn_head_dim = head_dim  # (the bytes alone do not tell 32 tokens of 64 from 16 of 128)
+    return cache
 
 
-def _paged(cache, block_table, kv_lens, cu_seqlens, T, n_kv, D, index):
+def _paged(cache, block_table, kv_lens, cu_seqlens, T, n_kv, D, page_size, index):
     """The arguments that say where a call's tokens lie: (cache, n_pages, page_size, table, table_stride,
     max_pages, kv_lens, cu, n_seq)."""
     i32 = torch.int32
@@ -653,6 +655,10 @@ def _paged(cache, block_table, kv_lens, cu_seqlens, T, n_kv, D, index):
     page = plane * 16 // (9 * D) if D else 0
     if page * 9 * D // 16 != plane or page <= 0:
         raise ValueError(f"the cache's pages of {plane} bytes a head do not hold tokens of head_dim {D}")
+    if getattr(cache, "gdn_head_dim", D) != D:
+        raise ValueError(f"the cache was made for head_dim {cache.gdn_head_dim}, not {D}")
+    if page_size is not None and page_size != page:
+        raise ValueError(f"the cache's pages of {plane} bytes a head hold {page} tokens of head_dim {D}, not page_size {page_size}")
     cp = _dense(cache, "cache", (pages, n_kv, 2, plane), torch.uint8, index)
     tp, ts = _rows(block_table, "block_table", (n, block_table.shape[1]), i32, index)
     if n <= 1:
@@ -664,7 +670,8 @@ def _paged(cache, block_table, kv_lens, cu_seqlens, T, n_kv, D, index):
 
 
 def gdn_kv_append(k, v, cache, block_table, kv_lens, q=None, inv_freq=None, interleaved: bool = False, positions=None,
-                  k_scale=None, v_scale=None, cu_seqlens=None, q_out=None, k_out=None, v_out=None, stream=None):
+                  k_scale=None, v_scale=None, cu_seqlens=None, q_out=None, k_out=None, v_out=None, stream=None,
+                  page_size=None):
     """Appends keys and values to the pages of their sequences in 4 bits, the keys (and the
     queries) rotated by position; updates ``cache`` in place and returns the rotated queries
     (None without ``q``).
@@ -676,14 +683,16 @@ def gdn_kv_append(k, v, cache, block_table, kv_lens, q=None, inv_freq=None, inte
     inv_freq: [rotary_dim / 2] FP32 (None: no rotation), positions: [T] int32 (None: a token's
     place in its cache); interleaved: pairs (2 i, 2 i + 1) rather than (i, i + rotary_dim / 2).
     k_scale, v_scale: [n_kv_heads] FP32 or None.  ``q_out`` is allocated if None (it may be ``q``);
-    ``k_out`` and ``v_out``, where given, receive what the cache holds of k and v.
+    ``k_out`` and ``v_out``, where given, receive what the cache holds of k and v.  page_size: the
+    cache's, checked where given (what gdn_kv_cache returned is known; the bytes of a view or of a
+    buffer of the caller's do not tell 32 tokens of 64 from 16 of 128).
     """
     dt, dev = _activations(k, "k", 3)
     ty, f32 = k.dtype, torch.float32
     T, G, D = shape = k.shape
     kp, ks = _rows(k, "k", shape, ty, dev)
     vp_, vs = _rows(v, "v", shape, ty, dev)
-    where = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, dev)
+    where = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, page_size, dev)
     rotary = 0
     if inv_freq is not None:
         _dims(inv_freq, "inv_freq", 1)
@@ -713,13 +722,13 @@ def gdn_kv_append(k, v, cache, block_table, kv_lens, q=None, inv_freq=None, inte
 
 
 def gdn_kv_attention(q, cache, block_table, kv_lens, k_scale=None, v_scale=None, scale=None, causal: bool = True,
-                     window: int = 0, cu_seqlens=None, out=None, lse=None, stream=None):
+                     window: int = 0, cu_seqlens=None, out=None, lse=None, stream=None, page_size=None):
     """Softmax attention of new tokens over their sequences' pages (gdn_kv_append's, theirs
     included); returns ``out``.
 
     q: [T][n_heads][head_dim], BF16 or FP16, the rows any distance apart; head h reads key/value
     head h % n_kv_heads.  cache, block_table, kv_lens, cu_seqlens, k_scale, v_scale as in
-    gdn_kv_append.  scale: of the scores (None: head_dim ** -0.5); causal: a token sees its own
+    gdn_kv_append, page_size too.  scale: of the scores (None: head_dim ** -0.5); causal: a token sees its own
     place and those before it, with a ``window`` only the last so many.  ``out`` (as q) is
     allocated if None; ``lse`` ([T][n_heads] FP32), where given, receives the logarithm of each
     row's sum.  Rows of no sequence are left as they were; a row that sees nothing gets zeros.
@@ -730,7 +739,7 @@ def gdn_kv_attention(q, cache, block_table, kv_lens, k_scale=None, v_scale=None,
     T, H, D = shape = q.shape
     G = cache.shape[1]
     qp, qs = _rows(q, "q", shape, ty, dev)
-    cp, pages, page, tp, ts, width, lp, cu, n = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, dev)
+    cp, pages, page, tp, ts, width, lp, cu, n = _paged(cache, block_table, kv_lens, cu_seqlens, T, G, D, page_size, dev)
     ksp, vsp = _dense(k_scale, "k_scale", (G,), f32, dev), _dense(v_scale, "v_scale", (G,), f32, dev)
     if out is None:
         out = _empty(shape, ty, dev, stream)
