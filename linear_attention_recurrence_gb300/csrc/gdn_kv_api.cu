@@ -154,7 +154,8 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     if (causal != 0 && causal != 1) return bad("causal must be 0 or 1");
     if (window < 0) return bad("window < 0");
     if (window > 0 && !causal) return bad("a window goes with causal");
-    if (!std::isfinite(scale)) return bad("scale must be finite");
+    const float scale2 = scale * 1.4426950408889634f;  // (exponentials are of base 2)
+    if (!std::isfinite(scale2)) return bad("scale must be finite, times log2 e too");
     const int64_t qw = static_cast<int64_t>(n_heads) * head_dim;
     if (q_stride < 0 || q_stride > kMaxStride || out_stride > kMaxStride) return bad("a row stride is out of range");
     if (out_stride < qw) return bad("out's row stride is below its row");
@@ -180,7 +181,7 @@ int gdn_kv_attention(const void* q, int64_t q_stride, const void* cache, int64_t
     if (any_overlap(ins, outs)) return bad("an output overlaps another argument");
     p.q = q, p.out = out, p.lse = lse, p.q_stride = q_stride, p.out_stride = out_stride;
     p.k_scale = k_scale, p.v_scale = v_scale, p.cache = static_cast<const uint8_t*>(cache);
-    p.scale = scale * 1.4426950408889634f;
+    p.scale = scale2;
     p.n_heads = n_heads, p.n_kv = n_kv_heads, p.head_dim = head_dim, p.causal = causal, p.window = window, p.dtype = dtype;
     p.vector = rows16(q, q_stride, e) && rows16(out, out_stride, e);
     if (kv_prompt_ctas(T, n_seq, n_heads, n_kv_heads) > INT32_MAX / 2) return unsupported("too many rows and heads");
