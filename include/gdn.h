@@ -425,13 +425,14 @@ int gdn_block_norm(const void* b, int64_t b_stride, const void* residual, int64_
  *     angle = position * inv_freq[i];  a' = a cos - b sin;  b' = b cos + a sin
  * position: positions[t], or NULL: the row's place.  Of 16 elements y of a key or value
  *     scale = e4m3(max|y| / (6 k_scale));  code = e2m1(y / (scale k_scale))
- * rounded to nearest, ties to even, and held at the largest finite number; the quotients are
- * those of exact arithmetic, so the codes do not depend on how a row was computed.  An infinity
- * counts as the largest, a NaN makes its scale a NaN.
+ * rounded to nearest, ties to even, and held at the largest finite number; a scale of 0 has codes
+ * of 0.  The quotients are those of exact arithmetic (the angles to 2^-64 of a turn a position),
+ * so the codes do not depend on how a row was computed.  An infinity counts as the largest, a
+ * NaN makes its scale a NaN.
  *   q, q_out [T][n_heads][head_dim] (both or neither; q_out may be q), k, v [T][n_kv_heads]
  *   [head_dim], k_out, v_out (each may be NULL) the same: of `dtype`.  k_out and v_out receive
- *   the keys and values as the cache holds them.  inv_freq [rotary_dim / 2], k_scale, v_scale
- *   [n_kv_heads] (or NULL; positive): FP32.
+ *   the keys and values as the cache holds them.  inv_freq [rotary_dim / 2] (finite, below
+ *   2^40), k_scale, v_scale [n_kv_heads] (or NULL; positive, finite): FP32.
  * Rows of no sequence are left as they were.  A token's place belongs to one row of a call.
  */
 int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -446,7 +447,8 @@ int gdn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
  * gdn_kv_attention - softmax attention of every row over its sequence's cache:
  *     out[t][h] = sum_j p_j V_j,  p = softmax over the j it sees of scale * q[t][h] . K_j
  * A row at place i sees the places j < kv_lens with j <= i where causal is 1, and j > i - window
- * where window is not 0 (which goes with causal).  A row that sees nothing gets zeros.
+ * where window is not 0 (which goes with causal).  A row that sees nothing gets zeros.  `scale` is
+ * finite, times log2 e too.
  *   q, out [T][n_heads][head_dim]: GDN_BF16 or GDN_F16.  lse [T][n_heads] FP32 or NULL: the
  *   logarithm of the softmax's sum (-infinity for a row that sees nothing), with which results
  *   over several caches can be joined.
